@@ -11,6 +11,13 @@ The entry points mirror include/ttt.h:
     branch concatenated and projected);
   * ttt_forward_fullbatch_noalloc (full-batch with the library's static scratch instead of a
     workspace, for callers that cannot allocate) and ttt_workspace_size.
+
+Those of include/ttt_seq.h, the operators of a block around and beside a TTT layer, each with its
+backward pass (seq.py):
+  * ttt_forward_layernorm, ttt_backward_layernorm (over a row or per head);
+  * ttt_forward_conv1d, ttt_step_conv1d, ttt_backward_conv1d (short causal depth-wise convolution);
+  * ttt_forward_selective_scan, ttt_step_selective_scan, ttt_backward_selective_scan (selective state
+    space scan); the step forms take one token of every sequence and update its state.
 """
 from .ttt import (  # noqa: F401
     TTT_BF16, TTT_F32, TTT_NOALLOC_SCRATCH_BYTES, TTT_OP_BIDIR, TTT_OP_CAUSAL, TTT_OP_FULLBATCH,
@@ -18,3 +25,6 @@ from .ttt import (  # noqa: F401
     TTTError, load_library, status_string, ttt_backward_chunked_bidir, ttt_backward_chunked_causal,
     ttt_backward_fullbatch, ttt_block_epilogue, ttt_forward_chunked_bidir, ttt_forward_chunked_bidir2d, ttt_forward_chunked_causal,
     ttt_dwconv3x3, ttt_forward_fullbatch, ttt_forward_fullbatch_epochs, ttt_forward_fullbatch_noalloc, ttt_mlp_forward, ttt_workspace_size)
+from .seq import (  # noqa: F401
+    ttt_backward_conv1d, ttt_backward_layernorm, ttt_backward_selective_scan, ttt_forward_conv1d, ttt_forward_layernorm,
+    ttt_forward_selective_scan, ttt_step_conv1d, ttt_step_selective_scan)

@@ -1,0 +1,285 @@
+// Short causal depth-wise convolution over the tokens of [B, N, C], forward, backward and one token at a
+// time: K = 2..4 taps per channel over the token and the K - 1 before it, then optionally SiLU.
+//   pre[n] = bias + sum_k w[k] x[n - (K - 1) + k],   y = pre or pre sigmoid(pre)
+//   dpre = dy act'(pre),  dx[n] = sum_k w[k] dpre[n + K - 1 - k],  dw[k] = sum dpre[n] x[n - (K - 1) + k]
+//
+// A stream bound by HBM. A thread owns 16 bytes of channels (one channel where rows are not 16-byte
+// aligned) and walks down a run of tokens with the last K inputs in registers, so that every
+// input is read once but for the K - 1 tokens before each run (from L2). The backward pass walks the
+// same way with the last K values of dpre beside the inputs: dx lags K - 1 tokens behind. dw and db
+// stay in registers over a run, are joined in LDS over the runs of a workgroup, and a second launch
+// sums the workgroups' partial rows in a fixed order.
+#include "internal.hpp"
+#include "rowops.hpp"
+#include "seq.hpp"
+
+namespace ttt {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kRun = 16;      // tokens per thread
+constexpr int kPieces = 32;   // backward: pieces of a row per workgroup
+constexpr int kRuns = kThreads / kPieces;  // backward: runs per workgroup
+
+template <bool SILU>
+__device__ __forceinline__ float act(float pre) {
+  return SILU ? pre * sigmoid(pre) : pre;
+}
+
+// Input token t (t < n) of a sequence: the state's rows before token 0, zeros without a state.
+template <class T, int V, int K>
+__device__ __forceinline__ void input(const T* x, long long xs, const T* state, int C, int t, float* out) {
+  if (t >= 0) {
+    load_row<T, V>(x + (long long)t * xs, out);
+  } else if (state) {
+    load_row<T, V>(state + (long long)(K - 1 + t) * C, out);
+  } else {
+    for (int i = 0; i < V; ++i) out[i] = 0.f;
+  }
+}
+
+__device__ __forceinline__ int length_of(const int* lengths, int b, int N) {
+  return lengths ? min(max(lengths[b], 0), N) : N;
+}
+
+template <int V, int K>
+__device__ __forceinline__ void load_taps(const float* w, const float* bias, int c0, float (*wt)[V], float* bs) {
+  for (int i = 0; i < V; ++i) {
+    for (int k = 0; k < K; ++k) wt[k][i] = w[(long long)(c0 + i) * K + k];
+    bs[i] = bias ? bias[c0 + i] : 0.f;
+  }
+}
+
+template <class T, int V, int K, bool SILU>
+__global__ __launch_bounds__(kThreads) void conv1d_fwd(Conv1dArgs a, int pieces, int runs) {
+  const long long id = ((long long)blockIdx.z * gridDim.x + blockIdx.x) * kThreads + threadIdx.x;
+  if (id >= (long long)pieces * runs) return;
+  const int run = (int)(id / pieces), piece = (int)(id - (long long)run * pieces);
+  const int b = blockIdx.y, C = a.C, c0 = piece * V;
+  const int n = length_of(a.lengths, b, a.N);
+  const T* x = (const T*)a.x + (long long)b * a.N * a.xs + c0;
+  const T* state = a.state ? (const T*)a.state + (long long)b * (K - 1) * C + c0 : nullptr;
+  T* y = (T*)a.y + (long long)b * a.N * C + c0;
+  if (run == 0 && a.state_out) {
+    T* so = (T*)a.state_out + (long long)b * (K - 1) * C + c0;
+    for (int j = 0; j < K - 1; ++j) {
+      float v[V];
+      input<T, V, K>(x, a.xs, state, C, n - (K - 1) + j, v);
+      store_row<T, V>(so + (long long)j * C, v);
+    }
+  }
+  float wt[K][V], bs[V], win[K][V];
+  load_taps<V, K>(a.w, a.bias, c0, wt, bs);
+  const int t0 = run * kRun, t1 = min(a.N, t0 + kRun), te = min(t1, n);
+  if (t0 < te)
+    for (int k = 0; k < K - 1; ++k) input<T, V, K>(x, a.xs, state, C, t0 - (K - 1) + k, win[k]);
+#pragma unroll 4
+  for (int t = t0; t < te; ++t) {
+    load_row<T, V>(x + (long long)t * a.xs, win[K - 1]);
+    float o[V];
+    for (int i = 0; i < V; ++i) {
+      float s = bs[i];
+      for (int k = 0; k < K; ++k) s = fmaf(wt[k][i], win[k][i], s);
+      o[i] = act<SILU>(s);
+      for (int k = 0; k < K - 1; ++k) win[k][i] = win[k + 1][i];
+    }
+    store_row<T, V>(y + (long long)t * C, o);
+  }
+  for (int t = max(t0, te); t < t1; ++t) {
+    float o[V] = {};
+    store_row<T, V>(y + (long long)t * C, o);
+  }
+}
+
+template <class T, int V, int K, bool SILU>
+__global__ __launch_bounds__(kThreads) void conv1d_step(Conv1dArgs a, int pieces) {
+  const long long id = wide_block() * kThreads + threadIdx.x;
+  if (id >= (long long)pieces * a.B) return;
+  const int b = (int)(id / pieces), c0 = (int)(id - (long long)b * pieces) * V, C = a.C;
+  const T* st = (const T*)a.state + (long long)b * (K - 1) * C + c0;
+  T* so = (T*)a.state_out + (long long)b * (K - 1) * C + c0;
+  float wt[K][V], bs[V], win[K][V];
+  for (int k = 0; k < K - 1; ++k) load_row<T, V>(st + (long long)k * C, win[k]);
+  load_row<T, V>((const T*)a.x + (long long)b * a.xs + c0, win[K - 1]);
+  load_taps<V, K>(a.w, a.bias, c0, wt, bs);
+  float o[V];
+  for (int i = 0; i < V; ++i) {
+    float s = bs[i];
+    for (int k = 0; k < K; ++k) s = fmaf(wt[k][i], win[k][i], s);
+    o[i] = act<SILU>(s);
+  }
+  for (int k = 0; k < K - 1; ++k) store_row<T, V>(so + (long long)k * C, win[k + 1]);
+  store_row<T, V>((T*)a.y + (long long)b * C + c0, o);
+}
+
+// Workgroup: kPieces pieces of the row x kRuns runs of one sequence. Partial row (b, run group):
+// [K + 1][C], the K sums of dw and that of db.
+template <class T, int V, int K, bool SILU>
+__global__ __launch_bounds__(kThreads) void conv1d_bwd(Conv1dArgs a, int pieces) {
+  __shared__ float join[kRuns][kPieces * V];
+  const int piece = blockIdx.x * kPieces + threadIdx.x % kPieces, sub = threadIdx.x / kPieces;
+  const int b = blockIdx.z, C = a.C, c0 = piece * V;
+  const bool live = piece < pieces;
+  float acc[K + 1][V] = {};
+  if (live) {
+    const int n = length_of(a.lengths, b, a.N);
+    const T* x = (const T*)a.x + (long long)b * a.N * a.xs + c0;
+    const T* state = a.state ? (const T*)a.state + (long long)b * (K - 1) * C + c0 : nullptr;
+    const T* dy = (const T*)a.dy + (long long)b * a.N * C + c0;
+    T* dx = (T*)a.dx + (long long)b * a.N * C + c0;
+    float wt[K][V], bs[V], win[K][V], dp[K][V] = {};
+    load_taps<V, K>(a.w, a.bias, c0, wt, bs);
+    const long long first = ((long long)blockIdx.y * kRuns + sub) * kRun;
+    if (first < a.N) {
+      const int t0 = (int)first, t1 = min(a.N, t0 + kRun);
+      // Tokens behind the sequence have no dpre; dx[t] needs dpre up to t + K - 1.
+      for (int k = 0; k < K - 1; ++k) {
+        const int t = t0 - (K - 1) + k;
+        if (t < n) input<T, V, K>(x, a.xs, state, C, t, win[k]);
+        else for (int i = 0; i < V; ++i) win[k][i] = 0.f;
+      }
+#pragma unroll 4
+      for (int t = t0; t < t1 + K - 1; ++t) {
+        float d[V] = {};
+        if (t < n) {
+          load_row<T, V>(x + (long long)t * a.xs, win[K - 1]);
+          load_row<T, V>(dy + (long long)t * C, d);
+          for (int i = 0; i < V; ++i) {
+            if (SILU) {
+              float pre = bs[i];
+              for (int k = 0; k < K; ++k) pre = fmaf(wt[k][i], win[k][i], pre);
+              const float s = sigmoid(pre);
+              d[i] *= s * fmaf(pre, 1.f - s, 1.f);
+            }
+            if (t < t1) {
+              acc[K][i] += d[i];
+              for (int k = 0; k < K; ++k) acc[k][i] = fmaf(d[i], win[k][i], acc[k][i]);
+            }
+            for (int k = 0; k < K - 1; ++k) win[k][i] = win[k + 1][i];
+          }
+        }
+        // dp[k] = dpre[t - (K - 1) + k]; dx[t - (K - 1)] = sum_k w[K - 1 - k] dp[k]
+        float o[V];
+        for (int i = 0; i < V; ++i) {
+          for (int k = 0; k < K - 1; ++k) dp[k][i] = dp[k + 1][i];
+          dp[K - 1][i] = d[i];
+          o[i] = 0.f;
+          for (int k = 0; k < K; ++k) o[i] = fmaf(wt[K - 1 - k][i], dp[k][i], o[i]);
+        }
+        const int td = t - (K - 1);
+        if (td >= t0) store_row<T, V>(dx + (long long)td * C, o);
+        else if (td < 0 && a.dstate) store_row<T, V>((T*)a.dstate + ((long long)b * (K - 1) + t) * C + c0, o);
+      }
+    }
+  }
+  float* row = a.partial + ((long long)b * gridDim.y + blockIdx.y) * (K + 1) * C;
+#pragma unroll
+  for (int k = 0; k <= K; ++k) {
+    __syncthreads();
+    for (int i = 0; i < V; ++i) join[sub][(threadIdx.x % kPieces) * V + i] = acc[k][i];
+    __syncthreads();
+    for (int t = threadIdx.x; t < kPieces * V; t += kThreads) {
+      const int c = blockIdx.x * kPieces * V + t;
+      if (c >= C) break;
+      float s = 0.f;
+      for (int q = 0; q < kRuns; ++q) s += join[q][t];
+      row[(long long)k * C + c] = s;
+    }
+  }
+}
+
+template <int K>
+struct StoreConvGrads {
+  float *dw, *db;
+  int C;
+  __device__ void operator()(int col, float s) const {
+    const int k = col / C, c = col - k * C;
+    if (k < K) dw[(long long)c * K + k] = s;
+    else if (db) db[c] = s;
+  }
+};
+
+bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+bool vector_rows(bool bf, const Conv1dArgs& a) {
+  const int V = bf ? 8 : 4;
+  return a.C % V == 0 && a.xs % V == 0 && aligned16(a.x) && aligned16(a.state) && aligned16(a.y) &&
+         aligned16(a.state_out) && aligned16(a.dy) && aligned16(a.dx) && aligned16(a.dstate);
+}
+
+int run_groups(int N) { return (int)(((long long)N + kRun * kRuns - 1) / (kRun * kRuns)); }
+
+// Calls f.run<T, V, K, SILU>().
+template <class F>
+hipError_t with_variant(bool bf, bool vec, int K, bool silu, const F& f) {
+#define TTT_CONV(T, v, k) \
+  if (K == k) return silu ? f.template run<T, v, k, true>() : f.template run<T, v, k, false>();
+  if (bf) {
+    if (vec) { TTT_CONV(bf16, 8, 2) TTT_CONV(bf16, 8, 3) TTT_CONV(bf16, 8, 4) }
+    else { TTT_CONV(bf16, 1, 2) TTT_CONV(bf16, 1, 3) TTT_CONV(bf16, 1, 4) }
+  } else {
+    if (vec) { TTT_CONV(float, 4, 2) TTT_CONV(float, 4, 3) TTT_CONV(float, 4, 4) }
+    else { TTT_CONV(float, 1, 2) TTT_CONV(float, 1, 3) TTT_CONV(float, 1, 4) }
+  }
+#undef TTT_CONV
+  return hipErrorInvalidValue;
+}
+
+struct FwdCall {
+  const Conv1dArgs& a;
+  hipStream_t st;
+  template <class T, int V, int K, bool SILU>
+  hipError_t run() const {
+    const int pieces = a.C / V, runs = (a.N + kRun - 1) / kRun;
+    const long long blocks = ((long long)pieces * runs + kThreads - 1) / kThreads;
+    const dim3 g = wide_grid(blocks);
+    hipLaunchKernelGGL((conv1d_fwd<T, V, K, SILU>), dim3(g.x, (unsigned)a.B, g.y), dim3(kThreads), 0, st, a, pieces,
+                       runs);
+    return hipGetLastError();
+  }
+};
+
+struct StepCall {
+  const Conv1dArgs& a;
+  hipStream_t st;
+  template <class T, int V, int K, bool SILU>
+  hipError_t run() const {
+    const int pieces = a.C / V;
+    const long long blocks = ((long long)pieces * a.B + kThreads - 1) / kThreads;
+    hipLaunchKernelGGL((conv1d_step<T, V, K, SILU>), wide_grid(blocks), dim3(kThreads), 0, st, a, pieces);
+    return hipGetLastError();
+  }
+};
+
+struct BwdCall {
+  const Conv1dArgs& a;
+  hipStream_t st;
+  template <class T, int V, int K, bool SILU>
+  hipError_t run() const {
+    const int pieces = a.C / V, groups = run_groups(a.N);
+    const dim3 grid((unsigned)((pieces + kPieces - 1) / kPieces), (unsigned)groups, (unsigned)a.B);
+    hipLaunchKernelGGL((conv1d_bwd<T, V, K, SILU>), grid, dim3(kThreads), 0, st, a, pieces);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    return column_sum_launch(a.partial, (long long)a.B * groups, (K + 1) * a.C, StoreConvGrads<K>{a.dw, a.db, a.C}, st);
+  }
+};
+
+}  // namespace
+
+hipError_t conv1d_launch(bool bf16_io, int K, bool silu, const Conv1dArgs& a, hipStream_t st) {
+  return with_variant(bf16_io, vector_rows(bf16_io, a), K, silu, FwdCall{a, st});
+}
+
+hipError_t conv1d_step_launch(bool bf16_io, int K, bool silu, const Conv1dArgs& a, hipStream_t st) {
+  return with_variant(bf16_io, vector_rows(bf16_io, a), K, silu, StepCall{a, st});
+}
+
+size_t conv1d_bwd_workspace_bytes(bool, int B, int N, int C, int K) {
+  return (size_t)B * run_groups(N) * (K + 1) * C * sizeof(float);
+}
+
+hipError_t conv1d_bwd_launch(bool bf16_io, int K, bool silu, const Conv1dArgs& a, hipStream_t st) {
+  return with_variant(bf16_io, vector_rows(bf16_io, a), K, silu, BwdCall{a, st});
+}
+
+}  // namespace ttt

@@ -1,0 +1,319 @@
+// Layer norm over each head's D channels, forward and backward: a block is Norm -> layer -> residual
+// (ViT^3 review on techloop.online, "TTT Block" section).
+//   y = xhat w + b,  xhat = (x - mean) rstd,  rstd = 1 / sqrt(mean((x - mean)^2) + eps)
+//   dx = rstd (g - mean(g) - xhat mean(g xhat)),  g = dy w;   dw = sum dy xhat,   db = sum dy.
+//
+// A stream of rows, bound by HBM: each row is read once into registers by a group of L lanes (8 lanes
+// for a head of 64 bf16 channels, a wave, or a workgroup of 256 threads for wide rows), the
+// statistics are taken there in two passes over the registers (the mean, then the centred squares:
+// no cancellation), and the result is written from them. The backward pass recomputes the
+// statistics, since it has to read x anyway; each group keeps the same channels over the rows it
+// walks, so that dw and db stay in registers until its last row; a workgroup's groups are joined in
+// LDS, and a second launch sums the workgroups' partial rows in a fixed order.
+#include "internal.hpp"
+#include "rowops.hpp"
+#include "seq.hpp"
+
+namespace ttt {
+namespace {
+
+constexpr int kThreads = 256;
+
+// Sum over a row's L lanes; for L = 256 (the whole workgroup) over the four waves through LDS, `slot`
+// alternating between consecutive sums so that one barrier each is enough.
+template <int L>
+__device__ __forceinline__ float row_sum(float v, float (*red)[4], int slot) {
+  if constexpr (L <= 64) {
+    return lanes_sum<L>(v);
+  } else {
+    v = lanes_sum<64>(v);
+    if ((threadIdx.x & 63) == 0) red[slot][threadIdx.x >> 6] = v;
+    __syncthreads();
+    return (red[slot][0] + red[slot][1]) + (red[slot][2] + red[slot][3]);
+  }
+}
+
+// One row into registers: element (k L + lane) V + i of the row is v[k V + i], zero past D.
+template <class T, int L, int K, int V>
+__device__ __forceinline__ void read_row(const T* p, int lane, int D, float* v) {
+#pragma unroll
+  for (int k = 0; k < K; ++k) {
+    const int at = (k * L + lane) * V;
+    if (at < D) {
+      load_row<T, V>(p + at, v + k * V);
+    } else {
+      for (int i = 0; i < V; ++i) v[k * V + i] = 0.f;
+    }
+  }
+}
+
+// v -> v - mean (zero past D); returns rstd.
+template <int L, int K, int V>
+__device__ __forceinline__ float centre(float* v, int lane, int D, float eps, float (*red)[4], int slot) {
+  float s = 0.f;
+#pragma unroll
+  for (int j = 0; j < K * V; ++j) s += v[j];
+  // (divided, not multiplied by 1 / D: a constant row has to have its value as its mean)
+  const float mean = row_sum<L>(s, red, slot) / (float)D;
+  float q = 0.f;
+#pragma unroll
+  for (int k = 0; k < K; ++k)
+    for (int i = 0; i < V; ++i) {
+      float& x = v[k * V + i];
+      x = (k * L + lane) * V < D ? x - mean : 0.f;
+      q = fmaf(x, x, q);
+    }
+  return 1.f / sqrtf(row_sum<L>(q, red, slot + 1) / (float)D + eps);
+}
+
+template <class T, int L, int K, int V>
+__global__ __launch_bounds__(kThreads) void layernorm_fwd(const T* __restrict__ x, long long xs,
+                                                          const float* __restrict__ w,
+                                                          const float* __restrict__ b, T* __restrict__ y,
+                                                          int rows, int H, int D, float eps) {
+  __shared__ float red[2][4];
+  const int lane = threadIdx.x % L;
+  const long long row = wide_block() * (kThreads / L) + threadIdx.x / L;
+  if (row >= rows) return;  // (whole groups; for L = 256 the whole workgroup)
+  const int m = (int)(row / H), h = (int)(row - (long long)m * H);
+  float v[K * V];
+  read_row<T, L, K, V>(x + (long long)m * xs + (long long)h * D, lane, D, v);
+  const float rstd = centre<L, K, V>(v, lane, D, eps, red, 0);
+  T* py = y + row * D;
+#pragma unroll
+  for (int k = 0; k < K; ++k) {
+    const int at = (k * L + lane) * V;
+    if (at < D) {
+      float wv[V], bv[V] = {};
+      load_params<V>(w + (long long)h * D + at, wv);
+      if (b) load_params<V>(b + (long long)h * D + at, bv);
+      for (int i = 0; i < V; ++i) wv[i] = fmaf(v[k * V + i] * rstd, wv[i], bv[i]);
+      store_row<T, V>(py + at, wv);
+    }
+  }
+}
+
+// Workgroup (bx, by): R tokens at a time of the HB heads from by HB on, tokens bx R + r, + gridDim.x R, ...
+// Group g of L lanes has token r = g / HB and head g % HB. Partial row bx: [dw (H D), db (H D)].
+template <class T, int L, int K, int V>
+__global__ __launch_bounds__(kThreads) void layernorm_bwd(const T* __restrict__ x, long long xs,
+                                                          const float* __restrict__ w,
+                                                          const T* __restrict__ dy, T* __restrict__ dx,
+                                                          float* __restrict__ part, int M, int H, int D,
+                                                          int HB, int R, float eps) {
+  constexpr int LKV = L * K * V;
+  __shared__ float red[4][4];
+  __shared__ float join[L <= 64 ? kThreads * K * V : 1];
+  const int lane = threadIdx.x % L, g = threadIdx.x / L;
+  const int r = g / HB, h = blockIdx.y * HB + g % HB;
+  const bool live = r < R && h < H;
+  float wv[K * V], aw[K * V], ab[K * V];
+#pragma unroll
+  for (int k = 0; k < K; ++k) {
+    const int at = (k * L + lane) * V;
+    for (int i = 0; i < V; ++i) wv[k * V + i] = aw[k * V + i] = ab[k * V + i] = 0.f;
+    if (live && at < D) load_params<V>(w + (long long)h * D + at, wv + k * V);
+  }
+  // (M is an int: the token counter stays below 2^31 + 2^31)
+  for (long long m = (long long)blockIdx.x * R + r; live && m < M; m += (long long)gridDim.x * R) {
+    const long long at0 = (m * H + h) * D;
+    float v[K * V], d[K * V];
+    read_row<T, L, K, V>(x + m * xs + (long long)h * D, lane, D, v);
+    read_row<T, L, K, V>(dy + at0, lane, D, d);
+    const float rstd = centre<L, K, V>(v, lane, D, eps, red, 0);
+    float s1 = 0.f, s2 = 0.f;
+#pragma unroll
+    for (int j = 0; j < K * V; ++j) {
+      v[j] *= rstd;  // xhat
+      ab[j] += d[j];
+      aw[j] = fmaf(d[j], v[j], aw[j]);
+      d[j] *= wv[j];  // g
+      s1 += d[j];
+      s2 = fmaf(d[j], v[j], s2);
+    }
+    s1 = row_sum<L>(s1, red, 2) / (float)D;
+    s2 = row_sum<L>(s2, red, 3) / (float)D;
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      const int at = (k * L + lane) * V;
+      if (at < D) {
+        float o[V];
+        for (int i = 0; i < V; ++i) o[i] = rstd * (d[k * V + i] - s1 - v[k * V + i] * s2);
+        store_row<T, V>(dx + at0 + at, o);
+      }
+    }
+  }
+  const long long W = (long long)H * D;
+  float* row = part + (long long)blockIdx.x * 2 * W;
+  if constexpr (L > 64) {  // one group: its registers are the workgroup's sums
+#pragma unroll
+    for (int k = 0; k < K; ++k)
+      for (int i = 0; i < V; ++i) {
+        const int at = (k * L + lane) * V + i;
+        if (at < D) {
+          row[(long long)h * D + at] = aw[k * V + i];
+          row[W + (long long)h * D + at] = ab[k * V + i];
+        }
+      }
+  } else {
+    for (int which = 0; which < 2; ++which) {
+      __syncthreads();
+#pragma unroll
+      for (int k = 0; k < K; ++k)
+        for (int i = 0; i < V; ++i) join[g * LKV + (k * L + lane) * V + i] = which ? ab[k * V + i] : aw[k * V + i];
+      __syncthreads();
+      for (int t = threadIdx.x; t < HB * D; t += blockDim.x) {
+        const int hh = t / D, at = t - hh * D;
+        if (blockIdx.y * HB + hh >= H) break;
+        float s = 0.f;
+        for (int q = 0; q < R; ++q) s += join[(q * HB + hh) * LKV + at];
+        row[which * W + (long long)(blockIdx.y * HB + hh) * D + at] = s;
+      }
+    }
+  }
+}
+
+struct StoreNormGrads {
+  float *dw, *db;
+  int W;
+  __device__ void operator()(int col, float s) const {
+    if (col < W) dw[col] = s;
+    else if (db) db[col - W] = s;
+  }
+};
+
+// How a row of D channels is spread over lanes: L lanes, K accesses of V elements each.
+struct Shape {
+  int L, K, V;
+};
+Shape shape_of(bool bf, bool vec, int D) {
+  const int V = vec ? (bf ? 8 : 4) : 1;
+  const int n = (D + V - 1) / V;  // accesses
+  if (!vec) {
+    if (n <= 64) return {64, 1, 1};
+    if (n <= 256) return {64, 4, 1};
+    if (n <= 1024) return {64, 16, 1};
+    return n <= 4096 ? Shape{256, 16, 1} : Shape{256, 64, 1};
+  }
+  for (int L = 8; L <= 64; L *= 2)
+    if (n <= L) return {L, 1, V};
+  if (n <= 128) return {64, 2, V};
+  if (n <= 256) return {64, 4, V};
+  for (int K = 2;; K *= 2)
+    if (n <= 256 * K) return {256, K, V};
+}
+
+// Calls f.run<T, L, K, V>() for the shape; every shape shape_of returns is listed.
+template <class F>
+hipError_t with_shape(bool bf, Shape s, const F& f) {
+#define TTT_LN(T, l, k, v) \
+  if (s.L == l && s.K == k && s.V == v) return f.template run<T, l, k, v>();
+  if (bf) {
+    TTT_LN(bf16, 8, 1, 8) TTT_LN(bf16, 16, 1, 8) TTT_LN(bf16, 32, 1, 8) TTT_LN(bf16, 64, 1, 8)
+    TTT_LN(bf16, 64, 2, 8) TTT_LN(bf16, 64, 4, 8)
+    TTT_LN(bf16, 256, 2, 8) TTT_LN(bf16, 256, 4, 8) TTT_LN(bf16, 256, 8, 8)
+    TTT_LN(bf16, 64, 1, 1) TTT_LN(bf16, 64, 4, 1) TTT_LN(bf16, 64, 16, 1) TTT_LN(bf16, 256, 16, 1) TTT_LN(bf16, 256, 64, 1)
+  } else {
+    TTT_LN(float, 8, 1, 4) TTT_LN(float, 16, 1, 4) TTT_LN(float, 32, 1, 4) TTT_LN(float, 64, 1, 4)
+    TTT_LN(float, 64, 2, 4) TTT_LN(float, 64, 4, 4)
+    TTT_LN(float, 256, 2, 4) TTT_LN(float, 256, 4, 4) TTT_LN(float, 256, 8, 4) TTT_LN(float, 256, 16, 4)
+    TTT_LN(float, 64, 1, 1) TTT_LN(float, 64, 4, 1) TTT_LN(float, 64, 16, 1) TTT_LN(float, 256, 16, 1) TTT_LN(float, 256, 64, 1)
+  }
+#undef TTT_LN
+  return hipErrorInvalidValue;
+}
+
+bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+// 16-byte accesses need whole vectors per row and aligned rows.
+bool vector_rows(bool bf, int D, long long xs) {
+  const int V = bf ? 8 : 4;
+  return D % V == 0 && xs % V == 0;
+}
+
+struct FwdCall {
+  const void* x;
+  long long xs;
+  const float *w, *b;
+  void* y;
+  int M, H, D;
+  float eps;
+  hipStream_t st;
+  template <class T, int L, int K, int V>
+  hipError_t run() const {
+    constexpr int G = kThreads / L;
+    const int rows = M * H;
+    hipLaunchKernelGGL((layernorm_fwd<T, L, K, V>), wide_grid(((long long)rows + G - 1) / G), dim3(kThreads), 0, st,
+                       (const T*)x, xs, w, b, (T*)y, rows, H, D, eps);
+    return hipGetLastError();
+  }
+};
+
+// The backward's grid: heads per workgroup, tokens at a time, workgroups along the tokens. It does not
+// depend on whether the vector path is taken (both fit the workspace sized for the larger).
+struct BwdPlan {
+  int HB, R, gy;
+  long long P;
+};
+BwdPlan bwd_plan(Shape s, int M, int H) {
+  const int groups = kThreads / s.L;
+  BwdPlan p;
+  p.HB = H < groups ? H : groups;
+  p.R = groups / p.HB;
+  p.gy = (H + p.HB - 1) / p.HB;
+  p.P = (M + p.R - 1) / p.R;
+  const long long most = 1024 / p.gy > 1 ? 1024 / p.gy : 1;
+  if (p.P > most) p.P = most;
+  return p;
+}
+
+struct BwdCall {
+  const void* x;
+  long long xs;
+  const float* w;
+  const void* dy;
+  void* dx;
+  float* part;
+  int M, H, D;
+  float eps;
+  BwdPlan p;
+  hipStream_t st;
+  template <class T, int L, int K, int V>
+  hipError_t run() const {
+    const int threads = (p.HB * p.R * L + 63) / 64 * 64;
+    hipLaunchKernelGGL((layernorm_bwd<T, L, K, V>), dim3((unsigned)p.P, (unsigned)p.gy), dim3(threads), 0, st,
+                       (const T*)x, xs, w, (const T*)dy, (T*)dx, part, M, H, D, p.HB, p.R, eps);
+    return hipGetLastError();
+  }
+};
+
+}  // namespace
+
+hipError_t layernorm_launch(bool bf16_io, int M, int H, int D, float eps, const void* x, long long xs,
+                            const float* w, const float* b, void* y, hipStream_t st) {
+  const bool vec = vector_rows(bf16_io, D, xs) && aligned16(x) && aligned16(w) && aligned16(b) && aligned16(y);
+  return with_shape(bf16_io, shape_of(bf16_io, vec, D), FwdCall{x, xs, w, b, y, M, H, D, eps, st});
+}
+
+size_t layernorm_bwd_workspace_bytes(bool bf16_io, int M, int H, int D) {
+  long long P = bwd_plan(shape_of(bf16_io, false, D), M, H).P;
+  if (vector_rows(bf16_io, D, 0)) {
+    const long long pv = bwd_plan(shape_of(bf16_io, true, D), M, H).P;
+    if (pv > P) P = pv;
+  }
+  return (size_t)P * 2 * H * D * sizeof(float);
+}
+
+hipError_t layernorm_bwd_launch(bool bf16_io, int M, int H, int D, float eps, const void* x,
+                                long long xs, const float* w, const void* dy, void* dx, float* dw,
+                                float* db, void* ws, hipStream_t st) {
+  const bool vec = vector_rows(bf16_io, D, xs) && aligned16(x) && aligned16(w) && aligned16(dy) && aligned16(dx);
+  const Shape s = shape_of(bf16_io, vec, D);
+  const BwdPlan p = bwd_plan(s, M, H);
+  float* part = static_cast<float*>(ws);
+  const hipError_t e = with_shape(bf16_io, s, BwdCall{x, xs, w, dy, dx, part, M, H, D, eps, p, st});
+  if (e != hipSuccess) return e;
+  return column_sum_launch(part, p.P, 2 * H * D, StoreNormGrads{dw, db, H * D}, st);
+}
+
+}  // namespace ttt

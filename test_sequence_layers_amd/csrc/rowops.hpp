@@ -1,0 +1,122 @@
+// Device pieces shared by the block operators' kernels: element loads and stores of either I/O type,
+// sums over groups of lanes, and the sum of partial rows that ends the parameters' gradients.
+#pragma once
+
+#include "device.hpp"
+
+namespace ttt {
+
+// Vector of V elements of T: V = 16 / sizeof(T) (one 16-byte access) or V = 1.
+template <class T, int V>
+__device__ __forceinline__ void load_row(const T* p, float* out) {
+  if constexpr (V == 1) {
+    out[0] = (float)p[0];
+  } else if constexpr (sizeof(T) == 2) {
+    const uint4 q = ld16(p);
+    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+    for (int i = 0; i < 4; ++i) {
+      out[2 * i] = __uint_as_float(w[i] << 16);
+      out[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
+  } else {
+    const float4 q = *reinterpret_cast<const float4*>(p);
+    out[0] = q.x; out[1] = q.y; out[2] = q.z; out[3] = q.w;
+  }
+}
+
+template <class T, int V>
+__device__ __forceinline__ void store_row(T* p, const float* v) {
+  if constexpr (V == 1) {
+    p[0] = (T)v[0];
+  } else if constexpr (sizeof(T) == 2) {
+    const bf16x8 o = cat8(to_bf16x4(f32x4{v[0], v[1], v[2], v[3]}), to_bf16x4(f32x4{v[4], v[5], v[6], v[7]}));
+    st16(p, __builtin_bit_cast(uint4, o));
+  } else {
+    *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
+  }
+}
+
+// V fp32 parameters; in the vector case p is 16-byte aligned.
+template <int V>
+__device__ __forceinline__ void load_params(const float* p, float* out) {
+  if constexpr (V == 1) {
+    out[0] = p[0];
+  } else {
+    for (int i = 0; i < V; i += 4) {
+      const float4 q = *reinterpret_cast<const float4*>(p + i);
+      out[i] = q.x; out[i + 1] = q.y; out[i + 2] = q.z; out[i + 3] = q.w;
+    }
+  }
+}
+
+template <int CTRL>
+__device__ __forceinline__ float dpp(float v) {
+  return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), CTRL, 0xf, 0xf, true));
+}
+constexpr int kDppXor1 = 0xB1;     // quad_perm [1, 0, 3, 2]
+constexpr int kDppXor2 = 0x4E;     // quad_perm [2, 3, 0, 1]
+constexpr int kDppMirror8 = 0x141;   // lane i of 8 reads lane 7 - i
+constexpr int kDppMirror16 = 0x140;  // lane i of 16 reads lane 15 - i
+constexpr int kDppRor8 = 0x128;      // lane i of 16 reads lane i ^ 8
+
+// Sum over aligned groups of L lanes (L a power of two up to 64); every lane gets it. Within 16
+// lanes by DPP: once the lanes of a quad agree, the mirrored lane holds the other quad's sum.
+template <int L>
+__device__ __forceinline__ float lanes_sum(float v) {
+  if constexpr (L >= 2) v += dpp<kDppXor1>(v);
+  if constexpr (L >= 4) v += dpp<kDppXor2>(v);
+  if constexpr (L >= 8) v += dpp<kDppMirror8>(v);
+  if constexpr (L >= 16) v += dpp<kDppMirror16>(v);
+  if constexpr (L >= 32) v += __shfl_xor(v, 16);
+  if constexpr (L >= 64) v += __shfl_xor(v, 32);
+  return v;
+}
+
+__device__ __forceinline__ float exp2_hw(float x) { return __builtin_amdgcn_exp2f(x); }
+__device__ __forceinline__ float rcp_hw(float x) { return __builtin_amdgcn_rcpf(x); }
+constexpr float kLog2e = 1.44269504088896340736f;
+// 1 / (1 + exp(-x)); exp(-x) overflows to infinity, whose reciprocal is 0, for x below about -88.
+__device__ __forceinline__ float sigmoid(float x) { return rcp_hw(1.f + exp2_hw(-kLog2e * x)); }
+
+// A launch's threads along one axis stay below 2^32: blocks past 2^20 go to a second axis.
+inline dim3 wide_grid(long long blocks) {
+  const long long x = blocks < (1 << 20) ? blocks : (1 << 20);
+  return dim3((unsigned)x, (unsigned)((blocks + x - 1) / x));
+}
+__device__ __forceinline__ long long wide_block() { return (long long)blockIdx.y * gridDim.x + blockIdx.x; }
+
+// Sum of P rows of W fp32 values, fixed order: thread row ty of 16 adds rows ty, ty + 16, ..., then
+// the 16 sums are added in order. out(column, sum) stores it.
+constexpr int kSumCols = 64, kSumRows = 16;
+template <class Out>
+__global__ __launch_bounds__(kSumCols* kSumRows) void column_sum(const float* __restrict__ part,
+                                                                 long long P, int W, Out out) {
+  __shared__ float sm[kSumRows][kSumCols];
+  const int tx = threadIdx.x % kSumCols, ty = threadIdx.x / kSumCols;
+  const int col = blockIdx.x * kSumCols + tx;
+  float acc = 0.f;
+  if (col < W) {
+    const float* p = part + col;
+    long long r = ty;
+    for (; r + 3 * kSumRows < P; r += 4 * kSumRows) {
+      float v[4];
+      for (int i = 0; i < 4; ++i) v[i] = p[(r + i * kSumRows) * W];
+      for (int i = 0; i < 4; ++i) acc += v[i];
+    }
+    for (; r < P; r += kSumRows) acc += p[r * W];
+  }
+  sm[ty][tx] = acc;
+  __syncthreads();
+  if (ty == 0 && col < W) {
+    for (int i = 1; i < kSumRows; ++i) acc += sm[i][tx];
+    out(col, acc);
+  }
+}
+template <class Out>
+hipError_t column_sum_launch(const float* part, long long P, int W, Out out, hipStream_t st) {
+  hipLaunchKernelGGL(column_sum<Out>, dim3((unsigned)((W + kSumCols - 1) / kSumCols)), dim3(kSumCols * kSumRows), 0,
+                     st, part, P, W, out);
+  return hipGetLastError();
+}
+
+}  // namespace ttt

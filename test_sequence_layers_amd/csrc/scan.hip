@@ -1,0 +1,698 @@
+// Selective state space scan: forward, one token at a time, and backward. Per channel c with S states,
+//   dt = softplus(delta + dbias),  h[s] = exp(dt A[s]) h[s] + dt B[s] u,  y = (sum_s C[s] h[s] + D u) z sigmoid(z).
+//
+// The recurrence is linear in h, so a sequence is cut into segments: a first launch runs every segment
+// from h = 0 and keeps its end state and its sum of dt (the segment's decay is exp(A sum dt)), a
+// second folds the segments' (decay, end) pairs in order into each segment's start state, and a last
+// one runs all segments again from their starts and writes y. A sequence of one segment needs the
+// last only.
+//
+// A lane owns one channel with all its S states in registers, a wave 64 channels of one segment: B
+// and C are then the same for the whole wave and come through scalar loads into SGPRs, the sum over
+// the states stays inside the lane, and every access of u, delta, z and y is a contiguous run over
+// channels. What bounds it is the vector ALU: one exponential (quarter rate) and four multiplies or
+// multiply-adds per state and token.
+#include "internal.hpp"
+#include "rowops.hpp"
+#include "seq.hpp"
+
+namespace ttt {
+namespace {
+
+constexpr int kWaves = 4;   // units per workgroup (forward)
+constexpr int kTok = 4;     // tokens loaded ahead
+
+// log(1 + exp(x)) with e = exp(-|x|): max(x, 0) + log1p(e), and log1p(e) = 2 atanh(e / (2 + e)) by
+// its series in odd powers of s = e / (2 + e) <= 1/3. The terms left out are below 9^-8 / 17 = 1.4e-9
+// of the sum, and small e keeps its relative precision. e is returned for the derivative.
+__device__ __forceinline__ float softplus_of(float x, float& e) {
+  e = exp2_hw(-kLog2e * fabsf(x));
+  const float s = e * rcp_hw(2.f + e), q = s * s;
+  float p = 1.f / 15.f;
+  p = fmaf(p, q, 1.f / 13.f);
+  p = fmaf(p, q, 1.f / 11.f);
+  p = fmaf(p, q, 1.f / 9.f);
+  p = fmaf(p, q, 1.f / 7.f);
+  p = fmaf(p, q, 1.f / 5.f);
+  p = fmaf(p, q, 1.f / 3.f);
+  p = fmaf(p, q, 1.f);
+  return fmaxf(x, 0.f) + 2.f * s * p;
+}
+// The step and its derivative by delta.
+__device__ __forceinline__ float step_of(float raw, int softplus) {
+  float e;
+  return softplus ? softplus_of(raw, e) : raw;
+}
+__device__ __forceinline__ float step_grad_of(float raw, int softplus, float& grad) {
+  if (!softplus) {
+    grad = 1.f;
+    return raw;
+  }
+  float e;
+  const float dt = softplus_of(raw, e);
+  grad = (raw >= 0.f ? 1.f : e) * rcp_hw(1.f + e);
+  return dt;
+}
+
+// S values of a row of B or C that is the same for the whole wave, by scalar loads.
+typedef const __attribute__((address_space(4))) uint32_t* ScalarPtr;
+template <class T, int S>
+__device__ __forceinline__ void load_uniform(const T* p, float* out) {
+  ScalarPtr q = (ScalarPtr)(uintptr_t)p;
+  if constexpr (sizeof(T) == 2) {
+#pragma unroll
+    for (int i = 0; i < S / 2; ++i) {
+      const uint32_t w = q[i];
+      out[2 * i] = __uint_as_float(w << 16);
+      out[2 * i + 1] = __uint_as_float(w & 0xffff0000u);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < S; ++i) out[i] = __uint_as_float(q[i]);
+  }
+}
+
+// How a call is cut up. Channel blocks: 64 channels of one group each.
+struct Plan {
+  int cbg, cb;      // channel blocks per group, in all
+  int nseg, T;      // segments per sequence, tokens each
+};
+
+struct Unit {
+  int b, seg, cb, g, c;  // c: this lane's channel (a block's lanes past its group repeat the first)
+  bool live;
+};
+__device__ __forceinline__ Unit unit_of(int id, const Plan& p, int C, int G) {
+  Unit u;
+  u.cb = id % p.cb;
+  const int rest = id / p.cb;
+  u.seg = rest % p.nseg;
+  u.b = rest / p.nseg;
+  u.g = u.cb / p.cbg;
+  const int cg = C / G, first = (u.cb - u.g * p.cbg) * 64;
+  u.live = first + lane_id() < cg;
+  u.c = u.g * cg + first + (u.live ? lane_id() : 0);
+  return u;
+}
+
+__device__ __forceinline__ int length_of(const int* lengths, int b, int N) {
+  return lengths ? min(max(lengths[b], 0), N) : N;
+}
+
+// Forward. FINAL: from the segment's start state (ends, once folded; h0 or zeros for a single
+// segment), writing y and h_out. Otherwise from zero, writing the end state and the sum of dt.
+// ends: [B][nseg][S][C], sums: [B][nseg][C].
+template <class T, int S, bool FINAL>
+__global__ __launch_bounds__(64 * kWaves) void scan_fwd(ScanArgs a, Plan p, int units, float* __restrict__ ends,
+                                                        float* __restrict__ sums) {
+  const int id = blockIdx.x * kWaves + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  if (id >= units) return;
+  const Unit un = unit_of(id, p, a.C, a.G);
+  const int C = a.C, N = a.N, c = un.c;
+  const int n = length_of(a.lengths, un.b, N);
+  const int t0 = un.seg * p.T, t1 = min(N, t0 + p.T), te = min(t1, n);
+  const long long row0 = (long long)un.b * N;
+  const T* u = (const T*)a.u + row0 * a.us + c;
+  const T* de = (const T*)a.delta + row0 * a.ds + c;
+  const T* z = a.z ? (const T*)a.z + row0 * a.zs + c : nullptr;
+  const T* bm = (const T*)a.bm + row0 * a.bs + (long long)un.g * S;
+  const T* cm = (const T*)a.cm + row0 * a.cs + (long long)un.g * S;
+  T* y = (T*)a.y + row0 * C + c;
+  const long long seg_at = ((long long)un.b * p.nseg + un.seg) * C;
+
+  float A2[S], h[S];
+  for (int s = 0; s < S; ++s) A2[s] = a.A[(long long)c * S + s] * kLog2e;
+  for (int s = 0; s < S; ++s) {
+    if (FINAL && p.nseg > 1) h[s] = ends[seg_at * S + (long long)s * C + c];
+    else if (FINAL && a.h0) h[s] = a.h0[((long long)un.b * C + c) * S + s];
+    else h[s] = 0.f;
+  }
+  const float db = a.dbias ? a.dbias[c] : 0.f, D = FINAL && a.D ? a.D[c] : 0.f;
+  float sum = 0.f;
+  const bool gate = FINAL && z;
+  // The next kTok tokens' rows are loaded before this kTok are worked on (past the end: the last row again).
+  float nu[kTok], nd[kTok], nz[kTok];
+  auto fetch = [&](int t) {
+#pragma unroll
+    for (int j = 0; j < kTok; ++j) {
+      const long long tt = min(t + j, te - 1);
+      nu[j] = (float)u[tt * a.us];
+      nd[j] = (float)de[tt * a.ds];
+      nz[j] = gate ? (float)z[tt * a.zs] : 0.f;
+    }
+  };
+  if (t0 < te) fetch(t0);
+  for (int t = t0; t < te; t += kTok) {
+    float cu[kTok], cd[kTok], cz[kTok];
+#pragma unroll
+    for (int j = 0; j < kTok; ++j) cu[j] = nu[j], cd[j] = nd[j], cz[j] = nz[j];
+    fetch(t + kTok);
+#pragma unroll
+    for (int j = 0; j < kTok; ++j) {
+      if (t + j < te) {
+        float bv[S], cv[S];
+        load_uniform<T, S>(bm + (long long)(t + j) * a.bs, bv);
+        if (FINAL) load_uniform<T, S>(cm + (long long)(t + j) * a.cs, cv);
+        const float dt = step_of(cd[j] + db, a.softplus), dtu = dt * cu[j];
+        float out = 0.f;
+#pragma unroll
+        for (int s = 0; s < S; ++s) {
+          h[s] = fmaf(exp2_hw(dt * A2[s]), h[s], dtu * bv[s]);
+          if (FINAL) out = fmaf(cv[s], h[s], out);
+        }
+        if (FINAL) {
+          out = fmaf(D, cu[j], out);
+          if (gate) out *= cz[j] * sigmoid(cz[j]);
+          if (un.live) y[(long long)(t + j) * C] = (T)out;
+        } else {
+          sum += dt;
+        }
+      }
+    }
+  }
+  if (!un.live) return;
+  if (FINAL) {
+    for (int t = max(t0, te); t < t1; ++t) y[(long long)t * C] = (T)0.f;
+    if (a.h_out && un.seg == p.nseg - 1)
+      for (int s = 0; s < S; ++s) a.h_out[((long long)un.b * C + c) * S + s] = h[s];
+  } else {
+    for (int s = 0; s < S; ++s) ends[seg_at * S + (long long)s * C + c] = h[s];
+    sums[seg_at + c] = sum;
+  }
+}
+
+// Folds the segments in order: ends[seg] becomes the segment's start state. One thread per (b, s, c).
+// For the backward pass back (same layout) holds the segments' own contributions to a_0 q_0 of their
+// first token, and becomes what flows into each segment from behind it; dh0 receives the first's.
+__global__ __launch_bounds__(256) void scan_fold(const float* __restrict__ A, const float* __restrict__ h0,
+                                                 float* __restrict__ ends, float* __restrict__ back,
+                                                 const float* __restrict__ sums, float* __restrict__ dh0,
+                                                 int C, int S, int nseg) {
+  const long long id = (long long)blockIdx.x * 256 + threadIdx.x;
+  if (id >= (long long)C * S) return;
+  const int s = (int)(id / C), c = (int)(id - (long long)s * C), b = blockIdx.y;
+  const float A2 = A[(long long)c * S + s] * kLog2e;
+  const long long hat = ((long long)b * C + c) * S + s;
+  float* e = ends + (long long)b * nseg * S * C + id;
+  const float* dts = sums + (long long)b * nseg * C + c;
+  const long long step = (long long)S * C;
+  if (blockIdx.z == 0) {
+    float h = h0 ? h0[hat] : 0.f;
+    for (int i = 0; i < nseg; ++i) {
+      const float own = e[i * step];
+      e[i * step] = h;
+      h = fmaf(exp2_hw(A2 * dts[(long long)i * C]), h, own);
+    }
+  } else {
+    float* f = back + (long long)b * nseg * S * C + id;
+    float q = 0.f;
+    for (int i = nseg - 1; i >= 0; --i) {
+      const float own = f[i * step];
+      f[i * step] = q;
+      q = fmaf(exp2_hw(A2 * dts[(long long)i * C]), q, own);
+    }
+    if (dh0) dh0[hat] = q;
+  }
+}
+
+// One token: S / 4 lanes per channel, four states each (one 16-byte access of the state).
+template <class T, int S, bool VEC>
+__global__ __launch_bounds__(256) void scan_step(ScanArgs a) {
+  constexpr int L = S / 4;
+  const long long id = wide_block() * 256 + threadIdx.x;
+  const long long row = id / L;  // b * C + c
+  if (row >= (long long)a.B * a.C) return;  // (whole groups of L lanes)
+  const int q = (int)(id % L), b = (int)(row / a.C), c = (int)(row - (long long)b * a.C);
+  const int g = c / (a.C / a.G);
+  float h[4], A[4], bv[4], cv[4];
+  if (VEC) {
+    load_params<4>(a.h0 + row * S + 4 * q, h);
+    load_params<4>(a.A + (long long)c * S + 4 * q, A);
+  } else {
+    for (int i = 0; i < 4; ++i) h[i] = a.h0[row * S + 4 * q + i];
+    for (int i = 0; i < 4; ++i) A[i] = a.A[(long long)c * S + 4 * q + i];
+  }
+  const T* bm = (const T*)a.bm + b * a.bs + (long long)g * S + 4 * q;
+  const T* cm = (const T*)a.cm + b * a.cs + (long long)g * S + 4 * q;
+  for (int i = 0; i < 4; ++i) bv[i] = (float)bm[i];
+  for (int i = 0; i < 4; ++i) cv[i] = (float)cm[i];
+  const float u = (float)((const T*)a.u)[b * a.us + c];
+  const float z = a.z ? (float)((const T*)a.z)[b * a.zs + c] : 0.f;
+  const float raw = (float)((const T*)a.delta)[b * a.ds + c] + (a.dbias ? a.dbias[c] : 0.f);
+  const float dt = step_of(raw, a.softplus), dtu = dt * u;
+  float y = 0.f;
+  for (int i = 0; i < 4; ++i) {
+    h[i] = fmaf(exp2_hw(dt * (A[i] * kLog2e)), h[i], dtu * bv[i]);
+    y = fmaf(cv[i], h[i], y);
+  }
+  y = lanes_sum<L>(y);
+  if (a.D) y = fmaf(a.D[c], u, y);
+  if (a.z) y *= z * sigmoid(z);
+  if (VEC) {
+    *reinterpret_cast<float4*>(a.h_out + row * S + 4 * q) = make_float4(h[0], h[1], h[2], h[3]);
+  } else {
+    for (int i = 0; i < 4; ++i) a.h_out[row * S + 4 * q + i] = h[i];
+  }
+  if (q == 0) ((T*)a.y)[row] = (T)y;
+}
+
+// ---- backward ---------------------------------------------------------------------------------
+//   v = dy z sigmoid(z),  q_n = v_n C_n + a_{n+1} q_{n+1}  (from the last token back)
+// scan_bwd_ends runs every segment once from h = 0, keeping the local state and the sum of dt at every
+// kSub-th token (the checkpoints), the end state, and the segment's contribution to a_0 q_0 of its
+// first token, sum_n (a_0 ... a_n) v_n C_n, whose running product shares the exponentials. scan_fold
+// joins the segments in both directions. scan_bwd then takes the sub-chunks of a segment from its
+// last to its first: it forms the sub-chunk's a and h in registers from the checkpoint (one more
+// exponential per state and token) and walks back through them.
+
+// Tokens per sub-chunk, states per wave and waves of a scan_bwd workgroup: kSub * SW = 64 values of
+// each of a and h stay in a lane's registers.
+template <int S>
+struct Bwd {
+  static constexpr int SW = S == 64 ? 8 : 4;
+  static constexpr int NW = S / SW;
+  static constexpr int kSub = 64 / SW;
+};
+int bwd_sub(int S) { return S == 64 ? 8 : 16; }
+
+// Buffers in the workspace.
+struct BwdBufs {
+  float* ends;   // [B][nseg][S][C]
+  float* back;   // [B][nseg][S][C]
+  float* sums;   // [B][nseg][C]
+  float* ck;     // [B][nsub][S][C] local states at the sub-chunks' starts
+  float* cksum;  // [B][nsub][C] sums of dt from the segment's start to the sub-chunk's
+  float* mats;   // [B][N][CB][2 S] a channel block's sums for dB and dC
+  float* part;   // [B][nseg][S C + 2 C] a segment's dA ([S][C]), dD, ddbias
+  int nsub;      // sub-chunks per sequence
+};
+
+template <class T, int S, int SB>
+__global__ __launch_bounds__(64 * kWaves) void scan_bwd_ends(ScanArgs a, Plan p, int units, BwdBufs w) {
+  constexpr int kSub = Bwd<S>::kSub;
+  int id = blockIdx.x * kWaves + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  if (id >= units) return;
+  constexpr int NB = S / SB;  // state blocks, one per wave
+  const int s0 = id % NB * SB;
+  const Unit un = unit_of(id / NB, p, a.C, a.G);
+  const int C = a.C, N = a.N, c = un.c;
+  const int n = length_of(a.lengths, un.b, N);
+  const int t0 = un.seg * p.T, t1 = min(N, t0 + p.T), te = min(t1, n);
+  const long long row0 = (long long)un.b * N;
+  const T* u = (const T*)a.u + row0 * a.us + c;
+  const T* de = (const T*)a.delta + row0 * a.ds + c;
+  const T* z = a.z ? (const T*)a.z + row0 * a.zs + c : nullptr;
+  const T* dy = (const T*)a.dy + row0 * C + c;
+  const T* bm = (const T*)a.bm + row0 * a.bs + (long long)un.g * S + s0;
+  const T* cm = (const T*)a.cm + row0 * a.cs + (long long)un.g * S + s0;
+  float A2[SB], h[SB], P[SB], q[SB];
+  for (int s = 0; s < SB; ++s) {
+    A2[s] = a.A[(long long)c * S + s0 + s] * kLog2e;
+    h[s] = q[s] = 0.f;
+    P[s] = 1.f;
+  }
+  const float db = a.dbias ? a.dbias[c] : 0.f;
+  float sum = 0.f;
+  for (int t = t0; t < t1; ++t) {
+    if ((t - t0) % kSub == 0 && un.live) {
+      const long long k = (long long)un.b * w.nsub + t / kSub;
+      for (int s = 0; s < SB; ++s) w.ck[(k * S + s0 + s) * C + c] = h[s];
+      if (s0 == 0) w.cksum[k * C + c] = sum;
+    }
+    if (t < te) {
+      float bv[SB], cv[SB];
+      load_uniform<T, SB>(bm + (long long)t * a.bs, bv);
+      load_uniform<T, SB>(cm + (long long)t * a.cs, cv);
+      const float dt = step_of((float)de[(long long)t * a.ds] + db, a.softplus);
+      const float dtu = dt * (float)u[(long long)t * a.us];
+      float v = (float)dy[(long long)t * C];
+      if (z) {
+        const float zz = (float)z[(long long)t * a.zs];
+        v *= zz * sigmoid(zz);
+      }
+      sum += dt;
+#pragma unroll
+      for (int s = 0; s < SB; ++s) {
+        const float e = exp2_hw(dt * A2[s]);
+        h[s] = fmaf(e, h[s], dtu * bv[s]);
+        P[s] *= e;
+        q[s] = fmaf(P[s], v * cv[s], q[s]);
+      }
+    }
+  }
+  if (!un.live) return;
+  const long long seg = (long long)un.b * p.nseg + un.seg;
+  for (int s = 0; s < SB; ++s) {
+    w.ends[(seg * S + s0 + s) * C + c] = h[s];
+    w.back[(seg * S + s0 + s) * C + c] = q[s];
+  }
+  if (s0 == 0) w.sums[seg * C + c] = sum;
+}
+
+// Sums 64 values over the 64 lanes: lane l gets the total of v[l]. Each step halves the values and the
+// lanes that hold a part of each: 32 and 16 by swaps of register halves, the rest within 16 lanes.
+__device__ __forceinline__ float lanes_scatter_sum(float* v) {
+#pragma unroll
+  for (int i = 0; i < 32; ++i) {
+    const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v[i]), __float_as_uint(v[i + 32]), false, false);
+    v[i] = __uint_as_float(r[0]) + __uint_as_float(r[1]);
+  }
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(v[i]), __float_as_uint(v[i + 16]), false, false);
+    v[i] = __uint_as_float(r[0]) + __uint_as_float(r[1]);
+  }
+  const int l = lane_id();
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = (l & 8 ? v[i + 8] : v[i]) + dpp<kDppRor8>(l & 8 ? v[i] : v[i + 8]);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) v[i] = (l & 4 ? v[i + 4] : v[i]) + dpp<kDppMirror8>(l & 4 ? v[i] : v[i + 4]);
+#pragma unroll
+  for (int i = 0; i < 2; ++i) v[i] = (l & 2 ? v[i + 2] : v[i]) + dpp<kDppXor2>(l & 2 ? v[i] : v[i + 2]);
+  return (l & 1 ? v[1] : v[0]) + dpp<kDppXor1>(l & 1 ? v[0] : v[1]);
+}
+
+// One workgroup per (b, segment, channel block), NW waves with SW states each of the same 64 channels.
+// A sub-chunk's per-channel values (dt, dt u, v) are formed once, a share of the tokens per wave, and
+// passed through LDS; each wave's sums over its states come back the same way.
+template <class T, int S>
+__global__ __launch_bounds__(64 * Bwd<S>::NW) void scan_bwd(ScanArgs a, Plan p, BwdBufs w) {
+  constexpr int SW = Bwd<S>::SW, NW = Bwd<S>::NW, kSub = Bwd<S>::kSub;
+  constexpr int TW = kSub / NW;          // tokens a wave prepares and finishes
+  constexpr int RB = 64 / (2 * SW);      // tokens whose dB and dC sums fill the 64 lanes
+  static_assert(kSub % NW == 0 && kSub % RB == 0, "sub-chunk shares");
+  __shared__ float s_dt[kSub][64], s_dtu[kSub][64], s_v[kSub][64];
+  __shared__ float s_y[NW][kSub][64], s_q[NW][kSub][64], s_r[NW][kSub][64];
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), l = lane_id();
+  const Unit un = unit_of(blockIdx.x, p, a.C, a.G);
+  const int C = a.C, N = a.N, c = un.c, s0 = wave * SW;
+  const int n = length_of(a.lengths, un.b, N);
+  const int t0 = un.seg * p.T, t1 = min(N, t0 + p.T);
+  const long long row0 = (long long)un.b * N;
+  const T* u = (const T*)a.u + row0 * a.us + c;
+  const T* de = (const T*)a.delta + row0 * a.ds + c;
+  const T* z = a.z ? (const T*)a.z + row0 * a.zs + c : nullptr;
+  const T* dy = (const T*)a.dy + row0 * C + c;
+  const T* bm = (const T*)a.bm + row0 * a.bs + (long long)un.g * S + s0;
+  const T* cm = (const T*)a.cm + row0 * a.cs + (long long)un.g * S + s0;
+  const long long seg = (long long)un.b * p.nseg + un.seg;
+  float A[SW], A2[SW], hs[SW], q[SW], dA[SW];
+  for (int s = 0; s < SW; ++s) {
+    A[s] = a.A[(long long)c * S + s0 + s];
+    A2[s] = A[s] * kLog2e;
+    hs[s] = w.ends[(seg * S + s0 + s) * C + c];
+    q[s] = w.back[(seg * S + s0 + s) * C + c];  // a q of the token behind
+    dA[s] = 0.f;
+  }
+  const float db = a.dbias ? a.dbias[c] : 0.f, D = a.D ? a.D[c] : 0.f;
+  float dD = 0.f, ddb = 0.f;
+  for (int tc = t0 + (t1 - 1 - t0) / kSub * kSub; tc >= t0; tc -= kSub) {
+    float pu[TW], pv[TW], pg[TW], pz[TW], pdy[TW], pdt[TW];
+#pragma unroll
+    for (int j = 0; j < TW; ++j) {
+      const int i = wave * TW + j, t = tc + i;
+      pu[j] = pv[j] = pg[j] = pz[j] = pdy[j] = pdt[j] = 0.f;
+      if (t < n && t < t1 && un.live) {
+        pu[j] = (float)u[(long long)t * a.us];
+        pdt[j] = step_grad_of((float)de[(long long)t * a.ds] + db, a.softplus, pg[j]);
+        pdy[j] = (float)dy[(long long)t * C];
+        pv[j] = pdy[j];
+        if (z) {
+          pz[j] = (float)z[(long long)t * a.zs];
+          pv[j] *= pz[j] * sigmoid(pz[j]);
+        }
+      }
+      s_dt[i][l] = pdt[j];
+      s_dtu[i][l] = pdt[j] * pu[j];
+      s_v[i][l] = pv[j];
+    }
+    __syncthreads();
+    const int te = min(t1, n) - tc;  // tokens of this sub-chunk (uniform)
+    float h0[SW], e[kSub][SW], h[kSub][SW];
+    {
+      const long long k = (long long)un.b * w.nsub + tc / kSub;
+      const float past = w.cksum[k * C + c];
+      for (int s = 0; s < SW; ++s)
+        h0[s] = fmaf(exp2_hw(A2[s] * past), hs[s], w.ck[(k * S + s0 + s) * C + c]);
+    }
+#pragma unroll
+    for (int j = 0; j < kSub; ++j) {
+      if (j < te) {
+        float bv[SW], cv[SW];
+        load_uniform<T, SW>(bm + (long long)(tc + j) * a.bs, bv);
+        load_uniform<T, SW>(cm + (long long)(tc + j) * a.cs, cv);
+        const float dt = s_dt[j][l], dtu = s_dtu[j][l];
+        float y = 0.f;
+#pragma unroll
+        for (int s = 0; s < SW; ++s) {
+          e[j][s] = exp2_hw(dt * A2[s]);
+          h[j][s] = fmaf(e[j][s], j ? h[j ? j - 1 : 0][s] : h0[s], dtu * bv[s]);
+          y = fmaf(cv[s], h[j][s], y);
+        }
+        s_y[wave][j][l] = y;
+      }
+    }
+#pragma unroll
+    for (int jb = kSub - RB; jb >= 0; jb -= RB) {
+      float val[64];
+#pragma unroll
+      for (int i = 0; i < 64; ++i) val[i] = 0.f;
+#pragma unroll
+      for (int jj = RB - 1; jj >= 0; --jj) {
+        const int j = jb + jj;
+        if (j < te) {
+          float bv[SW], cv[SW];
+          load_uniform<T, SW>(bm + (long long)(tc + j) * a.bs, bv);
+          load_uniform<T, SW>(cm + (long long)(tc + j) * a.cs, cv);
+          const float dt = s_dt[j][l], dtu = s_dtu[j][l], v = s_v[j][l];
+          float qb = 0.f, r = 0.f;
+#pragma unroll
+          for (int s = 0; s < SW; ++s) {
+            q[s] = fmaf(v, cv[s], q[s]);
+            val[jj * 2 * SW + s] = q[s] * dtu;
+            val[jj * 2 * SW + SW + s] = v * h[j][s];
+            qb = fmaf(q[s], bv[s], qb);
+            q[s] *= e[j][s];
+            const float x = q[s] * (j ? h[j ? j - 1 : 0][s] : h0[s]);
+            r = fmaf(x, A[s], r);
+            dA[s] = fmaf(x, dt, dA[s]);
+          }
+          s_q[wave][j][l] = qb;
+          s_r[wave][j][l] = r;
+        }
+      }
+      if (tc + jb < t1) {  // (uniform)
+        const float total = lanes_scatter_sum(val);
+        const int t = tc + jb + l / (2 * SW), k = l % (2 * SW);
+        if (t < t1)
+          w.mats[((row0 + t) * p.cb + un.cb) * 2 * S + (k / SW) * S + s0 + k % SW] = total;
+      }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < TW; ++j) {
+      const int i = wave * TW + j, t = tc + i;
+      if (t < t1 && un.live) {
+        float du = 0.f, dd = 0.f, dz = 0.f;
+        if (t < n) {
+          float sq = 0.f, sr = 0.f, sy = 0.f;
+          for (int k = 0; k < NW; ++k) sq += s_q[k][i][l], sr += s_r[k][i][l], sy += s_y[k][i][l];
+          du = fmaf(sq, pdt[j], D * pv[j]);
+          dd = fmaf(sq, pu[j], sr) * pg[j];
+          dD = fmaf(pv[j], pu[j], dD);
+          ddb += dd;
+          if (z) {
+            const float sg = sigmoid(pz[j]);
+            dz = pdy[j] * fmaf(D, pu[j], sy) * sg * fmaf(pz[j], 1.f - sg, 1.f);
+          }
+        }
+        const long long at = (row0 + t) * C + c;
+        ((T*)a.du)[at] = (T)du;
+        ((T*)a.ddelta)[at] = (T)dd;
+        if (z) ((T*)a.dz)[at] = (T)dz;
+      }
+    }
+  }
+  float* part = w.part + seg * ((long long)S * C + 2 * C);
+  if (un.live)
+    for (int s = 0; s < SW; ++s) part[(long long)(s0 + s) * C + c] = dA[s];
+  __syncthreads();
+  s_dt[wave][l] = dD;
+  s_dtu[wave][l] = ddb;
+  __syncthreads();
+  if (wave == 0 && un.live) {
+    for (int k = 1; k < NW; ++k) dD += s_dt[k][l], ddb += s_dtu[k][l];
+    part[(long long)S * C + c] = dD;
+    part[(long long)S * C + C + c] = ddb;
+  }
+}
+
+// dB and dC: the channel blocks of a group summed. One thread per (b, n, matrix, g, s).
+template <class T>
+__global__ __launch_bounds__(256) void scan_bwd_mats(const float* __restrict__ mats, T* __restrict__ dB,
+                                                     T* __restrict__ dC, long long rows, int G, int S,
+                                                     int cbg) {
+  const long long id = wide_block() * 256 + threadIdx.x;
+  const int width = 2 * G * S;
+  if (id >= rows * width) return;
+  const long long row = id / width;
+  const int r = (int)(id - row * width), which = r / (G * S), gs = r - which * G * S, g = gs / S, s = gs - g * S;
+  const float* m = mats + ((row * G + g) * cbg * 2 + which) * S + s;
+  float acc = 0.f;
+  for (int k = 0; k < cbg; ++k) acc += m[(long long)k * 2 * S];
+  (which ? dC : dB)[row * G * S + gs] = (T)acc;
+}
+
+struct StoreScanGrads {
+  float *dA, *dD, *ddb;
+  int C, S;
+  __device__ void operator()(int col, float v) const {
+    const int s = col / C, c = col - s * C;
+    if (s < S) dA[(long long)c * S + s] = v;
+    else if (s == S) {
+      if (dD) dD[c] = v;
+    } else if (ddb) ddb[c] = v;
+  }
+};
+
+// Segments: enough waves for four per SIMD (4096 on 256 CUs of four), but segments of at least
+// min_tokens, a multiple of `unit` tokens.
+Plan plan_of(int B, int N, int C, int G, int want, int min_tokens, int unit) {
+  Plan p;
+  p.cbg = (C / G + 63) / 64;
+  p.cb = p.cbg * G;
+  const long long blocks = (long long)B * p.cb;
+  long long nseg = (want + blocks - 1) / blocks;
+  const long long most = (N + min_tokens - 1) / min_tokens;
+  if (nseg > most) nseg = most;
+  if (nseg < 1) nseg = 1;
+  const long long T = ((N + nseg - 1) / nseg + unit - 1) / unit * unit;
+  p.T = (int)T;
+  p.nseg = (int)((N + T - 1) / T);
+  return p;
+}
+Plan fwd_plan(const ScanArgs& a) {
+  const int cb = (a.C / a.G + 63) / 64 * a.G;
+  if ((long long)a.B * cb >= 2048) return plan_of(a.B, a.N, a.C, a.G, 1, a.N, kTok);
+  return plan_of(a.B, a.N, a.C, a.G, 4096, 64, kTok);
+}
+Plan bwd_plan(const ScanArgs& a, int S) { return plan_of(a.B, a.N, a.C, a.G, 2048, 64, bwd_sub(S)); }
+
+size_t align_up(size_t x) { return (x + 255) / 256 * 256; }
+
+// Lays the backward's buffers out in the workspace; returns its size.
+size_t bwd_layout(const ScanArgs& a, int S, const Plan& p, char* ws, BwdBufs* w) {
+  w->nsub = (a.N + bwd_sub(S) - 1) / bwd_sub(S);
+  size_t at = 0;
+  auto take = [&](size_t floats) {
+    float* r = reinterpret_cast<float*>(ws + at);
+    at += align_up(floats * sizeof(float));
+    return r;
+  };
+  const size_t B = a.B, C = a.C, segs = B * p.nseg, subs = B * w->nsub;
+  w->ends = take(segs * S * C);
+  w->back = take(segs * S * C);
+  w->sums = take(segs * C);
+  w->ck = take(subs * S * C);
+  w->cksum = take(subs * C);
+  w->mats = take(B * a.N * p.cb * 2 * S);
+  w->part = take(segs * (S * C + 2 * C));
+  return at;
+}
+
+hipError_t fold(const ScanArgs& a, int S, const Plan& p, float* ends, float* back, const float* sums, hipStream_t st) {
+  const dim3 grid((unsigned)(((long long)a.C * S + 255) / 256), (unsigned)a.B, back ? 2 : 1);
+  hipLaunchKernelGGL(scan_fold, grid, dim3(256), 0, st, a.A, a.h0, ends, back, sums, a.dh0, a.C, S, p.nseg);
+  return hipGetLastError();
+}
+
+template <class T, int S>
+hipError_t fwd(const ScanArgs& a, void* ws, hipStream_t st) {
+  const Plan p = fwd_plan(a);
+  const long long units = (long long)a.B * p.nseg * p.cb;
+  if (units > 0x7fffffffll) return hipErrorInvalidValue;
+  const dim3 grid((unsigned)((units + kWaves - 1) / kWaves)), block(64 * kWaves);
+  float* ends = static_cast<float*>(ws);
+  float* sums = ends + (size_t)a.B * p.nseg * S * a.C;
+  if (p.nseg > 1) {
+    hipLaunchKernelGGL((scan_fwd<T, S, false>), grid, block, 0, st, a, p, (int)units, ends, sums);
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    e = fold(a, S, p, ends, nullptr, sums, st);
+    if (e != hipSuccess) return e;
+  }
+  hipLaunchKernelGGL((scan_fwd<T, S, true>), grid, block, 0, st, a, p, (int)units, ends, sums);
+  return hipGetLastError();
+}
+
+template <class T, int S>
+hipError_t step(const ScanArgs& a, hipStream_t st) {
+  const long long threads = (long long)a.B * a.C * (S / 4);
+  const dim3 grid = wide_grid((threads + 255) / 256);
+  const bool vec = ((reinterpret_cast<uintptr_t>(a.h0) | reinterpret_cast<uintptr_t>(a.h_out) |
+                     reinterpret_cast<uintptr_t>(a.A)) & 15u) == 0;
+  if (vec) hipLaunchKernelGGL((scan_step<T, S, true>), grid, dim3(256), 0, st, a);
+  else hipLaunchKernelGGL((scan_step<T, S, false>), grid, dim3(256), 0, st, a);
+  return hipGetLastError();
+}
+
+template <class T, int S>
+hipError_t bwd(const ScanArgs& a, void* ws, hipStream_t st) {
+  constexpr int SB = S < 16 ? S : 16;
+  const Plan p = bwd_plan(a, S);
+  BwdBufs w;
+  bwd_layout(a, S, p, static_cast<char*>(ws), &w);
+  const long long units = (long long)a.B * p.nseg * p.cb;
+  const long long ends_units = units * (S / SB);
+  const long long mats = (long long)a.B * a.N * 2 * a.G * S;
+  if (ends_units > 0x7fffffffll) return hipErrorInvalidValue;
+  hipLaunchKernelGGL((scan_bwd_ends<T, S, SB>), dim3((unsigned)((ends_units + kWaves - 1) / kWaves)), dim3(64 * kWaves),
+                     0, st, a, p, (int)ends_units, w);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  e = fold(a, S, p, w.ends, w.back, w.sums, st);
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL((scan_bwd<T, S>), dim3((unsigned)units), dim3(64 * Bwd<S>::NW), 0, st, a, p, w);
+  e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL(scan_bwd_mats<T>, wide_grid((mats + 255) / 256), dim3(256), 0, st, w.mats, (T*)a.dbm, (T*)a.dcm,
+                     (long long)a.B * a.N, a.G, S, p.cbg);
+  e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  return column_sum_launch(w.part, (long long)a.B * p.nseg, S * a.C + 2 * a.C,
+                           StoreScanGrads{a.dA, a.dD, a.ddbias, a.C, S}, st);
+}
+
+}  // namespace
+
+bool scan_supported_s(int S) { return S == 8 || S == 16 || S == 32 || S == 64; }
+
+size_t scan_workspace_bytes(bool, int B, int N, int C, int S, int G) {
+  ScanArgs a{};
+  a.B = B, a.N = N, a.C = C, a.G = G;
+  const Plan p = fwd_plan(a);
+  return p.nseg > 1 ? (size_t)B * p.nseg * (S + 1) * C * sizeof(float) : 0;
+}
+
+size_t scan_bwd_workspace_bytes(bool, int B, int N, int C, int S, int G) {
+  ScanArgs a{};
+  a.B = B, a.N = N, a.C = C, a.G = G;
+  BwdBufs w;
+  return bwd_layout(a, S, bwd_plan(a, S), nullptr, &w);
+}
+
+#define TTT_SCAN(fn, ...)                                               \
+  switch (S) {                                                          \
+    case 8: return bf16_io ? fn<bf16, 8>(__VA_ARGS__) : fn<float, 8>(__VA_ARGS__);    \
+    case 16: return bf16_io ? fn<bf16, 16>(__VA_ARGS__) : fn<float, 16>(__VA_ARGS__); \
+    case 32: return bf16_io ? fn<bf16, 32>(__VA_ARGS__) : fn<float, 32>(__VA_ARGS__); \
+    case 64: return bf16_io ? fn<bf16, 64>(__VA_ARGS__) : fn<float, 64>(__VA_ARGS__); \
+  }                                                                     \
+  return hipErrorInvalidValue;
+
+hipError_t scan_launch(bool bf16_io, int S, const ScanArgs& a, void* ws, hipStream_t st) { TTT_SCAN(fwd, a, ws, st) }
+hipError_t scan_step_launch(bool bf16_io, int S, const ScanArgs& a, hipStream_t st) { TTT_SCAN(step, a, st) }
+hipError_t scan_bwd_launch(bool bf16_io, int S, const ScanArgs& a, void* ws, hipStream_t st) { TTT_SCAN(bwd, a, ws, st) }
+#undef TTT_SCAN
+
+}  // namespace ttt

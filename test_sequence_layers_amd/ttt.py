@@ -18,8 +18,10 @@ TTT_F32, TTT_BF16 = 0, 1
  TTT_OP_BIDIR_BWD) = range(8)
 TTT_NOALLOC_SCRATCH_BYTES = 32 << 20  # static scratch of ttt_forward_fullbatch_noalloc, per device
 
-# Every symbol include/ttt.h declares, with its ctypes signature.
+# Every symbol include/ttt.h and include/ttt_seq.h declare, with its ctypes signature.
 _c_int, _c_float, _c_ll, _vp, _sz = ctypes.c_int, ctypes.c_float, ctypes.c_longlong, ctypes.c_void_p, ctypes.c_size_t
+# the scan's inputs in order: u, delta, A, Bm, Cm, D, delta_bias, z, the strided ones each with their stride
+_SCAN_INPUTS = [_vp, _c_ll, _vp, _c_ll, _vp, _vp, _c_ll, _vp, _c_ll, _vp, _vp, _vp, _c_ll]
 SIGNATURES = {
     "ttt_forward_fullbatch": (_c_int, [_c_int, _c_int, _c_int, _c_int, _c_int, _c_float, _vp, _vp, _vp, _vp, _c_ll,
                                        _vp, _vp, _vp, _sz, _vp]),
@@ -45,6 +47,19 @@ SIGNATURES = {
     "ttt_block_epilogue": (_c_int, [_c_int, _c_int, _c_int, _c_int, _vp, _vp, _vp, _vp, _vp, _vp, _vp]),
     "ttt_workspace_size": (_sz, [_c_int, _c_int, _c_int, _c_int, _c_int, _c_int, _c_int, _c_int]),
     "ttt_status_string": (ctypes.c_char_p, [_c_int]),
+    # include/ttt_seq.h
+    "ttt_forward_layernorm": (_c_int, [_c_int] * 4 + [_c_float, _vp, _c_ll] + [_vp] * 4),
+    "ttt_backward_layernorm": (_c_int, [_c_int] * 4 + [_c_float, _vp, _c_ll] + [_vp] * 6 + [_sz, _vp]),
+    "ttt_backward_layernorm_workspace": (_sz, [_c_int] * 4),
+    "ttt_forward_conv1d": (_c_int, [_c_int] * 6 + [_vp, _c_ll] + [_vp] * 7),
+    "ttt_step_conv1d": (_c_int, [_c_int] * 5 + [_vp, _c_ll] + [_vp] * 6),
+    "ttt_backward_conv1d": (_c_int, [_c_int] * 6 + [_vp, _c_ll] + [_vp] * 10 + [_sz, _vp]),
+    "ttt_backward_conv1d_workspace": (_sz, [_c_int] * 5),
+    "ttt_forward_selective_scan": (_c_int, [_c_int] * 7 + _SCAN_INPUTS + [_vp] * 5 + [_sz, _vp]),
+    "ttt_forward_selective_scan_workspace": (_sz, [_c_int] * 6),
+    "ttt_step_selective_scan": (_c_int, [_c_int] * 6 + _SCAN_INPUTS + [_vp] * 4),
+    "ttt_backward_selective_scan": (_c_int, [_c_int] * 7 + _SCAN_INPUTS + [_vp] * 13 + [_sz, _vp]),
+    "ttt_backward_selective_scan_workspace": (_sz, [_c_int] * 6),
 }
 
 _lib = None
