@@ -13,7 +13,11 @@ torch = None  # bound by the first call: the package itself loads without torch
 
 
 class _Call:
-    """The device, dtype and stream of one call, and the checks of its tensors against them."""
+    """The device, dtype and stream of one call, and the checks of its tensors against them.
+
+    A single-token call takes a few microseconds on the device, so the checks cost as little host time as
+    they can: each tensor is compared with what it should be at once, and only one that differs is
+    looked at piece by piece for the error's text."""
 
     def __init__(self, name, x, stream):
         global torch
@@ -25,7 +29,10 @@ class _Call:
         self.dt = _dtype_code(x)
         self.stream = stream
 
-    def _on_device(self, name, t, dtype, shape):
+    def _fits(self, t, dtype, shape):
+        return isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.device == self.device
+
+    def _refuse(self, name, t, dtype, shape):
         if not isinstance(t, torch.Tensor) or not t.is_cuda:
             raise TypeError(f"{name} must be a CUDA (HIP) tensor")
         if t.device != self.device:
@@ -34,22 +41,25 @@ class _Call:
             raise ValueError(f"{name} must have dtype {dtype}, not {t.dtype}")
         if t.shape != shape:
             raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
-
-    def dense(self, name, t, shape, dtype=None):
-        """Data pointer of a contiguous tensor (fp32 unless told otherwise); None for None."""
-        return None if t is None else self.need(name, t, shape, dtype)
+        raise ValueError(f"{name} must be contiguous")
 
     def need(self, name, t, shape, dtype=None):
-        """The same of a tensor that has to be there."""
-        self._on_device(name, t, torch.float32 if dtype is None else dtype, shape)
-        if not t.is_contiguous():
-            raise ValueError(f"{name} must be contiguous")
+        """Data pointer of a contiguous tensor, fp32 unless told otherwise."""
+        if dtype is None:
+            dtype = torch.float32
+        if not (self._fits(t, dtype, shape) and t.is_contiguous()):
+            self._refuse(name, t, dtype, shape)
         return t.data_ptr()
+
+    def dense(self, name, t, shape, dtype=None):
+        """The same of a tensor that may be left out; None for None."""
+        return None if t is None else self.need(name, t, shape, dtype)
 
     def rows(self, name, t, shape, width):
         """(data pointer, elements between rows) of an activation whose last dims (`width` elements) are
         contiguous and whose leading dims are one run of evenly spaced rows."""
-        self._on_device(name, t, self.io, shape)
+        if not self._fits(t, self.io, shape):
+            self._refuse(name, t, self.io, shape)
         if t.is_contiguous():
             return t.data_ptr(), width
         sizes, strides = t.shape, t.stride()
@@ -74,16 +84,19 @@ class _Call:
         return t.data_ptr(), step
 
     def empty(self, shape, dtype):
-        with torch.cuda.stream(self.stream):  # (no change for None)
+        if self.stream is None:
+            return torch.empty(shape, dtype=dtype, device=self.device)
+        with torch.cuda.stream(self.stream):
             return torch.empty(shape, dtype=dtype, device=self.device)
 
     def output(self, name, t, shape, dtype=None):
         """(tensor, pointer) of an output, allocated if it was not passed in."""
-        dtype = self.io if dtype is None else dtype
+        if dtype is None:
+            dtype = self.io
         if t is None:
             t = self.empty(shape, dtype)
             return t, t.data_ptr()
-        return t, self.dense(name, t, shape, dtype)
+        return t, self.need(name, t, shape, dtype)
 
     def workspace(self, t, need):
         """(tensor, pointer, bytes)."""
@@ -96,20 +109,19 @@ class _Call:
         return t, t.data_ptr(), t.numel() * t.element_size()
 
     def lengths(self, t, B):
-        return self.dense("lengths", t, (B,), torch.int32)
+        return None if t is None else self.need("lengths", t, (B,), torch.int32)
 
     def run(self, fn_name, *args):
         fn = getattr(load_library(), fn_name)
-        if self.device.index == torch.cuda.current_device():
-            st = fn(*args, self._handle())
+        index = self.device.index
+        s = torch.cuda.current_stream(index) if self.stream is None else self.stream
+        if index == torch.cuda.current_device():
+            st = fn(*args, s.cuda_stream)
         else:
-            with torch.cuda.device(self.device):
-                st = fn(*args, self._handle())
-        _raise(st, fn_name)
-
-    def _handle(self):
-        s = torch.cuda.current_stream(self.device) if self.stream is None else self.stream
-        return s.cuda_stream
+            with torch.cuda.device(index):
+                st = fn(*args, s.cuda_stream)
+        if st:
+            _raise(st, fn_name)
 
 
 # ---------------------------------------------------------------------------------- layer norm
