@@ -12,6 +12,8 @@
 // the states stays inside the lane, and every access of u, delta, z and y is a contiguous run over
 // channels. What bounds it is the vector ALU: one exponential (quarter rate) and four multiplies or
 // multiply-adds per state and token.
+#include <type_traits>
+
 #include "internal.hpp"
 #include "rowops.hpp"
 #include "seq.hpp"
@@ -20,7 +22,8 @@ namespace ttt {
 namespace {
 
 constexpr int kWaves = 4;   // units per workgroup (forward)
-constexpr int kTok = 4;     // tokens loaded ahead
+constexpr int kTokens = 2;  // tokens loaded ahead (4: 4 % slower, 8: 7 %; more registers, fewer waves)
+constexpr float kLn2 = 0.693147180559945309417f;
 
 // log(1 + exp(x)) with e = exp(-|x|): max(x, 0) + log1p(e), and log1p(e) = 2 atanh(e / (2 + e)) by
 // its series in odd powers of s = e / (2 + e) <= 1/3. The terms left out are below 9^-8 / 17 = 1.4e-9
@@ -41,20 +44,19 @@ __device__ __forceinline__ float softplus_of(float x, float& e) {
 // The step and its derivative by delta.
 __device__ __forceinline__ float step_of(float raw, int softplus) {
   float e;
-  return softplus ? softplus_of(raw, e) : raw;
+  const float dt = softplus_of(raw, e);  // (chosen, not branched to: a branch would part the tokens of a chunk)
+  return softplus ? dt : raw;
 }
 __device__ __forceinline__ float step_grad_of(float raw, int softplus, float& grad) {
-  if (!softplus) {
-    grad = 1.f;
-    return raw;
-  }
   float e;
   const float dt = softplus_of(raw, e);
-  grad = (raw >= 0.f ? 1.f : e) * rcp_hw(1.f + e);
-  return dt;
+  grad = softplus ? (raw >= 0.f ? 1.f : e) * rcp_hw(1.f + e) : 1.f;
+  return softplus ? dt : raw;
 }
 
-// S values of a row of B or C that is the same for the whole wave, by scalar loads.
+// S values of a row of B or C that is the same for the whole wave, by scalar loads. (Holding one row ahead
+// in SGPRs instead was slower: 259 against 247 us for the forward pass at 4 x 8192 x 768 x 16, bf16; the
+// other waves of a SIMD cover the wait.)
 typedef const __attribute__((address_space(4))) uint32_t* ScalarPtr;
 template <class T, int S>
 __device__ __forceinline__ void load_uniform(const T* p, float* out) {
@@ -70,6 +72,17 @@ __device__ __forceinline__ void load_uniform(const T* p, float* out) {
 #pragma unroll
     for (int i = 0; i < S; ++i) out[i] = __uint_as_float(q[i]);
   }
+}
+
+// Channel c of a row that is the same for the whole wave: the row's address stays in SGPRs and the lane's
+// part of it is 32 bits.
+template <class T>
+__device__ __forceinline__ float at(const T* row, int c) {
+  return (float)*reinterpret_cast<const T*>(reinterpret_cast<const char*>(row) + (uint32_t)c * (uint32_t)sizeof(T));
+}
+template <class T>
+__device__ __forceinline__ void put(T* row, int c, float v) {
+  *reinterpret_cast<T*>(reinterpret_cast<char*>(row) + (uint32_t)c * (uint32_t)sizeof(T)) = (T)v;
 }
 
 // How a call is cut up. Channel blocks: 64 channels of one group each.
@@ -105,6 +118,7 @@ __device__ __forceinline__ int length_of(const int* lengths, int b, int N) {
 template <class T, int S, bool FINAL>
 __global__ __launch_bounds__(64 * kWaves) void scan_fwd(ScanArgs a, Plan p, int units, float* __restrict__ ends,
                                                         float* __restrict__ sums) {
+  constexpr int kTok = S <= 16 ? kTokens : S == 32 ? 2 : 1;  // (wide states leave no registers for more)
   const int id = blockIdx.x * kWaves + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   if (id >= units) return;
   const Unit un = unit_of(id, p, a.C, a.G);
@@ -112,67 +126,93 @@ __global__ __launch_bounds__(64 * kWaves) void scan_fwd(ScanArgs a, Plan p, int 
   const int n = length_of(a.lengths, un.b, N);
   const int t0 = un.seg * p.T, t1 = min(N, t0 + p.T), te = min(t1, n);
   const long long row0 = (long long)un.b * N;
-  const T* u = (const T*)a.u + row0 * a.us + c;
-  const T* de = (const T*)a.delta + row0 * a.ds + c;
-  const T* z = a.z ? (const T*)a.z + row0 * a.zs + c : nullptr;
+  const T* u = (const T*)a.u + row0 * a.us;
+  const T* de = (const T*)a.delta + row0 * a.ds;
   const T* bm = (const T*)a.bm + row0 * a.bs + (long long)un.g * S;
   const T* cm = (const T*)a.cm + row0 * a.cs + (long long)un.g * S;
-  T* y = (T*)a.y + row0 * C + c;
+  T* y = (T*)a.y + row0 * C;
   const long long seg_at = ((long long)un.b * p.nseg + un.seg) * C;
 
   float A2[S], h[S];
   for (int s = 0; s < S; ++s) A2[s] = a.A[(long long)c * S + s] * kLog2e;
-  for (int s = 0; s < S; ++s) {
-    if (FINAL && p.nseg > 1) h[s] = ends[seg_at * S + (long long)s * C + c];
-    else if (FINAL && a.h0) h[s] = a.h0[((long long)un.b * C + c) * S + s];
-    else h[s] = 0.f;
+  if (FINAL && p.nseg > 1) {
+    for (int s = 0; s < S; ++s) h[s] = ends[seg_at * S + (long long)s * C + c];
+  } else if (FINAL && a.h0) {
+    for (int s = 0; s < S; ++s) h[s] = a.h0[((long long)un.b * C + c) * S + s];
+  } else {
+    for (int s = 0; s < S; ++s) h[s] = 0.f;
   }
   const float db = a.dbias ? a.dbias[c] : 0.f, D = FINAL && a.D ? a.D[c] : 0.f;
   float sum = 0.f;
-  const bool gate = FINAL && z;
-  // The next kTok tokens' rows are loaded before this kTok are worked on (past the end: the last row again).
+  // The next kTok tokens' rows are loaded before this kTok are worked on (past the end: the last row
+  // again), without a branch: behind one the loads would be waited for where it ends. Without a gate
+  // u's row stands in for z's.
+  const bool gate = FINAL && a.z;
+  const T* z = gate ? (const T*)a.z + row0 * a.zs : u;
+  const long long zs = gate ? a.zs : a.us;
   float nu[kTok], nd[kTok], nz[kTok];
   auto fetch = [&](int t) {
 #pragma unroll
     for (int j = 0; j < kTok; ++j) {
       const long long tt = min(t + j, te - 1);
-      nu[j] = (float)u[tt * a.us];
-      nd[j] = (float)de[tt * a.ds];
-      nz[j] = gate ? (float)z[tt * a.zs] : 0.f;
+      nu[j] = at(u + tt * a.us, c);
+      nd[j] = at(de + tt * a.ds, c);
+      if (FINAL) nz[j] = at(z + tt * zs, c);
     }
   };
-  if (t0 < te) fetch(t0);
-  for (int t = t0; t < te; t += kTok) {
-    float cu[kTok], cd[kTok], cz[kTok];
+  constexpr int SB = S < 16 ? S : 16;  // states per piece of B and C
+  // kTok tokens from t on (all there when FULL). Lanes past their group repeat its block's first channel
+  // in everything, stores too, so that the stores need no branch either: a load behind a store that may
+  // or may not be there is waited for together with it.
+  auto chunk = [&](int t, auto full) {
+    constexpr bool FULL = decltype(full)::value;
+    float cu[kTok], dt[kTok], cz[kTok], out[kTok];
 #pragma unroll
-    for (int j = 0; j < kTok; ++j) cu[j] = nu[j], cd[j] = nd[j], cz[j] = nz[j];
+    for (int j = 0; j < kTok; ++j) {
+      cu[j] = nu[j];
+      if (FINAL) cz[j] = nz[j];
+      dt[j] = step_of(nd[j] + db, a.softplus);
+    }
     fetch(t + kTok);
 #pragma unroll
     for (int j = 0; j < kTok; ++j) {
-      if (t + j < te) {
-        float bv[S], cv[S];
-        load_uniform<T, S>(bm + (long long)(t + j) * a.bs, bv);
-        if (FINAL) load_uniform<T, S>(cm + (long long)(t + j) * a.cs, cv);
-        const float dt = step_of(cd[j] + db, a.softplus), dtu = dt * cu[j];
-        float out = 0.f;
+      if (FULL || t + j < te) {
+        const float dtu = dt[j] * cu[j];
+        float o0 = 0.f, o1 = 0.f;
 #pragma unroll
-        for (int s = 0; s < S; ++s) {
-          h[s] = fmaf(exp2_hw(dt * A2[s]), h[s], dtu * bv[s]);
-          if (FINAL) out = fmaf(cv[s], h[s], out);
+        for (int s0 = 0; s0 < S; s0 += SB) {
+          float bv[SB], cv[SB];
+          load_uniform<T, SB>(bm + (t + j) * a.bs + s0, bv);
+          if (FINAL) load_uniform<T, SB>(cm + (t + j) * a.cs + s0, cv);
+#pragma unroll
+          for (int s = 0; s < SB; ++s) {
+            float& x = h[s0 + s];
+            x = fmaf(exp2_hw(dt[j] * A2[s0 + s]), x, dtu * bv[s]);
+            if (FINAL) {
+              float& o = s & 1 ? o1 : o0;
+              o = fmaf(cv[s], x, o);
+            }
+          }
         }
-        if (FINAL) {
-          out = fmaf(D, cu[j], out);
-          if (gate) out *= cz[j] * sigmoid(cz[j]);
-          if (un.live) y[(long long)(t + j) * C] = (T)out;
-        } else {
-          sum += dt;
-        }
+        out[j] = o0 + o1;
+        if (!FINAL) sum += dt[j];
       }
     }
-  }
-  if (!un.live) return;
+    if (FINAL) {
+#pragma unroll
+      for (int j = 0; j < kTok; ++j) {
+        float o = fmaf(D, cu[j], out[j]);
+        o = gate ? o * (cz[j] * sigmoid(cz[j])) : o;
+        if (FULL || t + j < te) put(y + (long long)(t + j) * C, c, o);
+      }
+    }
+  };
+  if (t0 < te) fetch(t0);
+  int t = t0;
+  for (; t + kTok <= te; t += kTok) chunk(t, std::true_type{});
+  if (t < te) chunk(t, std::false_type{});
   if (FINAL) {
-    for (int t = max(t0, te); t < t1; ++t) y[(long long)t * C] = (T)0.f;
+    for (int t = max(t0, te); t < t1; ++t) put(y + (long long)t * C, c, 0.f);
     if (a.h_out && un.seg == p.nseg - 1)
       for (int s = 0; s < S; ++s) a.h_out[((long long)un.b * C + c) * S + s] = h[s];
   } else {
@@ -184,35 +224,46 @@ __global__ __launch_bounds__(64 * kWaves) void scan_fwd(ScanArgs a, Plan p, int 
 // Folds the segments in order: ends[seg] becomes the segment's start state. One thread per (b, s, c).
 // For the backward pass back (same layout) holds the segments' own contributions to a_0 q_0 of their
 // first token, and becomes what flows into each segment from behind it; dh0 receives the first's.
-__global__ __launch_bounds__(256) void scan_fold(const float* __restrict__ A, const float* __restrict__ h0,
-                                                 float* __restrict__ ends, float* __restrict__ back,
-                                                 const float* __restrict__ sums, float* __restrict__ dh0,
-                                                 int C, int S, int nseg) {
-  const long long id = (long long)blockIdx.x * 256 + threadIdx.x;
-  if (id >= (long long)C * S) return;
-  const int s = (int)(id / C), c = (int)(id - (long long)s * C), b = blockIdx.y;
+constexpr int kFoldThreads = 64;  // (single waves: they spread over all CUs)
+__global__ __launch_bounds__(kFoldThreads) void scan_fold(const float* __restrict__ A, const float* __restrict__ h0,
+                                                          float* __restrict__ ends, float* __restrict__ back,
+                                                          const float* __restrict__ sums, float* __restrict__ dh0,
+                                                          int C, int S, int nseg) {
+  const int id = blockIdx.x * kFoldThreads + threadIdx.x;
+  if (id >= C * S) return;
+  const int s = id / C, c = id - s * C, b = blockIdx.y;
   const float A2 = A[(long long)c * S + s] * kLog2e;
-  const long long hat = ((long long)b * C + c) * S + s;
-  float* e = ends + (long long)b * nseg * S * C + id;
+  const long long hat = ((long long)b * C + c) * S + s, step = (long long)S * C;
+  const bool rev = blockIdx.z != 0;
+  float* f = (rev ? back : ends) + (long long)b * nseg * step + id;
   const float* dts = sums + (long long)b * nseg * C + c;
-  const long long step = (long long)S * C;
-  if (blockIdx.z == 0) {
-    float h = h0 ? h0[hat] : 0.f;
-    for (int i = 0; i < nseg; ++i) {
-      const float own = e[i * step];
-      e[i * step] = h;
-      h = fmaf(exp2_hw(A2 * dts[(long long)i * C]), h, own);
+  float x = !rev && h0 ? h0[hat] : 0.f;
+  // kFold segments' pairs are loaded while the chain goes through the kFold before them.
+  constexpr int kFold = 32;
+  float own[kFold], dec[kFold];
+  auto fetch = [&](int i0) {
+#pragma unroll
+    for (int i = 0; i < kFold; ++i) {
+      const int k = min(i0 + i, nseg - 1);
+      const long long seg = rev ? nseg - 1 - k : k;
+      own[i] = f[seg * step];
+      dec[i] = dts[seg * C];
     }
-  } else {
-    float* f = back + (long long)b * nseg * S * C + id;
-    float q = 0.f;
-    for (int i = nseg - 1; i >= 0; --i) {
-      const float own = f[i * step];
-      f[i * step] = q;
-      q = fmaf(exp2_hw(A2 * dts[(long long)i * C]), q, own);
-    }
-    if (dh0) dh0[hat] = q;
+  };
+  fetch(0);
+  for (int i0 = 0; i0 < nseg; i0 += kFold) {
+    float o[kFold], d[kFold];
+#pragma unroll
+    for (int i = 0; i < kFold; ++i) o[i] = own[i], d[i] = exp2_hw(A2 * dec[i]);
+    if (i0 + kFold < nseg) fetch(i0 + kFold);
+#pragma unroll
+    for (int i = 0; i < kFold; ++i)
+      if (i0 + i < nseg) {
+        f[(rev ? nseg - 1 - i0 - i : i0 + i) * step] = x;
+        x = fmaf(d[i], x, o[i]);
+      }
   }
+  if (rev && dh0) dh0[hat] = x;
 }
 
 // One token: S / 4 lanes per channel, four states each (one 16-byte access of the state).
@@ -265,15 +316,15 @@ __global__ __launch_bounds__(256) void scan_step(ScanArgs a) {
 // last to its first: it forms the sub-chunk's a and h in registers from the checkpoint (one more
 // exponential per state and token) and walks back through them.
 
-// Tokens per sub-chunk, states per wave and waves of a scan_bwd workgroup: kSub * SW = 64 values of
-// each of a and h stay in a lane's registers.
+// Tokens per sub-chunk, states per wave and waves of a scan_bwd workgroup: kSub * SW values of each of a
+// and h stay in a lane's registers.
 template <int S>
 struct Bwd {
   static constexpr int SW = S == 64 ? 8 : 4;
   static constexpr int NW = S / SW;
-  static constexpr int kSub = 64 / SW;
+  static constexpr int kSub = 8;
 };
-int bwd_sub(int S) { return S == 64 ? 8 : 16; }
+constexpr int kBwdSub = 8;
 
 // Buffers in the workspace.
 struct BwdBufs {
@@ -289,7 +340,7 @@ struct BwdBufs {
 
 template <class T, int S, int SB>
 __global__ __launch_bounds__(64 * kWaves) void scan_bwd_ends(ScanArgs a, Plan p, int units, BwdBufs w) {
-  constexpr int kSub = Bwd<S>::kSub;
+  constexpr int kSub = Bwd<S>::kSub, kTok = kTokens;
   int id = blockIdx.x * kWaves + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   if (id >= units) return;
   constexpr int NB = S / SB;  // state blocks, one per wave
@@ -299,10 +350,12 @@ __global__ __launch_bounds__(64 * kWaves) void scan_bwd_ends(ScanArgs a, Plan p,
   const int n = length_of(a.lengths, un.b, N);
   const int t0 = un.seg * p.T, t1 = min(N, t0 + p.T), te = min(t1, n);
   const long long row0 = (long long)un.b * N;
-  const T* u = (const T*)a.u + row0 * a.us + c;
-  const T* de = (const T*)a.delta + row0 * a.ds + c;
-  const T* z = a.z ? (const T*)a.z + row0 * a.zs + c : nullptr;
-  const T* dy = (const T*)a.dy + row0 * C + c;
+  const T* u = (const T*)a.u + row0 * a.us;
+  const T* de = (const T*)a.delta + row0 * a.ds;
+  const bool gate = a.z;
+  const T* z = gate ? (const T*)a.z + row0 * a.zs : u;
+  const long long zs = gate ? a.zs : a.us;
+  const T* dy = (const T*)a.dy + row0 * C;
   const T* bm = (const T*)a.bm + row0 * a.bs + (long long)un.g * S + s0;
   const T* cm = (const T*)a.cm + row0 * a.cs + (long long)un.g * S + s0;
   float A2[SB], h[SB], P[SB], q[SB];
@@ -313,34 +366,62 @@ __global__ __launch_bounds__(64 * kWaves) void scan_bwd_ends(ScanArgs a, Plan p,
   }
   const float db = a.dbias ? a.dbias[c] : 0.f;
   float sum = 0.f;
-  for (int t = t0; t < t1; ++t) {
-    if ((t - t0) % kSub == 0 && un.live) {
-      const long long k = (long long)un.b * w.nsub + t / kSub;
-      for (int s = 0; s < SB; ++s) w.ck[(k * S + s0 + s) * C + c] = h[s];
-      if (s0 == 0) w.cksum[k * C + c] = sum;
-    }
-    if (t < te) {
-      float bv[SB], cv[SB];
-      load_uniform<T, SB>(bm + (long long)t * a.bs, bv);
-      load_uniform<T, SB>(cm + (long long)t * a.cs, cv);
-      const float dt = step_of((float)de[(long long)t * a.ds] + db, a.softplus);
-      const float dtu = dt * (float)u[(long long)t * a.us];
-      float v = (float)dy[(long long)t * C];
-      if (z) {
-        const float zz = (float)z[(long long)t * a.zs];
-        v *= zz * sigmoid(zz);
-      }
-      sum += dt;
+  auto checkpoint = [&](int t) {
+    const long long k = (long long)un.b * w.nsub + t / kSub;
+    for (int s = 0; s < SB; ++s) w.ck[(k * S + s0 + s) * C + c] = h[s];
+    if (s0 == 0) w.cksum[k * C + c] = sum;
+  };
+  float nu[kTok], nd[kTok], nv[kTok], nz[kTok];
+  auto fetch = [&](int t) {
 #pragma unroll
-      for (int s = 0; s < SB; ++s) {
-        const float e = exp2_hw(dt * A2[s]);
-        h[s] = fmaf(e, h[s], dtu * bv[s]);
-        P[s] *= e;
-        q[s] = fmaf(P[s], v * cv[s], q[s]);
+    for (int j = 0; j < kTok; ++j) {
+      const long long tt = min(t + j, te - 1);
+      nu[j] = at(u + tt * a.us, c);
+      nd[j] = at(de + tt * a.ds, c);
+      nv[j] = at(dy + tt * C, c);
+      nz[j] = at(z + tt * zs, c);
+    }
+  };
+  auto chunk = [&](int t, auto full) {
+    constexpr bool FULL = decltype(full)::value;
+    float dtu[kTok], dt[kTok], v[kTok];
+#pragma unroll
+    for (int j = 0; j < kTok; ++j) {
+      dt[j] = step_of(nd[j] + db, a.softplus);
+      dtu[j] = dt[j] * nu[j];
+      v[j] = gate ? nv[j] * (nz[j] * sigmoid(nz[j])) : nv[j];
+    }
+    fetch(t + kTok);
+#pragma unroll
+    for (int j = 0; j < kTok; ++j) {
+      if (FULL || t + j < te) {
+        float bv[SB], cv[SB];
+        load_uniform<T, SB>(bm + (t + j) * a.bs, bv);
+        load_uniform<T, SB>(cm + (t + j) * a.cs, cv);
+#pragma unroll
+        for (int s = 0; s < SB; ++s) {
+          const float e = exp2_hw(dt[j] * A2[s]);
+          h[s] = fmaf(e, h[s], dtu[j] * bv[s]);
+          P[s] *= e;
+          q[s] = fmaf(P[s], v[j] * cv[s], q[s]);
+        }
+        sum += dt[j];
       }
     }
+  };
+  // A sub-chunk is kSub / kTok chunks; its checkpoint is written before the loads that are in flight are
+  // used.
+  if (t0 < te) fetch(t0);
+  int t = t0;
+  for (; t + kSub <= te; t += kSub) {
+    checkpoint(t);
+#pragma unroll
+    for (int i = 0; i < kSub; i += kTok) chunk(t + i, std::true_type{});
   }
-  if (!un.live) return;
+  if (t < te) checkpoint(t);
+  for (; t < te; t += kTok) chunk(t, std::false_type{});
+  // (the sub-chunks behind the sequence start from its end)
+  for (t = t0 + (max(te - t0, 0) + kSub - 1) / kSub * kSub; t < t1; t += kSub) checkpoint(t);
   const long long seg = (long long)un.b * p.nseg + un.seg;
   for (int s = 0; s < SB; ++s) {
     w.ends[(seg * S + s0 + s) * C + c] = h[s];
@@ -349,144 +430,193 @@ __global__ __launch_bounds__(64 * kWaves) void scan_bwd_ends(ScanArgs a, Plan p,
   if (s0 == 0) w.sums[seg * C + c] = sum;
 }
 
-// Sums 64 values over the 64 lanes: lane l gets the total of v[l]. Each step halves the values and the
-// lanes that hold a part of each: 32 and 16 by swaps of register halves, the rest within 16 lanes.
-__device__ __forceinline__ float lanes_scatter_sum(float* v) {
-#pragma unroll
-  for (int i = 0; i < 32; ++i) {
-    const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v[i]), __float_as_uint(v[i + 32]), false, false);
-    v[i] = __uint_as_float(r[0]) + __uint_as_float(r[1]);
+// Sums over the 64 lanes, halving the values and the lanes that hold a part of each at every step: joined
+// over lane bit M, lanes with that bit clear go on with x and the others with y. Bits 5 and 4 by swaps
+// of register halves, the rest within 16 lanes.
+template <int M>
+__device__ __forceinline__ float join_over(float x, float y) {
+  if constexpr (M == 32) {
+    const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(y), false, false);
+    return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+  } else if constexpr (M == 16) {
+    const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(y), false, false);
+    return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+  } else {
+    const bool up = lane_id() & M;
+    constexpr int ctrl = M == 8 ? kDppRor8 : M == 4 ? kDppMirror8 : M == 2 ? kDppXor2 : kDppXor1;
+    return (up ? y : x) + dpp<ctrl>(up ? x : y);
   }
+}
+template <int M, int NV>
+__device__ __forceinline__ void join_all(float* x, const float* y) {
 #pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(v[i]), __float_as_uint(v[i + 16]), false, false);
-    v[i] = __uint_as_float(r[0]) + __uint_as_float(r[1]);
-  }
-  const int l = lane_id();
+  for (int i = 0; i < NV; ++i) x[i] = join_over<M>(x[i], y[i]);
+}
+// x[0 .. N) -> the total of x[l % N] in lane l, when the sums over the lane bits from N on are done.
+template <int N>
+__device__ __forceinline__ float join_within(float* x) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i) v[i] = (l & 8 ? v[i + 8] : v[i]) + dpp<kDppRor8>(l & 8 ? v[i] : v[i + 8]);
-#pragma unroll
-  for (int i = 0; i < 4; ++i) v[i] = (l & 4 ? v[i + 4] : v[i]) + dpp<kDppMirror8>(l & 4 ? v[i] : v[i + 4]);
-#pragma unroll
-  for (int i = 0; i < 2; ++i) v[i] = (l & 2 ? v[i + 2] : v[i]) + dpp<kDppXor2>(l & 2 ? v[i] : v[i + 2]);
-  return (l & 1 ? v[1] : v[0]) + dpp<kDppXor1>(l & 1 ? v[0] : v[1]);
+  for (int i = 0; i < N / 2; ++i) x[i] = join_over<N / 2>(x[i], x[i + N / 2]);
+  if constexpr (N > 2) return join_within<N / 2>(x);
+  return x[0];
 }
 
 // One workgroup per (b, segment, channel block), NW waves with SW states each of the same 64 channels.
 // A sub-chunk's per-channel values (dt, dt u, v) are formed once, a share of the tokens per wave, and
-// passed through LDS; each wave's sums over its states come back the same way.
+// passed through LDS with its rows of B and C; each wave's sums over its states come back the same
+// way. Tokens behind the sequence are passed over as tokens of no step and no gradient.
 template <class T, int S>
 __global__ __launch_bounds__(64 * Bwd<S>::NW) void scan_bwd(ScanArgs a, Plan p, BwdBufs w) {
-  constexpr int SW = Bwd<S>::SW, NW = Bwd<S>::NW, kSub = Bwd<S>::kSub;
+  constexpr int SW = Bwd<S>::SW, NW = Bwd<S>::NW, kSub = Bwd<S>::kSub, kThreads = 64 * NW;
   constexpr int TW = kSub / NW;          // tokens a wave prepares and finishes
-  constexpr int RB = 64 / (2 * SW);      // tokens whose dB and dC sums fill the 64 lanes
+  constexpr int NV = 2 * SW;             // sums for dB and dC per token
+  constexpr int RB = 64 / NV;            // tokens whose sums fill the 64 lanes
+  constexpr int EW = (kSub * S + kThreads - 1) / kThreads;  // elements of B a thread passes on
   static_assert(kSub % NW == 0 && kSub % RB == 0, "sub-chunk shares");
   __shared__ float s_dt[kSub][64], s_dtu[kSub][64], s_v[kSub][64];
   __shared__ float s_y[NW][kSub][64], s_q[NW][kSub][64], s_r[NW][kSub][64];
+  __shared__ __align__(16) float s_b[kSub][S], s_c[kSub][S];
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), l = lane_id();
   const Unit un = unit_of(blockIdx.x, p, a.C, a.G);
   const int C = a.C, N = a.N, c = un.c, s0 = wave * SW;
   const int n = length_of(a.lengths, un.b, N);
-  const int t0 = un.seg * p.T, t1 = min(N, t0 + p.T);
+  const int t0 = un.seg * p.T, t1 = min(N, t0 + p.T), te = min(t1, n);
   const long long row0 = (long long)un.b * N;
-  const T* u = (const T*)a.u + row0 * a.us + c;
-  const T* de = (const T*)a.delta + row0 * a.ds + c;
-  const T* z = a.z ? (const T*)a.z + row0 * a.zs + c : nullptr;
-  const T* dy = (const T*)a.dy + row0 * C + c;
-  const T* bm = (const T*)a.bm + row0 * a.bs + (long long)un.g * S + s0;
-  const T* cm = (const T*)a.cm + row0 * a.cs + (long long)un.g * S + s0;
+  const T* u = (const T*)a.u + row0 * a.us;
+  const T* de = (const T*)a.delta + row0 * a.ds;
+  const bool gate = a.z;
+  const T* z = gate ? (const T*)a.z + row0 * a.zs : u;
+  const long long zs = gate ? a.zs : a.us;
+  const T* dy = (const T*)a.dy + row0 * C;
+  const T* bm = (const T*)a.bm + row0 * a.bs + (long long)un.g * S;
+  const T* cm = (const T*)a.cm + row0 * a.cs + (long long)un.g * S;
   const long long seg = (long long)un.b * p.nseg + un.seg;
-  float A[SW], A2[SW], hs[SW], q[SW], dA[SW];
+  float A2[SW], hs[SW], q[SW], dA[SW];
   for (int s = 0; s < SW; ++s) {
-    A[s] = a.A[(long long)c * S + s0 + s];
-    A2[s] = A[s] * kLog2e;
-    hs[s] = w.ends[(seg * S + s0 + s) * C + c];
-    q[s] = w.back[(seg * S + s0 + s) * C + c];  // a q of the token behind
+    A2[s] = a.A[(long long)c * S + s0 + s] * kLog2e;
+    hs[s] = at(w.ends + (seg * S + s0 + s) * C, c);
+    q[s] = at(w.back + (seg * S + s0 + s) * C, c);  // a q of the token behind
     dA[s] = 0.f;
   }
   const float db = a.dbias ? a.dbias[c] : 0.f, D = a.D ? a.D[c] : 0.f;
   float dD = 0.f, ddb = 0.f;
-  for (int tc = t0 + (t1 - 1 - t0) / kSub * kSub; tc >= t0; tc -= kSub) {
-    float pu[TW], pv[TW], pg[TW], pz[TW], pdy[TW], pdt[TW];
+  // A sub-chunk's inputs, loaded while the one behind it is worked on, without a branch (past the
+  // segment: its last row again); what is no token's is zeroed when it is used.
+  float nu[TW], nd[TW], nv[TW], nz[TW], nb[EW], nc[EW], nck[SW], npast;
+  auto fetch = [&](int tc) {
 #pragma unroll
     for (int j = 0; j < TW; ++j) {
-      const int i = wave * TW + j, t = tc + i;
-      pu[j] = pv[j] = pg[j] = pz[j] = pdy[j] = pdt[j] = 0.f;
-      if (t < n && t < t1 && un.live) {
-        pu[j] = (float)u[(long long)t * a.us];
-        pdt[j] = step_grad_of((float)de[(long long)t * a.ds] + db, a.softplus, pg[j]);
-        pdy[j] = (float)dy[(long long)t * C];
-        pv[j] = pdy[j];
-        if (z) {
-          pz[j] = (float)z[(long long)t * a.zs];
-          pv[j] *= pz[j] * sigmoid(pz[j]);
-        }
-      }
+      const long long t = min(tc + wave * TW + j, t1 - 1);
+      nu[j] = at(u + t * a.us, c);
+      nd[j] = at(de + t * a.ds, c);
+      nv[j] = at(dy + t * C, c);
+      nz[j] = at(z + t * zs, c);
+    }
+#pragma unroll
+    for (int i = 0; i < EW; ++i) {
+      const int e = threadIdx.x + i * kThreads;
+      const long long t = min(tc + e / S, t1 - 1);
+      nb[i] = (float)bm[t * a.bs + e % S];
+      nc[i] = (float)cm[t * a.cs + e % S];
+    }
+    const long long k = (long long)un.b * w.nsub + tc / kSub;
+    npast = at(w.cksum + k * C, c);
+    for (int s = 0; s < SW; ++s) nck[s] = at(w.ck + (k * S + s0 + s) * C, c);
+  };
+  // Where the lane's sum over the channels goes: its token of the RB and its place in that token's row.
+  const int tok = (l >> 5 & 1) | (l >> 4 & 1) << 1 | (RB == 8 ? (l >> 3 & 1) << 2 : 0), k = l % NV;
+  const int mat_at = tok * p.cb * 2 * S + (k / SW) * S + s0 + k % SW;
+  const int last = t0 + (t1 - 1 - t0) / kSub * kSub;
+  fetch(last);
+  for (int tc = last; tc >= t0; tc -= kSub) {
+    float pu[TW], pv[TW], pg[TW], pz[TW], pdy[TW], pdt[TW], h0[SW];
+#pragma unroll
+    for (int j = 0; j < TW; ++j) {
+      const int i = wave * TW + j;
+      const bool in = tc + i < te && un.live;
+      pu[j] = in ? nu[j] : 0.f;
+      pz[j] = nz[j];
+      pdy[j] = in ? nv[j] : 0.f;
+      pdt[j] = step_grad_of(nd[j] + db, a.softplus, pg[j]);
+      if (!in) pdt[j] = 0.f;
+      pv[j] = gate && in ? pdy[j] * (pz[j] * sigmoid(pz[j])) : pdy[j];
       s_dt[i][l] = pdt[j];
       s_dtu[i][l] = pdt[j] * pu[j];
       s_v[i][l] = pv[j];
     }
-    __syncthreads();
-    const int te = min(t1, n) - tc;  // tokens of this sub-chunk (uniform)
-    float h0[SW], e[kSub][SW], h[kSub][SW];
-    {
-      const long long k = (long long)un.b * w.nsub + tc / kSub;
-      const float past = w.cksum[k * C + c];
-      for (int s = 0; s < SW; ++s)
-        h0[s] = fmaf(exp2_hw(A2[s] * past), hs[s], w.ck[(k * S + s0 + s) * C + c]);
+#pragma unroll
+    for (int i = 0; i < EW; ++i) {
+      const int e = threadIdx.x + i * kThreads;
+      const bool in = tc + e / S < te;
+      if (kSub * S % kThreads == 0 || e < kSub * S) {
+        (&s_b[0][0])[e] = in ? nb[i] : 0.f;
+        (&s_c[0][0])[e] = in ? nc[i] : 0.f;
+      }
     }
+    for (int s = 0; s < SW; ++s) h0[s] = fmaf(exp2_hw(A2[s] * npast), hs[s], nck[s]);
+    __syncthreads();
+    if (tc > t0) fetch(tc - kSub);
+    float e[kSub][SW], h[kSub][SW];
 #pragma unroll
     for (int j = 0; j < kSub; ++j) {
-      if (j < te) {
-        float bv[SW], cv[SW];
-        load_uniform<T, SW>(bm + (long long)(tc + j) * a.bs, bv);
-        load_uniform<T, SW>(cm + (long long)(tc + j) * a.cs, cv);
-        const float dt = s_dt[j][l], dtu = s_dtu[j][l];
-        float y = 0.f;
+      float bv[SW], cv[SW];
+      load_params<SW>(&s_b[j][s0], bv);
+      load_params<SW>(&s_c[j][s0], cv);
+      const float dt = s_dt[j][l], dtu = s_dtu[j][l];
+      float y = 0.f;
 #pragma unroll
-        for (int s = 0; s < SW; ++s) {
-          e[j][s] = exp2_hw(dt * A2[s]);
-          h[j][s] = fmaf(e[j][s], j ? h[j ? j - 1 : 0][s] : h0[s], dtu * bv[s]);
-          y = fmaf(cv[s], h[j][s], y);
-        }
-        s_y[wave][j][l] = y;
+      for (int s = 0; s < SW; ++s) {
+        e[j][s] = exp2_hw(dt * A2[s]);
+        h[j][s] = fmaf(e[j][s], j ? h[j ? j - 1 : 0][s] : h0[s], dtu * bv[s]);
+        y = fmaf(cv[s], h[j][s], y);
       }
+      if (gate) s_y[wave][j][l] = y;
+      if (j & 1) __builtin_amdgcn_sched_barrier(0);
     }
 #pragma unroll
     for (int jb = kSub - RB; jb >= 0; jb -= RB) {
-      float val[64];
-#pragma unroll
-      for (int i = 0; i < 64; ++i) val[i] = 0.f;
+      // The sums over the channels are joined as the tokens come, so that few wait in registers.
+      float x[NV], l0[NV], l1[NV], l2[NV];
 #pragma unroll
       for (int jj = RB - 1; jj >= 0; --jj) {
         const int j = jb + jj;
-        if (j < te) {
-          float bv[SW], cv[SW];
-          load_uniform<T, SW>(bm + (long long)(tc + j) * a.bs, bv);
-          load_uniform<T, SW>(cm + (long long)(tc + j) * a.cs, cv);
-          const float dt = s_dt[j][l], dtu = s_dtu[j][l], v = s_v[j][l];
-          float qb = 0.f, r = 0.f;
+        float bv[SW], cv[SW];
+        load_params<SW>(&s_b[j][s0], bv);
+        load_params<SW>(&s_c[j][s0], cv);
+        const float dt = s_dt[j][l], dtu = s_dtu[j][l], v = s_v[j][l];
+        float qb = 0.f, r = 0.f;
 #pragma unroll
-          for (int s = 0; s < SW; ++s) {
-            q[s] = fmaf(v, cv[s], q[s]);
-            val[jj * 2 * SW + s] = q[s] * dtu;
-            val[jj * 2 * SW + SW + s] = v * h[j][s];
-            qb = fmaf(q[s], bv[s], qb);
-            q[s] *= e[j][s];
-            const float x = q[s] * (j ? h[j ? j - 1 : 0][s] : h0[s]);
-            r = fmaf(x, A[s], r);
-            dA[s] = fmaf(x, dt, dA[s]);
-          }
-          s_q[wave][j][l] = qb;
-          s_r[wave][j][l] = r;
+        for (int s = 0; s < SW; ++s) {
+          q[s] = fmaf(v, cv[s], q[s]);
+          x[s] = q[s] * dtu;
+          x[SW + s] = v * h[j][s];
+          qb = fmaf(q[s], bv[s], qb);
+          q[s] *= e[j][s];
+          const float g = q[s] * (j ? h[j ? j - 1 : 0][s] : h0[s]);
+          r = fmaf(g, A2[s], r);
+          dA[s] = fmaf(g, dt, dA[s]);
         }
+        s_q[wave][j][l] = qb;
+        s_r[wave][j][l] = r;
+        if (jj & 1) {
+          for (int i = 0; i < NV; ++i) l0[i] = x[i];
+        } else {
+          join_all<32, NV>(x, l0);
+          if (jj & 2) {
+            for (int i = 0; i < NV; ++i) l1[i] = x[i];
+          } else {
+            join_all<16, NV>(x, l1);
+            if (RB == 8 && (jj & 4)) {
+              for (int i = 0; i < NV; ++i) l2[i] = x[i];
+            } else if (RB == 8) {
+              join_all<8, NV>(x, l2);
+            }
+          }
+        }
+        __builtin_amdgcn_sched_barrier(0);
       }
-      if (tc + jb < t1) {  // (uniform)
-        const float total = lanes_scatter_sum(val);
-        const int t = tc + jb + l / (2 * SW), k = l % (2 * SW);
-        if (t < t1)
-          w.mats[((row0 + t) * p.cb + un.cb) * 2 * S + (k / SW) * S + s0 + k % SW] = total;
-      }
+      const float total = join_within<NV>(x);
+      if (tc + jb + tok < t1) put(w.mats + ((row0 + tc + jb) * p.cb + un.cb) * 2 * S, mat_at, total);
     }
     __syncthreads();
 #pragma unroll
@@ -496,20 +626,20 @@ __global__ __launch_bounds__(64 * Bwd<S>::NW) void scan_bwd(ScanArgs a, Plan p, 
         float du = 0.f, dd = 0.f, dz = 0.f;
         if (t < n) {
           float sq = 0.f, sr = 0.f, sy = 0.f;
-          for (int k = 0; k < NW; ++k) sq += s_q[k][i][l], sr += s_r[k][i][l], sy += s_y[k][i][l];
+          for (int k = 0; k < NW; ++k) sq += s_q[k][i][l], sr += s_r[k][i][l], sy += gate ? s_y[k][i][l] : 0.f;
           du = fmaf(sq, pdt[j], D * pv[j]);
-          dd = fmaf(sq, pu[j], sr) * pg[j];
+          dd = fmaf(sq, pu[j], sr * kLn2) * pg[j];  // (sr has A log2(e) for A)
           dD = fmaf(pv[j], pu[j], dD);
           ddb += dd;
-          if (z) {
+          if (gate) {
             const float sg = sigmoid(pz[j]);
             dz = pdy[j] * fmaf(D, pu[j], sy) * sg * fmaf(pz[j], 1.f - sg, 1.f);
           }
         }
-        const long long at = (row0 + t) * C + c;
-        ((T*)a.du)[at] = (T)du;
-        ((T*)a.ddelta)[at] = (T)dd;
-        if (z) ((T*)a.dz)[at] = (T)dz;
+        const long long row = (row0 + t) * C;
+        put((T*)a.du + row, c, du);
+        put((T*)a.ddelta + row, c, dd);
+        if (gate) put((T*)a.dz + row, c, dz);
       }
     }
   }
@@ -555,14 +685,13 @@ struct StoreScanGrads {
   }
 };
 
-// Segments: enough waves for four per SIMD (4096 on 256 CUs of four), but segments of at least
-// min_tokens, a multiple of `unit` tokens.
+// Segments: at most `want` waves in all and at least min_tokens each, a multiple of `unit` tokens.
 Plan plan_of(int B, int N, int C, int G, int want, int min_tokens, int unit) {
   Plan p;
   p.cbg = (C / G + 63) / 64;
   p.cb = p.cbg * G;
   const long long blocks = (long long)B * p.cb;
-  long long nseg = (want + blocks - 1) / blocks;
+  long long nseg = want / blocks;
   const long long most = (N + min_tokens - 1) / min_tokens;
   if (nseg > most) nseg = most;
   if (nseg < 1) nseg = 1;
@@ -571,18 +700,24 @@ Plan plan_of(int B, int N, int C, int G, int want, int min_tokens, int unit) {
   p.nseg = (int)((N + T - 1) / T);
   return p;
 }
+// Forward: as many waves as 256 CUs hold at once (six per SIMD at S = 16; 4 x 8192 x 768 x 16: 216 us, against 237
+// with five, 250 with four, 226 with eight, where the last ones run in a second turn), of at least
+// 24 tokens (3 x 1999 x 1000 x 32, fp32: 105 us; 117 at 16, 132 at 32). From 2048 blocks of channels on
+// (two waves per SIMD) a second run over the tokens costs more than the idle slots.
 Plan fwd_plan(const ScanArgs& a) {
   const int cb = (a.C / a.G + 63) / 64 * a.G;
-  if ((long long)a.B * cb >= 2048) return plan_of(a.B, a.N, a.C, a.G, 1, a.N, kTok);
-  return plan_of(a.B, a.N, a.C, a.G, 4096, 64, kTok);
+  if ((long long)a.B * cb >= 2048) return plan_of(a.B, a.N, a.C, a.G, 1, a.N, kTokens);
+  return plan_of(a.B, a.N, a.C, a.G, 6144, 24, kTokens);
 }
-Plan bwd_plan(const ScanArgs& a, int S) { return plan_of(a.B, a.N, a.C, a.G, 2048, 64, bwd_sub(S)); }
+// Backward: 2 x 4096 x 768 x 16 takes 198 us with 4096 waves of scan_bwd_ends, 245 with twice as many;
+// 2 x 333 x 193 x 8 28 us with segments of 16 tokens, 36 at 24, 43 at 32.
+Plan bwd_plan(const ScanArgs& a) { return plan_of(a.B, a.N, a.C, a.G, 4096, 16, kBwdSub); }
 
 size_t align_up(size_t x) { return (x + 255) / 256 * 256; }
 
 // Lays the backward's buffers out in the workspace; returns its size.
 size_t bwd_layout(const ScanArgs& a, int S, const Plan& p, char* ws, BwdBufs* w) {
-  w->nsub = (a.N + bwd_sub(S) - 1) / bwd_sub(S);
+  w->nsub = (a.N + kBwdSub - 1) / kBwdSub;
   size_t at = 0;
   auto take = [&](size_t floats) {
     float* r = reinterpret_cast<float*>(ws + at);
@@ -601,8 +736,8 @@ size_t bwd_layout(const ScanArgs& a, int S, const Plan& p, char* ws, BwdBufs* w)
 }
 
 hipError_t fold(const ScanArgs& a, int S, const Plan& p, float* ends, float* back, const float* sums, hipStream_t st) {
-  const dim3 grid((unsigned)(((long long)a.C * S + 255) / 256), (unsigned)a.B, back ? 2 : 1);
-  hipLaunchKernelGGL(scan_fold, grid, dim3(256), 0, st, a.A, a.h0, ends, back, sums, a.dh0, a.C, S, p.nseg);
+  const dim3 grid((unsigned)((a.C * S + kFoldThreads - 1) / kFoldThreads), (unsigned)a.B, back ? 2 : 1);
+  hipLaunchKernelGGL(scan_fold, grid, dim3(kFoldThreads), 0, st, a.A, a.h0, ends, back, sums, a.dh0, a.C, S, p.nseg);
   return hipGetLastError();
 }
 
@@ -639,7 +774,7 @@ hipError_t step(const ScanArgs& a, hipStream_t st) {
 template <class T, int S>
 hipError_t bwd(const ScanArgs& a, void* ws, hipStream_t st) {
   constexpr int SB = S < 16 ? S : 16;
-  const Plan p = bwd_plan(a, S);
+  const Plan p = bwd_plan(a);
   BwdBufs w;
   bwd_layout(a, S, p, static_cast<char*>(ws), &w);
   const long long units = (long long)a.B * p.nseg * p.cb;
@@ -678,7 +813,7 @@ size_t scan_bwd_workspace_bytes(bool, int B, int N, int C, int S, int G) {
   ScanArgs a{};
   a.B = B, a.N = N, a.C = C, a.G = G;
   BwdBufs w;
-  return bwd_layout(a, S, bwd_plan(a, S), nullptr, &w);
+  return bwd_layout(a, S, bwd_plan(a), nullptr, &w);
 }
 
 #define TTT_SCAN(fn, ...)                                               \

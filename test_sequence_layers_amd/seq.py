@@ -25,7 +25,7 @@ class _Call:
             torch = _torch()
         if not isinstance(x, torch.Tensor) or not x.is_cuda:
             raise TypeError(f"{name} must be a CUDA (HIP) tensor")
-        self.device, self.io = x.device, x.dtype
+        self.x, self.device, self.io = x, x.device, x.dtype
         self.dt = _dtype_code(x)
         self.stream = stream
 
@@ -84,10 +84,12 @@ class _Call:
         return t.data_ptr(), step
 
     def empty(self, shape, dtype):
-        if self.stream is None:
-            return torch.empty(shape, dtype=dtype, device=self.device)
-        with torch.cuda.stream(self.stream):
-            return torch.empty(shape, dtype=dtype, device=self.device)
+        if self.stream is not None:
+            with torch.cuda.stream(self.stream):
+                return torch.empty(shape, dtype=dtype, device=self.device)
+        if dtype is self.io and shape == self.x.shape:  # (half the host time of torch.empty)
+            return torch.empty_like(self.x, memory_format=torch.contiguous_format)
+        return torch.empty(shape, dtype=dtype, device=self.device)
 
     def output(self, name, t, shape, dtype=None):
         """(tensor, pointer) of an output, allocated if it was not passed in."""
@@ -114,12 +116,13 @@ class _Call:
     def run(self, fn_name, *args):
         fn = getattr(load_library(), fn_name)
         index = self.device.index
-        s = torch.cuda.current_stream(index) if self.stream is None else self.stream
+        # (the handle itself: torch.cuda.current_stream makes an object first, a tenth of a small call)
+        s = torch._C._cuda_getCurrentRawStream(index) if self.stream is None else self.stream.cuda_stream
         if index == torch.cuda.current_device():
-            st = fn(*args, s.cuda_stream)
+            st = fn(*args, s)
         else:
             with torch.cuda.device(index):
-                st = fn(*args, s.cuda_stream)
+                st = fn(*args, s)
         if st:
             _raise(st, fn_name)
 
