@@ -25,12 +25,9 @@ class _Call:
             torch = _torch()
         if not isinstance(x, torch.Tensor) or not x.is_cuda:
             raise TypeError(f"{name} must be a CUDA (HIP) tensor")
-        self.x, self.device, self.io = x, x.device, x.dtype
+        self.device, self.io = x.device, x.dtype
         self.dt = _dtype_code(x)
         self.stream = stream
-
-    def _fits(self, t, dtype, shape):
-        return isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.device == self.device
 
     def _refuse(self, name, t, dtype, shape):
         if not isinstance(t, torch.Tensor) or not t.is_cuda:
@@ -47,9 +44,10 @@ class _Call:
         """Data pointer of a contiguous tensor, fp32 unless told otherwise."""
         if dtype is None:
             dtype = torch.float32
-        if not (self._fits(t, dtype, shape) and t.is_contiguous()):
-            self._refuse(name, t, dtype, shape)
-        return t.data_ptr()
+        if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.device == self.device
+                and t.is_contiguous()):
+            return t.data_ptr()
+        self._refuse(name, t, dtype, shape)
 
     def dense(self, name, t, shape, dtype=None):
         """The same of a tensor that may be left out; None for None."""
@@ -58,7 +56,7 @@ class _Call:
     def rows(self, name, t, shape, width):
         """(data pointer, elements between rows) of an activation whose last dims (`width` elements) are
         contiguous and whose leading dims are one run of evenly spaced rows."""
-        if not self._fits(t, self.io, shape):
+        if not (isinstance(t, torch.Tensor) and t.dtype is self.io and t.shape == shape and t.device == self.device):
             self._refuse(name, t, self.io, shape)
         if t.is_contiguous():
             return t.data_ptr(), width
@@ -87,18 +85,17 @@ class _Call:
         if self.stream is not None:
             with torch.cuda.stream(self.stream):
                 return torch.empty(shape, dtype=dtype, device=self.device)
-        if dtype is self.io and shape == self.x.shape:  # (half the host time of torch.empty)
-            return torch.empty_like(self.x, memory_format=torch.contiguous_format)
         return torch.empty(shape, dtype=dtype, device=self.device)
 
-    def output(self, name, t, shape, dtype=None):
-        """(tensor, pointer) of an output, allocated if it was not passed in."""
-        if dtype is None:
-            dtype = self.io
-        if t is None:
-            t = self.empty(shape, dtype)
-            return t, t.data_ptr()
-        return t, self.need(name, t, shape, dtype)
+    def output(self, name, t, like):
+        """(tensor, pointer) of an output of `like`'s shape and dtype, allocated if it was not passed in."""
+        if t is not None:
+            return t, self.need(name, t, like.shape, like.dtype)
+        if self.stream is None:  # (empty_like takes half the host time of empty)
+            t = torch.empty_like(like, memory_format=torch.contiguous_format)
+        else:
+            t = self.empty(like.shape, like.dtype)
+        return t, t.data_ptr()
 
     def workspace(self, t, need):
         """(tensor, pointer, bytes)."""
@@ -130,14 +127,14 @@ class _Call:
 # ---------------------------------------------------------------------------------- layer norm
 def _norm_shape(x, weight):
     """(M, H, D): weight [D] norms x's rows, weight [H, D] each head's D of [..., H, D]."""
-    if not isinstance(weight, torch.Tensor) or weight.dim() not in (1, 2):
+    shape = weight.shape if isinstance(weight, torch.Tensor) else ()
+    nd = len(shape)
+    if nd not in (1, 2):
         raise ValueError("weight must be [D] or [H, D]")
-    nd = weight.dim()
-    if x.dim() < nd + 1 or x.shape[-nd:] != weight.shape:
-        raise ValueError(f"x must be [..., {', '.join(map(str, weight.shape))}], not {tuple(x.shape)}")
-    H, D = (1, weight.shape[0]) if nd == 1 else weight.shape
-    M = x.numel() // max(H * D, 1)
-    return M, H, D
+    if x.dim() <= nd or x.shape[-nd:] != shape:
+        raise ValueError(f"x must be [..., {', '.join(map(str, shape))}], not {tuple(x.shape)}")
+    H, D = (1, shape[0]) if nd == 1 else shape
+    return x.numel() // max(H * D, 1), H, D
 
 
 def ttt_forward_layernorm(x, weight, bias=None, eps: float = 1e-5, *, y=None, stream=None):
@@ -149,7 +146,7 @@ def ttt_forward_layernorm(x, weight, bias=None, eps: float = 1e-5, *, y=None, st
     M, H, D = _norm_shape(x, weight)
     px, xs = call.rows("x", x, x.shape, H * D)
     pw, pb = call.need("weight", weight, weight.shape), call.dense("bias", bias, weight.shape)
-    y, py = call.output("y", y, x.shape)
+    y, py = call.output("y", y, x)
     call.run("ttt_forward_layernorm", call.dt, M, H, D, float(eps), px, xs, pw, pb, py)
     return y
 
@@ -161,9 +158,9 @@ def ttt_backward_layernorm(x, weight, d_y, eps: float = 1e-5, *, d_x=None, d_wei
     M, H, D = _norm_shape(x, weight)
     px, xs = call.rows("x", x, x.shape, H * D)
     pw, pdy = call.need("weight", weight, weight.shape), call.need("d_y", d_y, x.shape, call.io)
-    d_x, pdx = call.output("d_x", d_x, x.shape)
-    d_weight, pdw = call.output("d_weight", d_weight, weight.shape, torch.float32)
-    d_bias, pdb = call.output("d_bias", d_bias, weight.shape, torch.float32)
+    d_x, pdx = call.output("d_x", d_x, x)
+    d_weight, pdw = call.output("d_weight", d_weight, weight)
+    d_bias, pdb = call.output("d_bias", d_bias, weight)
     workspace, pws, nws = call.workspace(workspace, load_library().ttt_backward_layernorm_workspace(call.dt, M, H, D))
     call.run("ttt_backward_layernorm", call.dt, M, H, D, float(eps), px, xs, pw, pdy, pdx, pdw, pdb, pws, nws)
     return d_x, d_weight, d_bias
@@ -193,7 +190,7 @@ def ttt_forward_conv1d(x, weight, bias=None, *, silu: bool = False, state=None, 
     held = (B, K - 1, C)
     ps, pl = call.dense("state", state, held, call.io), call.lengths(lengths, B)
     pso = call.dense("state_out", state_out, held, call.io)
-    y, py = call.output("y", y, x.shape)
+    y, py = call.output("y", y, x)
     call.run("ttt_forward_conv1d", call.dt, B, N, C, K, int(bool(silu)), px, xs, pw, pb, ps, pl, py, pso)
     return y
 
@@ -207,7 +204,7 @@ def ttt_step_conv1d(x, weight, bias=None, *, state, silu: bool = False, state_ou
     pw, pb = call.need("weight", weight, (C, K)), call.dense("bias", bias, (C,))
     ps = call.need("state", state, (B, K - 1, C), call.io)
     pso = ps if state_out is None else call.dense("state_out", state_out, (B, K - 1, C), call.io)
-    y, py = call.output("y", y, x.shape)
+    y, py = call.output("y", y, x)
     call.run("ttt_step_conv1d", call.dt, B, C, K, int(bool(silu)), px, xs, pw, pb, ps, py, pso)
     return y
 
@@ -223,15 +220,15 @@ def ttt_backward_conv1d(x, weight, bias, d_y, *, silu: bool = False, state=None,
     held = (B, K - 1, C)
     ps, pl = call.dense("state", state, held, call.io), call.lengths(lengths, B)
     pdy = call.need("d_y", d_y, x.shape, call.io)
-    d_x, pdx = call.output("d_x", d_x, x.shape)
-    d_weight, pdw = call.output("d_weight", d_weight, (C, K), torch.float32)
+    d_x, pdx = call.output("d_x", d_x, x)
+    d_weight, pdw = call.output("d_weight", d_weight, weight)
     pdb = pds = None
     if bias is not None:
-        d_bias, pdb = call.output("d_bias", d_bias, (C,), torch.float32)
+        d_bias, pdb = call.output("d_bias", d_bias, bias)
     elif d_bias is not None:
         raise ValueError("d_bias is given without bias")
     if state is not None:
-        d_state, pds = call.output("d_state", d_state, held)
+        d_state, pds = call.output("d_state", d_state, state)
     elif d_state is not None:
         raise ValueError("d_state is given without state")
     workspace, pws, nws = call.workspace(workspace, load_library().ttt_backward_conv1d_workspace(call.dt, B, N, C, K))
@@ -269,7 +266,7 @@ def ttt_forward_selective_scan(u, delta, A, Bm, Cm, D=None, delta_bias=None, z=N
     call = _Call("u", u, stream)
     args, (B, N, C, S, G) = _scan_inputs(call, u, delta, A, Bm, Cm, D, delta_bias, z, 2)
     ph, pho, pl = call.dense("h0", h0, (B, C, S)), call.dense("h_out", h_out, (B, C, S)), call.lengths(lengths, B)
-    y, py = call.output("y", y, u.shape)
+    y, py = call.output("y", y, u)
     workspace, pws, nws = call.workspace(
         workspace, load_library().ttt_forward_selective_scan_workspace(call.dt, B, N, C, S, G))
     call.run("ttt_forward_selective_scan", call.dt, B, N, C, S, G, int(bool(softplus)), *args, ph, pl, py, pho, pws, nws)
@@ -284,7 +281,7 @@ def ttt_step_selective_scan(u, delta, A, Bm, Cm, D=None, delta_bias=None, z=None
     args, (B, _, C, S, G) = _scan_inputs(call, u, delta, A, Bm, Cm, D, delta_bias, z, 1)
     ph = call.need("h", h, (B, C, S))
     pho = ph if h_out is None else call.dense("h_out", h_out, (B, C, S))
-    y, py = call.output("y", y, u.shape)
+    y, py = call.output("y", y, u)
     call.run("ttt_step_selective_scan", call.dt, B, C, S, G, int(bool(softplus)), *args, ph, py, pho)
     return y
 
@@ -298,19 +295,15 @@ def ttt_backward_selective_scan(u, delta, A, Bm, Cm, d_y, D=None, delta_bias=Non
     args, (B, N, C, S, G) = _scan_inputs(call, u, delta, A, Bm, Cm, D, delta_bias, z, 2)
     ph, pl = call.dense("h0", h0, (B, C, S)), call.lengths(lengths, B)
     pdy = call.need("d_y", d_y, u.shape, call.io)
-    f32 = torch.float32
     outs, ptrs = [], []
-    for name, t, of, shape, dtype in (
-            ("d_u", d_u, u, u.shape, call.io), ("d_delta", d_delta, u, u.shape, call.io), ("d_A", d_A, A, (C, S), f32),
-            ("d_B", d_B, Bm, Bm.shape, call.io), ("d_C", d_C, Cm, Cm.shape, call.io), ("d_D", d_D, D, (C,), f32),
-            ("d_delta_bias", d_delta_bias, delta_bias, (C,), f32), ("d_z", d_z, z, u.shape, call.io),
-            ("d_h0", d_h0, h0, (B, C, S), f32)):
+    for name, t, of in (("d_u", d_u, u), ("d_delta", d_delta, delta), ("d_A", d_A, A), ("d_B", d_B, Bm), ("d_C", d_C, Cm),
+                        ("d_D", d_D, D), ("d_delta_bias", d_delta_bias, delta_bias), ("d_z", d_z, z), ("d_h0", d_h0, h0)):
         if of is None:
             if t is not None:
                 raise ValueError(f"{name} is given without its input")
             p = None
         else:
-            t, p = call.output(name, t, shape, dtype)
+            t, p = call.output(name, t, of)
         outs.append(t)
         ptrs.append(p)
     workspace, pws, nws = call.workspace(
