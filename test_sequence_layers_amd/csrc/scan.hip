@@ -22,7 +22,7 @@ namespace ttt {
 namespace {
 
 constexpr int kWaves = 4;   // units per workgroup (forward)
-constexpr int kTokens = 2;  // tokens loaded ahead (4: 4 % slower, 8: 7 %; more registers, fewer waves)
+constexpr int kTokens = 2;  // tokens loaded ahead (4: 3 % slower, 1: 5 %)
 constexpr float kLn2 = 0.693147180559945309417f;
 
 // log(1 + exp(x)) with e = exp(-|x|): max(x, 0) + log1p(e), and log1p(e) = 2 atanh(e / (2 + e)) by
@@ -54,35 +54,47 @@ __device__ __forceinline__ float step_grad_of(float raw, int softplus, float& gr
   return softplus ? dt : raw;
 }
 
-// S values of a row of B or C that is the same for the whole wave, by scalar loads. (Holding one row ahead
-// in SGPRs instead was slower: 259 against 247 us for the forward pass at 4 x 8192 x 768 x 16, bf16; the
-// other waves of a SIMD cover the wait.)
+// A row piece of B and of C that is the same for the whole wave, as raw dwords by scalar loads: those of a
+// chunk's tokens are asked for together, before the chunk's steps are computed, as far as SGPRs hold
+// them (4 x 8192 x 768 x 16, bf16: 196 us, against 211 with each token's asked for where it is used).
 typedef const __attribute__((address_space(4))) uint32_t* ScalarPtr;
-template <class T, int S>
-__device__ __forceinline__ void load_uniform(const T* p, float* out) {
-  ScalarPtr q = (ScalarPtr)(uintptr_t)p;
-  if constexpr (sizeof(T) == 2) {
+template <class T, int SB>
+struct Piece {
+  static constexpr int W = SB * (int)sizeof(T) / 4;
+  uint32_t b[W], c[W];
+  __device__ __forceinline__ void load(const T* pb, const T* pc) {
+    const ScalarPtr qb = (ScalarPtr)(uintptr_t)pb, qc = (ScalarPtr)(uintptr_t)pc;
 #pragma unroll
-    for (int i = 0; i < S / 2; ++i) {
-      const uint32_t w = q[i];
-      out[2 * i] = __uint_as_float(w << 16);
-      out[2 * i + 1] = __uint_as_float(w & 0xffff0000u);
-    }
-  } else {
+    for (int i = 0; i < W; ++i) b[i] = qb[i];
+    if (pc)
 #pragma unroll
-    for (int i = 0; i < S; ++i) out[i] = __uint_as_float(q[i]);
+      for (int i = 0; i < W; ++i) c[i] = qc[i];
+  }
+};
+template <class T, int SB>
+__device__ __forceinline__ void widen(const uint32_t* w, float* out) {
+#pragma unroll
+  for (int i = 0; i < SB; ++i) {
+    if constexpr (sizeof(T) == 4) out[i] = __uint_as_float(w[i]);
+    else out[i] = __uint_as_float(i & 1 ? w[i / 2] & 0xffff0000u : w[i / 2] << 16);
   }
 }
 
-// Channel c of a row that is the same for the whole wave: the row's address stays in SGPRs and the lane's
-// part of it is 32 bits.
+// Channel c of a row that is the same for the whole wave: the row's address in SGPRs, the lane's part of it
+// in one 32-bit register. (The empty asm keeps the two apart: added up ahead of the loop they would be a
+// 64-bit address per lane and tensor, advanced by vector additions.)
+__device__ __forceinline__ uint32_t lane_part(int c, int size) {
+  uint32_t off = (uint32_t)c * (uint32_t)size;
+  asm volatile("" : "+v"(off));
+  return off;
+}
 template <class T>
 __device__ __forceinline__ float at(const T* row, int c) {
-  return (float)*reinterpret_cast<const T*>(reinterpret_cast<const char*>(row) + (uint32_t)c * (uint32_t)sizeof(T));
+  return (float)*reinterpret_cast<const T*>(reinterpret_cast<const char*>(row) + lane_part(c, sizeof(T)));
 }
 template <class T>
 __device__ __forceinline__ void put(T* row, int c, float v) {
-  *reinterpret_cast<T*>(reinterpret_cast<char*>(row) + (uint32_t)c * (uint32_t)sizeof(T)) = (T)v;
+  *reinterpret_cast<T*>(reinterpret_cast<char*>(row) + lane_part(c, sizeof(T))) = (T)v;
 }
 
 // How a call is cut up. Channel blocks: 64 channels of one group each.
@@ -118,7 +130,8 @@ __device__ __forceinline__ int length_of(const int* lengths, int b, int N) {
 template <class T, int S, bool FINAL>
 __global__ __launch_bounds__(64 * kWaves) void scan_fwd(ScanArgs a, Plan p, int units, float* __restrict__ ends,
                                                         float* __restrict__ sums) {
-  constexpr int kTok = S <= 16 ? kTokens : S == 32 ? 2 : 1;  // (wide states leave no registers for more)
+  constexpr int kTok = S <= 16 ? kTokens : 1;  // (wide states leave no registers for more)
+  constexpr bool kAhead = 2 * kTok * S * sizeof(T) <= 256;
   const int id = blockIdx.x * kWaves + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   if (id >= units) return;
   const Unit un = unit_of(id, p, a.C, a.G);
@@ -167,6 +180,14 @@ __global__ __launch_bounds__(64 * kWaves) void scan_fwd(ScanArgs a, Plan p, int 
   auto chunk = [&](int t, auto full) {
     constexpr bool FULL = decltype(full)::value;
     float cu[kTok], dt[kTok], cz[kTok], out[kTok];
+    Piece<T, S> mats[kTok];
+    if constexpr (kAhead) {
+#pragma unroll
+      for (int j = 0; j < kTok; ++j) {
+        const int tt = FULL ? t + j : min(t + j, te - 1);
+        mats[j].load(bm + tt * a.bs, FINAL ? cm + tt * a.cs : nullptr);
+      }
+    }
 #pragma unroll
     for (int j = 0; j < kTok; ++j) {
       cu[j] = nu[j];
@@ -182,8 +203,10 @@ __global__ __launch_bounds__(64 * kWaves) void scan_fwd(ScanArgs a, Plan p, int 
 #pragma unroll
         for (int s0 = 0; s0 < S; s0 += SB) {
           float bv[SB], cv[SB];
-          load_uniform<T, SB>(bm + (t + j) * a.bs + s0, bv);
-          if (FINAL) load_uniform<T, SB>(cm + (t + j) * a.cs + s0, cv);
+          Piece<T, SB> part;
+          if constexpr (!kAhead) part.load(bm + (t + j) * a.bs + s0, FINAL ? cm + (t + j) * a.cs + s0 : nullptr);
+          widen<T, SB>(kAhead ? mats[j].b + s0 * sizeof(T) / 4 : part.b, bv);
+          if (FINAL) widen<T, SB>(kAhead ? mats[j].c + s0 * sizeof(T) / 4 : part.c, cv);
 #pragma unroll
           for (int s = 0; s < SB; ++s) {
             float& x = h[s0 + s];
@@ -385,19 +408,27 @@ __global__ __launch_bounds__(64 * kWaves) void scan_bwd_ends(ScanArgs a, Plan p,
   auto chunk = [&](int t, auto full) {
     constexpr bool FULL = decltype(full)::value;
     float dtu[kTok], dt[kTok], v[kTok];
+    Piece<T, SB> mats[kTok];
+#pragma unroll
+    for (int j = 0; j < kTok; ++j) {
+      const int tt = FULL ? t + j : min(t + j, te - 1);
+      mats[j].load(bm + tt * a.bs, cm + tt * a.cs);
+    }
 #pragma unroll
     for (int j = 0; j < kTok; ++j) {
       dt[j] = step_of(nd[j] + db, a.softplus);
       dtu[j] = dt[j] * nu[j];
       v[j] = gate ? nv[j] * (nz[j] * sigmoid(nz[j])) : nv[j];
     }
+    // (the checkpoint's stores before the next loads: what is waited for next has them behind it anyway)
+    if ((t - t0) % kSub == 0) checkpoint(t);
     fetch(t + kTok);
 #pragma unroll
     for (int j = 0; j < kTok; ++j) {
       if (FULL || t + j < te) {
         float bv[SB], cv[SB];
-        load_uniform<T, SB>(bm + (t + j) * a.bs, bv);
-        load_uniform<T, SB>(cm + (t + j) * a.cs, cv);
+        widen<T, SB>(mats[j].b, bv);
+        widen<T, SB>(mats[j].c, cv);
 #pragma unroll
         for (int s = 0; s < SB; ++s) {
           const float e = exp2_hw(dt[j] * A2[s]);
@@ -409,17 +440,10 @@ __global__ __launch_bounds__(64 * kWaves) void scan_bwd_ends(ScanArgs a, Plan p,
       }
     }
   };
-  // A sub-chunk is kSub / kTok chunks; its checkpoint is written before the loads that are in flight are
-  // used.
   if (t0 < te) fetch(t0);
   int t = t0;
-  for (; t + kSub <= te; t += kSub) {
-    checkpoint(t);
-#pragma unroll
-    for (int i = 0; i < kSub; i += kTok) chunk(t + i, std::true_type{});
-  }
-  if (t < te) checkpoint(t);
-  for (; t < te; t += kTok) chunk(t, std::false_type{});
+  for (; t + kTok <= te; t += kTok) chunk(t, std::true_type{});
+  if (t < te) chunk(t, std::false_type{});
   // (the sub-chunks behind the sequence start from its end)
   for (t = t0 + (max(te - t0, 0) + kSub - 1) / kSub * kSub; t < t1; t += kSub) checkpoint(t);
   const long long seg = (long long)un.b * p.nseg + un.seg;
@@ -452,13 +476,15 @@ __device__ __forceinline__ void join_all(float* x, const float* y) {
 #pragma unroll
   for (int i = 0; i < NV; ++i) x[i] = join_over<M>(x[i], y[i]);
 }
-// x[0 .. N) -> the total of x[l % N] in lane l, when the sums over the lane bits from N on are done.
-template <int N>
-__device__ __forceinline__ float join_within(float* x) {
+// x[0 .. N) over the lane bits M, M / 2, ... (2 N = 2 M: bit 0 is left for a plain sum): value k's total ends up
+// in the lanes whose bits from M down spell k.
+template <int M, int N>
+__device__ __forceinline__ float join_values(float* x) {
+  static_assert(N == M || N == 1, "one lane bit per halving, and bit 0");
+  if constexpr (N == 1) return x[0] + dpp<kDppXor1>(x[0]);
 #pragma unroll
-  for (int i = 0; i < N / 2; ++i) x[i] = join_over<N / 2>(x[i], x[i + N / 2]);
-  if constexpr (N > 2) return join_within<N / 2>(x);
-  return x[0];
+  for (int i = 0; i < N / 2; ++i) x[i] = join_over<M>(x[i], x[i + N / 2]);
+  return join_values<M / 2, N / 2>(x);
 }
 
 // One workgroup per (b, segment, channel block), NW waves with SW states each of the same 64 channels.
@@ -470,10 +496,11 @@ __global__ __launch_bounds__(64 * Bwd<S>::NW) void scan_bwd(ScanArgs a, Plan p, 
   constexpr int SW = Bwd<S>::SW, NW = Bwd<S>::NW, kSub = Bwd<S>::kSub, kThreads = 64 * NW;
   constexpr int TW = kSub / NW;          // tokens a wave prepares and finishes
   constexpr int NV = 2 * SW;             // sums for dB and dC per token
-  constexpr int RB = 64 / NV;            // tokens whose sums fill the 64 lanes
+  constexpr int RB = 32 / NV;            // tokens whose sums are joined together
   constexpr int EW = (kSub * S + kThreads - 1) / kThreads;  // elements of B a thread passes on
   static_assert(kSub % NW == 0 && kSub % RB == 0, "sub-chunk shares");
   __shared__ float s_dt[kSub][64], s_dtu[kSub][64], s_v[kSub][64];
+  __shared__ float s_u[kSub][64], s_g[kSub][64], s_z[kSub][64], s_dy[kSub][64];  // for the end of the sub-chunk
   __shared__ float s_y[NW][kSub][64], s_q[NW][kSub][64], s_r[NW][kSub][64];
   __shared__ __align__(16) float s_b[kSub][S], s_c[kSub][S];
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), l = lane_id();
@@ -524,25 +551,24 @@ __global__ __launch_bounds__(64 * Bwd<S>::NW) void scan_bwd(ScanArgs a, Plan p, 
     for (int s = 0; s < SW; ++s) nck[s] = at(w.ck + (k * S + s0 + s) * C, c);
   };
   // Where the lane's sum over the channels goes: its token of the RB and its place in that token's row.
-  const int tok = (l >> 5 & 1) | (l >> 4 & 1) << 1 | (RB == 8 ? (l >> 3 & 1) << 2 : 0), k = l % NV;
+  const int tok = RB == 4 ? (l >> 5 & 1) | (l >> 4 & 1) << 1 : l >> 5, k = l / 2 % NV;
+  static_assert(RB == 4 || RB == 2, "token bits of a lane");
   const int mat_at = tok * p.cb * 2 * S + (k / SW) * S + s0 + k % SW;
   const int last = t0 + (t1 - 1 - t0) / kSub * kSub;
   fetch(last);
   for (int tc = last; tc >= t0; tc -= kSub) {
-    float pu[TW], pv[TW], pg[TW], pz[TW], pdy[TW], pdt[TW], h0[SW];
+    float h0[SW];
 #pragma unroll
     for (int j = 0; j < TW; ++j) {
       const int i = wave * TW + j;
       const bool in = tc + i < te && un.live;
-      pu[j] = in ? nu[j] : 0.f;
-      pz[j] = nz[j];
-      pdy[j] = in ? nv[j] : 0.f;
-      pdt[j] = step_grad_of(nd[j] + db, a.softplus, pg[j]);
-      if (!in) pdt[j] = 0.f;
-      pv[j] = gate && in ? pdy[j] * (pz[j] * sigmoid(pz[j])) : pdy[j];
-      s_dt[i][l] = pdt[j];
-      s_dtu[i][l] = pdt[j] * pu[j];
-      s_v[i][l] = pv[j];
+      const float uu = in ? nu[j] : 0.f, g = in ? nv[j] : 0.f;
+      float grad, dt = step_grad_of(nd[j] + db, a.softplus, grad);
+      dt = in ? dt : 0.f;
+      s_dt[i][l] = dt;
+      s_dtu[i][l] = dt * uu;
+      s_v[i][l] = gate && in ? g * (nz[j] * sigmoid(nz[j])) : g;
+      s_u[i][l] = uu, s_g[i][l] = grad, s_z[i][l] = nz[j], s_dy[i][l] = g;
     }
 #pragma unroll
     for (int i = 0; i < EW; ++i) {
@@ -576,7 +602,7 @@ __global__ __launch_bounds__(64 * Bwd<S>::NW) void scan_bwd(ScanArgs a, Plan p, 
 #pragma unroll
     for (int jb = kSub - RB; jb >= 0; jb -= RB) {
       // The sums over the channels are joined as the tokens come, so that few wait in registers.
-      float x[NV], l0[NV], l1[NV], l2[NV];
+      float x[NV], l0[NV], l1[NV];
 #pragma unroll
       for (int jj = RB - 1; jj >= 0; --jj) {
         const int j = jb + jj;
@@ -602,21 +628,16 @@ __global__ __launch_bounds__(64 * Bwd<S>::NW) void scan_bwd(ScanArgs a, Plan p, 
           for (int i = 0; i < NV; ++i) l0[i] = x[i];
         } else {
           join_all<32, NV>(x, l0);
-          if (jj & 2) {
+          if (RB == 4 && (jj & 2)) {
             for (int i = 0; i < NV; ++i) l1[i] = x[i];
-          } else {
+          } else if (RB == 4) {
             join_all<16, NV>(x, l1);
-            if (RB == 8 && (jj & 4)) {
-              for (int i = 0; i < NV; ++i) l2[i] = x[i];
-            } else if (RB == 8) {
-              join_all<8, NV>(x, l2);
-            }
           }
         }
         __builtin_amdgcn_sched_barrier(0);
       }
-      const float total = join_within<NV>(x);
-      if (tc + jb + tok < t1) put(w.mats + ((row0 + tc + jb) * p.cb + un.cb) * 2 * S, mat_at, total);
+      const float total = join_values<NV, NV>(x);
+      if (!(l & 1) && tc + jb + tok < t1) put(w.mats + ((row0 + tc + jb) * p.cb + un.cb) * 2 * S, mat_at, total);
     }
     __syncthreads();
 #pragma unroll
@@ -627,13 +648,14 @@ __global__ __launch_bounds__(64 * Bwd<S>::NW) void scan_bwd(ScanArgs a, Plan p, 
         if (t < n) {
           float sq = 0.f, sr = 0.f, sy = 0.f;
           for (int k = 0; k < NW; ++k) sq += s_q[k][i][l], sr += s_r[k][i][l], sy += gate ? s_y[k][i][l] : 0.f;
-          du = fmaf(sq, pdt[j], D * pv[j]);
-          dd = fmaf(sq, pu[j], sr * kLn2) * pg[j];  // (sr has A log2(e) for A)
-          dD = fmaf(pv[j], pu[j], dD);
+          const float uu = s_u[i][l], v = s_v[i][l];
+          du = fmaf(sq, s_dt[i][l], D * v);
+          dd = fmaf(sq, uu, sr * kLn2) * s_g[i][l];  // (sr has A log2(e) for A)
+          dD = fmaf(v, uu, dD);
           ddb += dd;
           if (gate) {
-            const float sg = sigmoid(pz[j]);
-            dz = pdy[j] * fmaf(D, pu[j], sy) * sg * fmaf(pz[j], 1.f - sg, 1.f);
+            const float zz = s_z[i][l], sg = sigmoid(zz);
+            dz = s_dy[i][l] * fmaf(D, uu, sy) * sg * fmaf(zz, 1.f - sg, 1.f);
           }
         }
         const long long row = (row0 + t) * C;
@@ -702,11 +724,13 @@ Plan plan_of(int B, int N, int C, int G, int want, int min_tokens, int unit) {
 }
 // Forward: as many waves as 256 CUs hold at once (six per SIMD at S = 16; 4 x 8192 x 768 x 16: 216 us, against 237
 // with five, 250 with four, 226 with eight, where the last ones run in a second turn), of at least
-// 24 tokens (3 x 1999 x 1000 x 32, fp32: 105 us; 117 at 16, 132 at 32). From 2048 blocks of channels on
-// (two waves per SIMD) a second run over the tokens costs more than the idle slots.
+// 24 tokens (3 x 1999 x 1000 x 32, fp32: 105 us; 117 at 16, 132 at 32). One segment where a second run over
+// the tokens costs more than it gives: sequences of up to 48 tokens (768 channels: 32 tokens 19 us in one
+// launch and 23 in three, 64 tokens 35 and 28) and 1600 blocks of channels or more (512 tokens of 1536
+// blocks: 417 and 401 us, of 2040: 427 and 530).
 Plan fwd_plan(const ScanArgs& a) {
   const int cb = (a.C / a.G + 63) / 64 * a.G;
-  if ((long long)a.B * cb >= 2048) return plan_of(a.B, a.N, a.C, a.G, 1, a.N, kTokens);
+  if (a.N <= 48 || (long long)a.B * cb >= 1600) return plan_of(a.B, a.N, a.C, a.G, 1, a.N, kTokens);
   return plan_of(a.B, a.N, a.C, a.G, 6144, 24, kTokens);
 }
 // Backward: 2 x 4096 x 768 x 16 takes 198 us with 4096 waves of scan_bwd_ends, 245 with twice as many;
