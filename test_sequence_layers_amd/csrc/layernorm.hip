@@ -17,44 +17,60 @@
 namespace ttt {
 namespace {
 
-constexpr int kThreads = 256;
-
-// Sum over a row's L lanes; for L = 256 (the whole workgroup) over the four waves through LDS, `slot`
-// alternating between consecutive sums so that one barrier each is enough.
+constexpr int kThreads = 256;  // of a workgroup of several rows; a wide row has L threads to itself
 template <int L>
-__device__ __forceinline__ float row_sum(float v, float (*red)[4], int slot) {
+constexpr int threads_of = L <= 64 ? kThreads : L;
+// The backward pass: more rows to a workgroup where a lane holds few elements, so that fewer partial rows
+// are written for as many waves (32768 x 12 x 64, bf16: 30.2 us, against 36.1 with 256 threads).
+constexpr int bwd_threads(int L, int KV) { return L > 64 ? L : KV <= 8 ? 1024 : kThreads; }
+
+// Sum over a row's L lanes; a row of more than a wave over its waves through LDS, `slot` going through
+// 0 .. 3 with consecutive sums so that one barrier each is enough.
+template <int L>
+__device__ __forceinline__ float row_sum(float v, float (*red)[16], int slot) {
   if constexpr (L <= 64) {
     return lanes_sum<L>(v);
   } else {
     v = lanes_sum<64>(v);
     if ((threadIdx.x & 63) == 0) red[slot][threadIdx.x >> 6] = v;
     __syncthreads();
-    return (red[slot][0] + red[slot][1]) + (red[slot][2] + red[slot][3]);
+    float s = 0.f;
+#pragma unroll
+    for (int i = 0; i < L / 64; ++i) s += red[slot][i];
+    return s;
   }
 }
 
-// One row into registers: element (k L + lane) V + i of the row is v[k V + i], zero past D.
+// One row: element (k L + lane) V + i is v[k V + i]. Past D the row's first elements are loaded again,
+// and zeroed when they are used.
 template <class T, int L, int K, int V>
-__device__ __forceinline__ void read_row(const T* p, int lane, int D, float* v) {
+struct Row {
+  Raw<T, V> r[K];
+  __device__ __forceinline__ void load(const T* p, int lane, int D) {
 #pragma unroll
-  for (int k = 0; k < K; ++k) {
-    const int at = (k * L + lane) * V;
-    if (at < D) {
-      load_row<T, V>(p + at, v + k * V);
-    } else {
-      for (int i = 0; i < V; ++i) v[k * V + i] = 0.f;
+    for (int k = 0; k < K; ++k) {
+      const int at = (k * L + lane) * V;
+      r[k].load(p + (at < D ? at : 0));
     }
   }
-}
+  __device__ __forceinline__ void widen(float* v, int lane, int D, bool in = true) const {
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      r[k].widen(v + k * V);
+      const bool ok = in && (k * L + lane) * V < D;
+      for (int i = 0; i < V; ++i) v[k * V + i] = ok ? v[k * V + i] : 0.f;
+    }
+  }
+};
 
 // v -> v - mean (zero past D); returns rstd.
 template <int L, int K, int V>
-__device__ __forceinline__ float centre(float* v, int lane, int D, float eps, float (*red)[4], int slot) {
+__device__ __forceinline__ float centre(float* v, int lane, int D, float eps, float (*red)[16]) {
   float s = 0.f;
 #pragma unroll
   for (int j = 0; j < K * V; ++j) s += v[j];
   // (divided, not multiplied by 1 / D: a constant row has to have its value as its mean)
-  const float mean = row_sum<L>(s, red, slot) / (float)D;
+  const float mean = row_sum<L>(s, red, 0) / (float)D;
   float q = 0.f;
 #pragma unroll
   for (int k = 0; k < K; ++k)
@@ -63,22 +79,24 @@ __device__ __forceinline__ float centre(float* v, int lane, int D, float eps, fl
       x = (k * L + lane) * V < D ? x - mean : 0.f;
       q = fmaf(x, x, q);
     }
-  return 1.f / sqrtf(row_sum<L>(q, red, slot + 1) / (float)D + eps);
+  return rcp_hw(sqrtf(fmaf(row_sum<L>(q, red, 1), rcp_hw((float)D), eps)));
 }
 
 template <class T, int L, int K, int V>
-__global__ __launch_bounds__(kThreads) void layernorm_fwd(const T* __restrict__ x, long long xs,
-                                                          const float* __restrict__ w,
-                                                          const float* __restrict__ b, T* __restrict__ y,
-                                                          int rows, int H, int D, float eps) {
-  __shared__ float red[2][4];
+__global__ __launch_bounds__(threads_of<L>) void layernorm_fwd(const T* __restrict__ x, long long xs,
+                                                               const float* __restrict__ w,
+                                                               const float* __restrict__ b, T* __restrict__ y,
+                                                               int rows, int H, int D, float eps) {
+  __shared__ float red[2][16];
   const int lane = threadIdx.x % L;
-  const long long row = wide_block() * (kThreads / L) + threadIdx.x / L;
-  if (row >= rows) return;  // (whole groups; for L = 256 the whole workgroup)
+  const long long row = wide_block() * (threads_of<L> / L) + threadIdx.x / L;
+  if (row >= rows) return;  // (whole groups; for L > 64 the whole workgroup)
   const int m = (int)(row / H), h = (int)(row - (long long)m * H);
+  Row<T, L, K, V> raw;
+  raw.load(x + (long long)m * xs + (long long)h * D, lane, D);
   float v[K * V];
-  read_row<T, L, K, V>(x + (long long)m * xs + (long long)h * D, lane, D, v);
-  const float rstd = centre<L, K, V>(v, lane, D, eps, red, 0);
+  raw.widen(v, lane, D);
+  const float rstd = centre<L, K, V>(v, lane, D, eps, red);
   T* py = y + row * D;
 #pragma unroll
   for (int k = 0; k < K; ++k) {
@@ -94,53 +112,70 @@ __global__ __launch_bounds__(kThreads) void layernorm_fwd(const T* __restrict__ 
 }
 
 // Workgroup (bx, by): R tokens at a time of the HB heads from by HB on, tokens bx R + r, + gridDim.x R, ...
-// Group g of L lanes has token r = g / HB and head g % HB. Partial row bx: [dw (H D), db (H D)].
+// Group g of L lanes has token r = g / HB and head g % HB; the next token's row is loaded while this one's
+// is worked on. Partial row bx: [dw (H D), db (H D)].
 template <class T, int L, int K, int V>
-__global__ __launch_bounds__(kThreads) void layernorm_bwd(const T* __restrict__ x, long long xs,
-                                                          const float* __restrict__ w,
-                                                          const T* __restrict__ dy, T* __restrict__ dx,
-                                                          float* __restrict__ part, int M, int H, int D,
-                                                          int HB, int R, float eps) {
+__global__ __launch_bounds__(bwd_threads(L, K* V)) void layernorm_bwd(const T* __restrict__ x, long long xs,
+                                                               const float* __restrict__ w,
+                                                               const T* __restrict__ dy, T* __restrict__ dx,
+                                                               float* __restrict__ part, int M, int H, int D,
+                                                               int HB, int R, float eps) {
   constexpr int LKV = L * K * V;
-  __shared__ float red[4][4];
-  __shared__ float join[L <= 64 ? kThreads * K * V : 1];
+  // A workgroup of 1024 threads has 128 registers a lane: there the weights are read again for each row,
+  // and rows are not loaded ahead.
+  constexpr bool kRoom = L <= 256;
+  __shared__ float red[4][16];
+  __shared__ float join[L <= 64 ? bwd_threads(L, K * V) * K * V : 1];
   const int lane = threadIdx.x % L, g = threadIdx.x / L;
-  const int r = g / HB, h = blockIdx.y * HB + g % HB;
-  const bool live = r < R && h < H;
-  float wv[K * V], aw[K * V], ab[K * V];
+  const int r = g / HB, hg = blockIdx.y * HB + g % HB, h = min(hg, H - 1);
+  const bool live = r < R && hg < H;
+  const float inv_d = rcp_hw((float)D);
+  float wv[K * V], aw[K * V] = {}, ab[K * V] = {};
+  auto weights = [&]() {
 #pragma unroll
-  for (int k = 0; k < K; ++k) {
-    const int at = (k * L + lane) * V;
-    for (int i = 0; i < V; ++i) wv[k * V + i] = aw[k * V + i] = ab[k * V + i] = 0.f;
-    if (live && at < D) load_params<V>(w + (long long)h * D + at, wv + k * V);
-  }
-  // (M is an int: the token counter stays below 2^31 + 2^31)
-  for (long long m = (long long)blockIdx.x * R + r; live && m < M; m += (long long)gridDim.x * R) {
-    const long long at0 = (m * H + h) * D;
+    for (int k = 0; k < K; ++k) {
+      const int at = (k * L + lane) * V;
+      load_params<V>(w + (long long)h * D + (at < D ? at : 0), wv + k * V);
+    }
+  };
+  if (kRoom) weights();
+  Row<T, L, K, V> rx, rd;
+  auto fetch = [&](long long m) {  // (past the last token: the last again)
+    const long long t = m < M ? m : M - 1;
+    rx.load(x + t * xs + (long long)h * D, lane, D);
+    rd.load(dy + (t * H + h) * D, lane, D);
+  };
+  const long long step = (long long)gridDim.x * R;
+  if (kRoom) fetch((long long)blockIdx.x * R + r);
+  for (long long m0 = (long long)blockIdx.x * R; m0 < M; m0 += step) {
+    const long long m = m0 + r;
+    const bool in = live && m < M;
     float v[K * V], d[K * V];
-    read_row<T, L, K, V>(x + m * xs + (long long)h * D, lane, D, v);
-    read_row<T, L, K, V>(dy + at0, lane, D, d);
-    const float rstd = centre<L, K, V>(v, lane, D, eps, red, 0);
+    if (!kRoom) fetch(m);
+    rx.widen(v, lane, D);
+    rd.widen(d, lane, D, in);
+    if (kRoom) fetch(m + step);
+    const float rstd = centre<L, K, V>(v, lane, D, eps, red);
+    if (!kRoom) weights();
     float s1 = 0.f, s2 = 0.f;
 #pragma unroll
     for (int j = 0; j < K * V; ++j) {
       v[j] *= rstd;  // xhat
       ab[j] += d[j];
-      aw[j] = fmaf(d[j], v[j], aw[j]);
+      aw[j] += in ? d[j] * v[j] : 0.f;
       d[j] *= wv[j];  // g
       s1 += d[j];
       s2 = fmaf(d[j], v[j], s2);
     }
-    s1 = row_sum<L>(s1, red, 2) / (float)D;
-    s2 = row_sum<L>(s2, red, 3) / (float)D;
+    s1 = row_sum<L>(s1, red, 2) * inv_d;
+    s2 = row_sum<L>(s2, red, 3) * inv_d;
+    T* o = dx + (m * H + h) * D;
 #pragma unroll
     for (int k = 0; k < K; ++k) {
       const int at = (k * L + lane) * V;
-      if (at < D) {
-        float o[V];
-        for (int i = 0; i < V; ++i) o[i] = rstd * (d[k * V + i] - s1 - v[k * V + i] * s2);
-        store_row<T, V>(dx + at0 + at, o);
-      }
+      float ov[V];
+      for (int i = 0; i < V; ++i) ov[i] = rstd * (d[k * V + i] - s1 - v[k * V + i] * s2);
+      if (in && at < D) store_row<T, V>(o + at, ov);
     }
   }
   const long long W = (long long)H * D;
@@ -182,7 +217,9 @@ struct StoreNormGrads {
   }
 };
 
-// How a row of D channels is spread over lanes: L lanes, K accesses of V elements each.
+// How a row of D channels is spread over lanes: L lanes, K accesses of V elements each, at most 24 elements
+// a lane (the backward pass holds five of such a set). A wave as far as that goes, since sums over more
+// waves take a barrier each.
 struct Shape {
   int L, K, V;
 };
@@ -193,14 +230,19 @@ Shape shape_of(bool bf, bool vec, int D) {
     if (n <= 64) return {64, 1, 1};
     if (n <= 256) return {64, 4, 1};
     if (n <= 1024) return {64, 16, 1};
-    return n <= 4096 ? Shape{256, 16, 1} : Shape{256, 64, 1};
+    return n <= 4096 ? Shape{256, 16, 1} : Shape{1024, 16, 1};
   }
   for (int L = 8; L <= 64; L *= 2)
     if (n <= L) return {L, 1, V};
   if (n <= 128) return {64, 2, V};
+  if (bf) {
+    if (n <= 192) return {64, 3, V};
+    if (n <= 512) return {256, n <= 256 ? 1 : 2, V};
+    return {1024, n <= 1024 ? 1 : 2, V};
+  }
   if (n <= 256) return {64, 4, V};
-  for (int K = 2;; K *= 2)
-    if (n <= 256 * K) return {256, K, V};
+  if (n <= 1024) return {256, n <= 512 ? 2 : 4, V};
+  return {1024, n <= 2048 ? 2 : 4, V};
 }
 
 // Calls f.run<T, L, K, V>() for the shape; every shape shape_of returns is listed.
@@ -208,17 +250,20 @@ template <class F>
 hipError_t with_shape(bool bf, Shape s, const F& f) {
 #define TTT_LN(T, l, k, v) \
   if (s.L == l && s.K == k && s.V == v) return f.template run<T, l, k, v>();
+#define TTT_LN_SCALAR(T) \
+  TTT_LN(T, 64, 1, 1) TTT_LN(T, 64, 4, 1) TTT_LN(T, 64, 16, 1) TTT_LN(T, 256, 16, 1) TTT_LN(T, 1024, 16, 1)
   if (bf) {
     TTT_LN(bf16, 8, 1, 8) TTT_LN(bf16, 16, 1, 8) TTT_LN(bf16, 32, 1, 8) TTT_LN(bf16, 64, 1, 8)
-    TTT_LN(bf16, 64, 2, 8) TTT_LN(bf16, 64, 4, 8)
-    TTT_LN(bf16, 256, 2, 8) TTT_LN(bf16, 256, 4, 8) TTT_LN(bf16, 256, 8, 8)
-    TTT_LN(bf16, 64, 1, 1) TTT_LN(bf16, 64, 4, 1) TTT_LN(bf16, 64, 16, 1) TTT_LN(bf16, 256, 16, 1) TTT_LN(bf16, 256, 64, 1)
+    TTT_LN(bf16, 64, 2, 8) TTT_LN(bf16, 64, 3, 8) TTT_LN(bf16, 256, 1, 8) TTT_LN(bf16, 256, 2, 8)
+    TTT_LN(bf16, 1024, 1, 8) TTT_LN(bf16, 1024, 2, 8)
+    TTT_LN_SCALAR(bf16)
   } else {
     TTT_LN(float, 8, 1, 4) TTT_LN(float, 16, 1, 4) TTT_LN(float, 32, 1, 4) TTT_LN(float, 64, 1, 4)
-    TTT_LN(float, 64, 2, 4) TTT_LN(float, 64, 4, 4)
-    TTT_LN(float, 256, 2, 4) TTT_LN(float, 256, 4, 4) TTT_LN(float, 256, 8, 4) TTT_LN(float, 256, 16, 4)
-    TTT_LN(float, 64, 1, 1) TTT_LN(float, 64, 4, 1) TTT_LN(float, 64, 16, 1) TTT_LN(float, 256, 16, 1) TTT_LN(float, 256, 64, 1)
+    TTT_LN(float, 64, 2, 4) TTT_LN(float, 64, 4, 4) TTT_LN(float, 256, 2, 4) TTT_LN(float, 256, 4, 4)
+    TTT_LN(float, 1024, 2, 4) TTT_LN(float, 1024, 4, 4)
+    TTT_LN_SCALAR(float)
   }
+#undef TTT_LN_SCALAR
 #undef TTT_LN
   return hipErrorInvalidValue;
 }
@@ -241,9 +286,9 @@ struct FwdCall {
   hipStream_t st;
   template <class T, int L, int K, int V>
   hipError_t run() const {
-    constexpr int G = kThreads / L;
+    constexpr int G = threads_of<L> / L;
     const int rows = M * H;
-    hipLaunchKernelGGL((layernorm_fwd<T, L, K, V>), wide_grid(((long long)rows + G - 1) / G), dim3(kThreads), 0, st,
+    hipLaunchKernelGGL((layernorm_fwd<T, L, K, V>), wide_grid(((long long)rows + G - 1) / G), dim3(threads_of<L>), 0, st,
                        (const T*)x, xs, w, b, (T*)y, rows, H, D, eps);
     return hipGetLastError();
   }
@@ -256,14 +301,19 @@ struct BwdPlan {
   long long P;
 };
 BwdPlan bwd_plan(Shape s, int M, int H) {
-  const int groups = kThreads / s.L;
+  const int threads = bwd_threads(s.L, s.K * s.V), groups = s.L <= 64 ? threads / s.L : 1;
   BwdPlan p;
   p.HB = H < groups ? H : groups;
   p.R = groups / p.HB;
   p.gy = (H + p.HB - 1) / p.HB;
   p.P = (M + p.R - 1) / p.R;
-  const long long most = 1024 / p.gy > 1 ? 1024 / p.gy : 1;
-  if (p.P > most) p.P = most;
+  // Workgroups: four waves per SIMD of 256 CUs with 1024 threads each, two with fewer (8192 x 4096: 50.5 us
+  // with 512 workgroups, 55.8 with 768, 63 with 1024; 65536 x 768: 66.6, 63.7 and 67.1).
+  const long long wgs = threads >= 1024 ? 256 : 512, most = wgs > p.gy ? wgs / p.gy : 1;
+  if (p.P > most) {  // as many turns each, up to one
+    const long long turns = (p.P + most - 1) / most;
+    p.P = (p.P + turns - 1) / turns;
+  }
   return p;
 }
 
@@ -280,7 +330,7 @@ struct BwdCall {
   hipStream_t st;
   template <class T, int L, int K, int V>
   hipError_t run() const {
-    const int threads = (p.HB * p.R * L + 63) / 64 * 64;
+    const int threads = L <= 64 ? (p.HB * p.R * L + 63) / 64 * 64 : L;
     hipLaunchKernelGGL((layernorm_bwd<T, L, K, V>), dim3((unsigned)p.P, (unsigned)p.gy), dim3(threads), 0, st,
                        (const T*)x, xs, w, (const T*)dy, (T*)dx, part, M, H, D, p.HB, p.R, eps);
     return hipGetLastError();

@@ -6,22 +6,35 @@
 
 namespace ttt {
 
-// Vector of V elements of T: V = 16 / sizeof(T) (one 16-byte access) or V = 1.
+// V elements of T as they are loaded, V = 16 / sizeof(T) (one 16-byte access) or V = 1; widened to fp32 where
+// they are used. (Widened where they are loaded, inside a branch, they would be waited for there.)
+template <class T, int V>
+struct Raw {
+  uint4 r;
+  __device__ __forceinline__ void load(const T* p) { r = ld16(p); }
+  __device__ __forceinline__ void widen(float* out) const {
+    const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+    for (int i = 0; i < 4; ++i) {
+      if constexpr (sizeof(T) == 2) {
+        out[2 * i] = __uint_as_float(w[i] << 16);
+        out[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+      } else {
+        out[i] = __uint_as_float(w[i]);
+      }
+    }
+  }
+};
+template <class T>
+struct Raw<T, 1> {
+  T r;
+  __device__ __forceinline__ void load(const T* p) { r = p[0]; }
+  __device__ __forceinline__ void widen(float* out) const { out[0] = (float)r; }
+};
 template <class T, int V>
 __device__ __forceinline__ void load_row(const T* p, float* out) {
-  if constexpr (V == 1) {
-    out[0] = (float)p[0];
-  } else if constexpr (sizeof(T) == 2) {
-    const uint4 q = ld16(p);
-    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
-    for (int i = 0; i < 4; ++i) {
-      out[2 * i] = __uint_as_float(w[i] << 16);
-      out[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-    }
-  } else {
-    const float4 q = *reinterpret_cast<const float4*>(p);
-    out[0] = q.x; out[1] = q.y; out[2] = q.z; out[3] = q.w;
-  }
+  Raw<T, V> r;
+  r.load(p);
+  r.widen(out);
 }
 
 template <class T, int V>
@@ -60,15 +73,23 @@ constexpr int kDppMirror16 = 0x140;  // lane i of 16 reads lane 15 - i
 constexpr int kDppRor8 = 0x128;      // lane i of 16 reads lane i ^ 8
 
 // Sum over aligned groups of L lanes (L a power of two up to 64); every lane gets it. Within 16
-// lanes by DPP: once the lanes of a quad agree, the mirrored lane holds the other quad's sum.
+// lanes by DPP: once the lanes of a quad agree, the mirrored lane holds the other quad's sum. Over 16
+// and 32 lanes by swapping register halves with a copy: the two results are the two halves' values in
+// all lanes.
 template <int L>
 __device__ __forceinline__ float lanes_sum(float v) {
   if constexpr (L >= 2) v += dpp<kDppXor1>(v);
   if constexpr (L >= 4) v += dpp<kDppXor2>(v);
   if constexpr (L >= 8) v += dpp<kDppMirror8>(v);
   if constexpr (L >= 16) v += dpp<kDppMirror16>(v);
-  if constexpr (L >= 32) v += __shfl_xor(v, 16);
-  if constexpr (L >= 64) v += __shfl_xor(v, 32);
+  if constexpr (L >= 32) {
+    const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    v = __uint_as_float(r[0]) + __uint_as_float(r[1]);
+  }
+  if constexpr (L >= 64) {
+    const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    v = __uint_as_float(r[0]) + __uint_as_float(r[1]);
+  }
   return v;
 }
 
@@ -85,9 +106,10 @@ inline dim3 wide_grid(long long blocks) {
 }
 __device__ __forceinline__ long long wide_block() { return (long long)blockIdx.y * gridDim.x + blockIdx.x; }
 
-// Sum of P rows of W fp32 values, fixed order: thread row ty of 16 adds rows ty, ty + 16, ..., then
-// the 16 sums are added in order. out(column, sum) stores it.
-constexpr int kSumCols = 64, kSumRows = 16;
+// Sum of P rows of W fp32 values, fixed order: thread row ty of kSumRows adds rows ty, ty + kSumRows, ...,
+// then its sums are added in order. out(column, sum) stores it. Few columns per workgroup: a narrow
+// matrix of many rows is spread over more CUs, and a thread has a few rounds of loads at most.
+constexpr int kSumCols = 16, kSumRows = 64;
 template <class Out>
 __global__ __launch_bounds__(kSumCols* kSumRows) void column_sum(const float* __restrict__ part,
                                                                  long long P, int W, Out out) {
@@ -98,12 +120,14 @@ __global__ __launch_bounds__(kSumCols* kSumRows) void column_sum(const float* __
   if (col < W) {
     const float* p = part + col;
     long long r = ty;
-    for (; r + 3 * kSumRows < P; r += 4 * kSumRows) {
-      float v[4];
-      for (int i = 0; i < 4; ++i) v[i] = p[(r + i * kSumRows) * W];
-      for (int i = 0; i < 4; ++i) acc += v[i];
+    for (; r < P; r += 8 * kSumRows) {
+      float v[8];
+      for (int i = 0; i < 8; ++i) {
+        const long long k = r + i * kSumRows;
+        v[i] = p[(k < P ? k : r) * W];
+      }
+      for (int i = 0; i < 8; ++i) acc += r + i * kSumRows < P ? v[i] : 0.f;
     }
-    for (; r < P; r += kSumRows) acc += p[r * W];
   }
   sm[ty][tx] = acc;
   __syncthreads();
