@@ -3,12 +3,15 @@
 //   pre[n] = bias + sum_k w[k] x[n - (K - 1) + k],   y = pre or pre sigmoid(pre)
 //   dpre = dy act'(pre),  dx[n] = sum_k w[k] dpre[n + K - 1 - k],  dw[k] = sum dpre[n] x[n - (K - 1) + k]
 //
-// A stream bound by HBM. A thread owns 16 bytes of channels (one channel where rows are not 16-byte
+// A stream bound by HBM. A thread owns 8 bytes of channels (one channel where rows are not 8-byte
 // aligned) and walks down a run of tokens with the last K inputs in registers, so that every
-// input is read once but for the K - 1 tokens before each run (from L2). The backward pass walks the
-// same way with the last K values of dpre beside the inputs: dx lags K - 1 tokens behind. dw and db
-// stay in registers over a run, are joined in LDS over the runs of a workgroup, and a second launch
-// sums the workgroups' partial rows in a fixed order.
+// input is read once but for the K - 1 tokens before each run (from L2). The next tokens are loaded while
+// the last are worked on, and nothing in the walk branches: loads are clamped to the sequence and
+// their values chosen, stores past the run write its last row again with the same value, so that no
+// load is waited for together with a store behind it. The backward pass walks the same way with the last
+// K values of dpre beside the inputs: dx lags K - 1 tokens behind. dw and db stay in registers over a run,
+// are joined in LDS over the runs of a workgroup, and a second launch sums the workgroups' partial
+// rows in a fixed order.
 #include "internal.hpp"
 #include "rowops.hpp"
 #include "seq.hpp"
@@ -18,6 +21,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kRun = 16;      // tokens per thread
+constexpr int kAhead = 4;     // tokens loaded ahead; divides kRun
 constexpr int kPieces = 32;   // backward: pieces of a row per workgroup
 constexpr int kRuns = kThreads / kPieces;  // backward: runs per workgroup
 
@@ -60,6 +64,16 @@ __global__ __launch_bounds__(kThreads) void conv1d_fwd(Conv1dArgs a, int pieces,
   const T* x = (const T*)a.x + (long long)b * a.N * a.xs + c0;
   const T* state = a.state ? (const T*)a.state + (long long)b * (K - 1) * C + c0 : nullptr;
   T* y = (T*)a.y + (long long)b * a.N * C + c0;
+  const int t0 = run * kRun, t1 = min(a.N, t0 + kRun);
+  Raw<T, V> next[kAhead];
+  auto fetch = [&](int t) {
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j) next[j].load(x + (long long)max(min(t + j, n - 1), 0) * a.xs);
+  };
+  fetch(t0);
+  float wt[K][V], bs[V], win[K][V], o[V];
+  load_taps<V, K>(a.w, a.bias, c0, wt, bs);
+  for (int k = 0; k < K - 1; ++k) input<T, V, K>(x, a.xs, state, C, min(t0, n) - (K - 1) + k, win[k]);
   if (run == 0 && a.state_out) {
     T* so = (T*)a.state_out + (long long)b * (K - 1) * C + c0;
     for (int j = 0; j < K - 1; ++j) {
@@ -68,26 +82,24 @@ __global__ __launch_bounds__(kThreads) void conv1d_fwd(Conv1dArgs a, int pieces,
       store_row<T, V>(so + (long long)j * C, v);
     }
   }
-  float wt[K][V], bs[V], win[K][V];
-  load_taps<V, K>(a.w, a.bias, c0, wt, bs);
-  const int t0 = run * kRun, t1 = min(a.N, t0 + kRun), te = min(t1, n);
-  if (t0 < te)
-    for (int k = 0; k < K - 1; ++k) input<T, V, K>(x, a.xs, state, C, t0 - (K - 1) + k, win[k]);
-#pragma unroll 4
-  for (int t = t0; t < te; ++t) {
-    load_row<T, V>(x + (long long)t * a.xs, win[K - 1]);
-    float o[V];
-    for (int i = 0; i < V; ++i) {
-      float s = bs[i];
-      for (int k = 0; k < K; ++k) s = fmaf(wt[k][i], win[k][i], s);
-      o[i] = act<SILU>(s);
-      for (int k = 0; k < K - 1; ++k) win[k][i] = win[k + 1][i];
+  for (int i = 0; i < V; ++i) o[i] = 0.f;
+  for (int t = t0; t < t1; t += kAhead) {
+    Raw<T, V> cur[kAhead];
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j) cur[j] = next[j];
+    fetch(t + kAhead);
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j) {
+      cur[j].widen(win[K - 1]);
+      const bool in = t + j < n, mine = t + j < t1;
+      for (int i = 0; i < V; ++i) {
+        float s = bs[i];
+        for (int k = 0; k < K; ++k) s = fmaf(wt[k][i], win[k][i], s);
+        o[i] = mine ? (in ? act<SILU>(s) : 0.f) : o[i];
+        for (int k = 0; k < K - 1; ++k) win[k][i] = win[k + 1][i];
+      }
+      store_row<T, V>(y + (long long)min(t + j, t1 - 1) * C, o);
     }
-    store_row<T, V>(y + (long long)t * C, o);
-  }
-  for (int t = max(t0, te); t < t1; ++t) {
-    float o[V] = {};
-    store_row<T, V>(y + (long long)t * C, o);
   }
 }
 
@@ -121,54 +133,78 @@ __global__ __launch_bounds__(kThreads) void conv1d_bwd(Conv1dArgs a, int pieces)
   const int b = blockIdx.z, C = a.C, c0 = piece * V;
   const bool live = piece < pieces;
   float acc[K + 1][V] = {};
-  if (live) {
+  const long long first = ((long long)blockIdx.y * kRuns + sub) * kRun;
+  if (live && first < a.N) {
     const int n = length_of(a.lengths, b, a.N);
     const T* x = (const T*)a.x + (long long)b * a.N * a.xs + c0;
     const T* state = a.state ? (const T*)a.state + (long long)b * (K - 1) * C + c0 : nullptr;
     const T* dy = (const T*)a.dy + (long long)b * a.N * C + c0;
     T* dx = (T*)a.dx + (long long)b * a.N * C + c0;
-    float wt[K][V], bs[V], win[K][V], dp[K][V] = {};
-    load_taps<V, K>(a.w, a.bias, c0, wt, bs);
-    const long long first = ((long long)blockIdx.y * kRuns + sub) * kRun;
-    if (first < a.N) {
-      const int t0 = (int)first, t1 = min(a.N, t0 + kRun);
-      // Tokens behind the sequence have no dpre; dx[t] needs dpre up to t + K - 1.
-      for (int k = 0; k < K - 1; ++k) {
-        const int t = t0 - (K - 1) + k;
-        if (t < n) input<T, V, K>(x, a.xs, state, C, t, win[k]);
-        else for (int i = 0; i < V; ++i) win[k][i] = 0.f;
+    const int t0 = (int)first, t1 = min(a.N, t0 + kRun);
+    Raw<T, V> nx[kAhead], nd[kAhead];
+    auto fetch = [&](int t) {
+#pragma unroll
+      for (int j = 0; j < kAhead; ++j) {
+        const long long tt = max(min(t + j, n - 1), 0);
+        nx[j].load(x + tt * a.xs);
+        nd[j].load(dy + tt * C);
       }
-#pragma unroll 4
-      for (int t = t0; t < t1 + K - 1; ++t) {
-        float d[V] = {};
-        if (t < n) {
-          load_row<T, V>(x + (long long)t * a.xs, win[K - 1]);
-          load_row<T, V>(dy + (long long)t * C, d);
-          for (int i = 0; i < V; ++i) {
-            if (SILU) {
-              float pre = bs[i];
-              for (int k = 0; k < K; ++k) pre = fmaf(wt[k][i], win[k][i], pre);
-              const float s = sigmoid(pre);
-              d[i] *= s * fmaf(pre, 1.f - s, 1.f);
-            }
-            if (t < t1) {
-              acc[K][i] += d[i];
-              for (int k = 0; k < K; ++k) acc[k][i] = fmaf(d[i], win[k][i], acc[k][i]);
-            }
-            for (int k = 0; k < K - 1; ++k) win[k][i] = win[k + 1][i];
-          }
+    };
+    fetch(t0);
+    float wt[K][V], bs[V], win[K][V], dp[K][V] = {}, o[V];
+    load_taps<V, K>(a.w, a.bias, c0, wt, bs);
+    for (int k = 0; k < K - 1; ++k) input<T, V, K>(x, a.xs, state, C, min(t0, n) - (K - 1) + k, win[k]);
+    // One token: its dpre (none behind the sequence), its part of the parameters' gradients (of the run's
+    // own tokens), and o = dx[t - (K - 1)], which then has all it needs:
+    // dp[k] = dpre[t - (K - 1) + k], dx[t - (K - 1)] = sum_k w[K - 1 - k] dp[k].
+    auto token = [&](int t, const Raw<T, V>& rx, const Raw<T, V>& rd, float* out) {
+      float d[V];
+      rx.widen(win[K - 1]);
+      rd.widen(d);
+      const bool in = t < n;
+      for (int i = 0; i < V; ++i) {
+        win[K - 1][i] = in ? win[K - 1][i] : 0.f;
+        if (SILU) {
+          float pre = bs[i];
+          for (int k = 0; k < K; ++k) pre = fmaf(wt[k][i], win[k][i], pre);
+          const float s = sigmoid(pre);
+          d[i] *= s * fmaf(pre, 1.f - s, 1.f);
         }
-        // dp[k] = dpre[t - (K - 1) + k]; dx[t - (K - 1)] = sum_k w[K - 1 - k] dp[k]
-        float o[V];
+        d[i] = in ? d[i] : 0.f;
+      }
+      if (t < t1)
         for (int i = 0; i < V; ++i) {
-          for (int k = 0; k < K - 1; ++k) dp[k][i] = dp[k + 1][i];
-          dp[K - 1][i] = d[i];
-          o[i] = 0.f;
-          for (int k = 0; k < K; ++k) o[i] = fmaf(wt[K - 1 - k][i], dp[k][i], o[i]);
+          acc[K][i] += d[i];
+          for (int k = 0; k < K; ++k) acc[k][i] = fmaf(d[i], win[k][i], acc[k][i]);
         }
-        const int td = t - (K - 1);
-        if (td >= t0) store_row<T, V>(dx + (long long)td * C, o);
-        else if (td < 0 && a.dstate) store_row<T, V>((T*)a.dstate + ((long long)b * (K - 1) + t) * C + c0, o);
+      for (int i = 0; i < V; ++i) {
+        for (int k = 0; k < K - 1; ++k) win[k][i] = win[k + 1][i], dp[k][i] = dp[k + 1][i];
+        dp[K - 1][i] = d[i];
+        out[i] = 0.f;
+        for (int k = 0; k < K; ++k) out[i] = fmaf(wt[K - 1 - k][i], dp[k][i], out[i]);
+      }
+    };
+    // The first K - 1 tokens complete no dx of this run; a sequence's first run has the state's there.
+    Raw<T, V> cx[kAhead], cd[kAhead];
+    static_assert(K - 1 <= kAhead, "the tokens before the first dx are one fetch");
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j) cx[j] = nx[j], cd[j] = nd[j];
+    fetch(t0 + K - 1);
+#pragma unroll
+    for (int j = 0; j < K - 1; ++j) {
+      token(t0 + j, cx[j], cd[j], o);
+      if (t0 == 0 && a.dstate) store_row<T, V>((T*)a.dstate + ((long long)b * (K - 1) + j) * C + c0, o);
+    }
+    for (int t = t0; t < t1; t += kAhead) {  // t: the dx completed
+#pragma unroll
+      for (int j = 0; j < kAhead; ++j) cx[j] = nx[j], cd[j] = nd[j];
+      fetch(t + K - 1 + kAhead);
+#pragma unroll
+      for (int j = 0; j < kAhead; ++j) {
+        float v[V];
+        token(t + K - 1 + j, cx[j], cd[j], v);
+        for (int i = 0; i < V; ++i) o[i] = t + j < t1 ? v[i] : o[i];
+        store_row<T, V>(dx + (long long)min(t + j, t1 - 1) * C, o);
       }
     }
   }
@@ -199,11 +235,13 @@ struct StoreConvGrads {
   }
 };
 
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+// Four channels at a time (8 bytes of bf16, 16 of fp32) where every row starts on such a piece.
 bool vector_rows(bool bf, const Conv1dArgs& a) {
-  const int V = bf ? 8 : 4;
-  return a.C % V == 0 && a.xs % V == 0 && aligned16(a.x) && aligned16(a.state) && aligned16(a.y) &&
-         aligned16(a.state_out) && aligned16(a.dy) && aligned16(a.dx) && aligned16(a.dstate);
+  uintptr_t at = 0;
+  for (const void* p : {a.x, a.state, (const void*)a.y, (const void*)a.state_out, a.dy, (const void*)a.dx,
+                        (const void*)a.dstate})
+    at |= reinterpret_cast<uintptr_t>(p);
+  return a.C % 4 == 0 && a.xs % 4 == 0 && at % (bf ? 8 : 16) == 0;
 }
 
 int run_groups(int N) { return (int)(((long long)N + kRun * kRuns - 1) / (kRun * kRuns)); }
@@ -214,7 +252,7 @@ hipError_t with_variant(bool bf, bool vec, int K, bool silu, const F& f) {
 #define TTT_CONV(T, v, k) \
   if (K == k) return silu ? f.template run<T, v, k, true>() : f.template run<T, v, k, false>();
   if (bf) {
-    if (vec) { TTT_CONV(bf16, 8, 2) TTT_CONV(bf16, 8, 3) TTT_CONV(bf16, 8, 4) }
+    if (vec) { TTT_CONV(bf16, 4, 2) TTT_CONV(bf16, 4, 3) TTT_CONV(bf16, 4, 4) }
     else { TTT_CONV(bf16, 1, 2) TTT_CONV(bf16, 1, 3) TTT_CONV(bf16, 1, 4) }
   } else {
     if (vec) { TTT_CONV(float, 4, 2) TTT_CONV(float, 4, 3) TTT_CONV(float, 4, 4) }

@@ -6,20 +6,22 @@
 
 namespace ttt {
 
-// V elements of T as they are loaded, V = 16 / sizeof(T) (one 16-byte access) or V = 1; widened to fp32 where
+// V elements of T as they are loaded, in one access of 8 or 16 bytes or one element; widened to fp32 where
 // they are used. (Widened where they are loaded, inside a branch, they would be waited for there.)
 template <class T, int V>
 struct Raw {
-  uint4 r;
-  __device__ __forceinline__ void load(const T* p) { r = ld16(p); }
+  static constexpr int W = V * (int)sizeof(T) / 4;
+  static_assert(W == 2 || W == 4, "8 or 16 bytes");
+  typedef uint32_t Words __attribute__((ext_vector_type(W)));
+  Words r;
+  __device__ __forceinline__ void load(const T* p) { r = *reinterpret_cast<const Words*>(p); }
   __device__ __forceinline__ void widen(float* out) const {
-    const uint32_t w[4] = {r.x, r.y, r.z, r.w};
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < W; ++i) {
       if constexpr (sizeof(T) == 2) {
-        out[2 * i] = __uint_as_float(w[i] << 16);
-        out[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+        out[2 * i] = __uint_as_float(r[i] << 16);
+        out[2 * i + 1] = __uint_as_float(r[i] & 0xffff0000u);
       } else {
-        out[i] = __uint_as_float(w[i]);
+        out[i] = __uint_as_float(r[i]);
       }
     }
   }
@@ -41,6 +43,8 @@ template <class T, int V>
 __device__ __forceinline__ void store_row(T* p, const float* v) {
   if constexpr (V == 1) {
     p[0] = (T)v[0];
+  } else if constexpr (sizeof(T) == 2 && V == 4) {
+    *reinterpret_cast<bf16x4*>(p) = to_bf16x4(f32x4{v[0], v[1], v[2], v[3]});
   } else if constexpr (sizeof(T) == 2) {
     const bf16x8 o = cat8(to_bf16x4(f32x4{v[0], v[1], v[2], v[3]}), to_bf16x4(f32x4{v[4], v[5], v[6], v[7]}));
     st16(p, __builtin_bit_cast(uint4, o));
