@@ -20,10 +20,18 @@ namespace ttt {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kRun = 16;      // tokens per thread
-constexpr int kAhead = 4;     // tokens loaded ahead; divides kRun
+constexpr int kAhead = 4;     // tokens loaded ahead
 constexpr int kPieces = 32;   // backward: pieces of a row per workgroup
 constexpr int kRuns = kThreads / kPieces;  // backward: runs per workgroup
+
+// Tokens per thread, a multiple of kAhead. Long runs read fewer tokens twice, short ones give more threads and
+// end sooner: 1024 x 768 tokens and channels take 4.6 us forward (9.0 backward) in runs of 4, 5.6 (10.5) of 8
+// and 11.0 (16.9) of 32; 8 x 1024 x 768 10.2 (20.6), 9.7 (18.2), 13.1 (19.5); 4 x 4096 x 768 13.9 (24.3) of 16,
+// 14.2 (27.4) of 8, 16.0 (26.6) of 32; 4 x 8192 x 768 backward 36.5 of 32 and 39.4 of 16.
+int run_length(int B, int N, int C) {
+  const double all = (double)B * N * C;
+  return all < (1 << 21) ? 4 : all < (1 << 23) ? 8 : all < (1 << 24) ? 16 : 32;
+}
 
 template <bool SILU>
 __device__ __forceinline__ float act(float pre) {
@@ -55,7 +63,7 @@ __device__ __forceinline__ void load_taps(const float* w, const float* bias, int
 }
 
 template <class T, int V, int K, bool SILU>
-__global__ __launch_bounds__(kThreads) void conv1d_fwd(Conv1dArgs a, int pieces, int runs) {
+__global__ __launch_bounds__(kThreads) void conv1d_fwd(Conv1dArgs a, int pieces, int runs, int len) {
   const long long id = ((long long)blockIdx.z * gridDim.x + blockIdx.x) * kThreads + threadIdx.x;
   if (id >= (long long)pieces * runs) return;
   const int run = (int)(id / pieces), piece = (int)(id - (long long)run * pieces);
@@ -64,7 +72,7 @@ __global__ __launch_bounds__(kThreads) void conv1d_fwd(Conv1dArgs a, int pieces,
   const T* x = (const T*)a.x + (long long)b * a.N * a.xs + c0;
   const T* state = a.state ? (const T*)a.state + (long long)b * (K - 1) * C + c0 : nullptr;
   T* y = (T*)a.y + (long long)b * a.N * C + c0;
-  const int t0 = run * kRun, t1 = min(a.N, t0 + kRun);
+  const int t0 = run * len, t1 = min(a.N, t0 + len);
   Raw<T, V> next[kAhead];
   auto fetch = [&](int t) {
 #pragma unroll
@@ -127,20 +135,20 @@ __global__ __launch_bounds__(kThreads) void conv1d_step(Conv1dArgs a, int pieces
 // Workgroup: kPieces pieces of the row x kRuns runs of one sequence. Partial row (b, run group):
 // [K + 1][C], the K sums of dw and that of db.
 template <class T, int V, int K, bool SILU>
-__global__ __launch_bounds__(kThreads) void conv1d_bwd(Conv1dArgs a, int pieces) {
+__global__ __launch_bounds__(kThreads) void conv1d_bwd(Conv1dArgs a, int pieces, int len) {
   __shared__ float join[kRuns][kPieces * V];
-  const int piece = blockIdx.x * kPieces + threadIdx.x % kPieces, sub = threadIdx.x / kPieces;
+  const int piece = blockIdx.y * kPieces + threadIdx.x % kPieces, sub = threadIdx.x / kPieces;
   const int b = blockIdx.z, C = a.C, c0 = piece * V;
   const bool live = piece < pieces;
   float acc[K + 1][V] = {};
-  const long long first = ((long long)blockIdx.y * kRuns + sub) * kRun;
+  const long long first = ((long long)blockIdx.x * kRuns + sub) * len;
   if (live && first < a.N) {
     const int n = length_of(a.lengths, b, a.N);
     const T* x = (const T*)a.x + (long long)b * a.N * a.xs + c0;
     const T* state = a.state ? (const T*)a.state + (long long)b * (K - 1) * C + c0 : nullptr;
     const T* dy = (const T*)a.dy + (long long)b * a.N * C + c0;
     T* dx = (T*)a.dx + (long long)b * a.N * C + c0;
-    const int t0 = (int)first, t1 = min(a.N, t0 + kRun);
+    const int t0 = (int)first, t1 = min(a.N, t0 + len);
     Raw<T, V> nx[kAhead], nd[kAhead];
     auto fetch = [&](int t) {
 #pragma unroll
@@ -208,14 +216,14 @@ __global__ __launch_bounds__(kThreads) void conv1d_bwd(Conv1dArgs a, int pieces)
       }
     }
   }
-  float* row = a.partial + ((long long)b * gridDim.y + blockIdx.y) * (K + 1) * C;
+  float* row = a.partial + ((long long)b * gridDim.x + blockIdx.x) * (K + 1) * C;
 #pragma unroll
   for (int k = 0; k <= K; ++k) {
     __syncthreads();
     for (int i = 0; i < V; ++i) join[sub][(threadIdx.x % kPieces) * V + i] = acc[k][i];
     __syncthreads();
     for (int t = threadIdx.x; t < kPieces * V; t += kThreads) {
-      const int c = blockIdx.x * kPieces * V + t;
+      const int c = blockIdx.y * kPieces * V + t;
       if (c >= C) break;
       float s = 0.f;
       for (int q = 0; q < kRuns; ++q) s += join[q][t];
@@ -244,7 +252,10 @@ bool vector_rows(bool bf, const Conv1dArgs& a) {
   return a.C % 4 == 0 && a.xs % 4 == 0 && at % (bf ? 8 : 16) == 0;
 }
 
-int run_groups(int N) { return (int)(((long long)N + kRun * kRuns - 1) / (kRun * kRuns)); }
+int run_groups(int B, int N, int C) {
+  const int per = run_length(B, N, C) * kRuns;
+  return (int)(((long long)N + per - 1) / per);
+}
 
 // Calls f.run<T, V, K, SILU>().
 template <class F>
@@ -267,11 +278,11 @@ struct FwdCall {
   hipStream_t st;
   template <class T, int V, int K, bool SILU>
   hipError_t run() const {
-    const int pieces = a.C / V, runs = (a.N + kRun - 1) / kRun;
+    const int pieces = a.C / V, len = run_length(a.B, a.N, a.C), runs = (a.N + len - 1) / len;
     const long long blocks = ((long long)pieces * runs + kThreads - 1) / kThreads;
     const dim3 g = wide_grid(blocks);
     hipLaunchKernelGGL((conv1d_fwd<T, V, K, SILU>), dim3(g.x, (unsigned)a.B, g.y), dim3(kThreads), 0, st, a, pieces,
-                       runs);
+                       runs, len);
     return hipGetLastError();
   }
 };
@@ -293,9 +304,10 @@ struct BwdCall {
   hipStream_t st;
   template <class T, int V, int K, bool SILU>
   hipError_t run() const {
-    const int pieces = a.C / V, groups = run_groups(a.N);
-    const dim3 grid((unsigned)((pieces + kPieces - 1) / kPieces), (unsigned)groups, (unsigned)a.B);
-    hipLaunchKernelGGL((conv1d_bwd<T, V, K, SILU>), grid, dim3(kThreads), 0, st, a, pieces);
+    const int pieces = a.C / V, groups = run_groups(a.B, a.N, a.C);
+    const dim3 grid((unsigned)groups, (unsigned)((pieces + kPieces - 1) / kPieces), (unsigned)a.B);
+    hipLaunchKernelGGL((conv1d_bwd<T, V, K, SILU>), grid, dim3(kThreads), 0, st, a, pieces,
+                       run_length(a.B, a.N, a.C));
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     return column_sum_launch(a.partial, (long long)a.B * groups, (K + 1) * a.C, StoreConvGrads<K>{a.dw, a.db, a.C}, st);
@@ -313,7 +325,7 @@ hipError_t conv1d_step_launch(bool bf16_io, int K, bool silu, const Conv1dArgs& 
 }
 
 size_t conv1d_bwd_workspace_bytes(bool, int B, int N, int C, int K) {
-  return (size_t)B * run_groups(N) * (K + 1) * C * sizeof(float);
+  return (size_t)B * run_groups(B, N, C) * (K + 1) * C * sizeof(float);
 }
 
 hipError_t conv1d_bwd_launch(bool bf16_io, int K, bool silu, const Conv1dArgs& a, hipStream_t st) {
