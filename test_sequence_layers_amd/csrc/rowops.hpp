@@ -110,21 +110,20 @@ inline dim3 wide_grid(long long blocks) {
 }
 __device__ __forceinline__ long long wide_block() { return (long long)blockIdx.y * gridDim.x + blockIdx.x; }
 
-// Sum of P rows of W fp32 values, fixed order: thread row ty of kSumRows adds rows ty, ty + kSumRows, ...,
-// then its sums are added in order. out(column, sum) stores it. Few columns per workgroup: a narrow
-// matrix of many rows is spread over more CUs, and a thread has a few rounds of loads at most.
-constexpr int kSumCols = 16, kSumRows = 64;
+// Sum of P rows of W fp32 values in a fixed order: thread row ty of kSumRows adds rows ty, ty + kSumRows, ...,
+// then the thread rows are added pairwise. out(column, sum) stores it. Few columns per workgroup: a
+// narrow matrix of many rows is spread over more CUs, and a thread has a few rounds of loads at most.
+constexpr int kSumCols = 16, kSumRows = 64, kSumThreads = kSumCols * kSumRows;
 template <class Out>
-__global__ __launch_bounds__(kSumCols* kSumRows) void column_sum(const float* __restrict__ part,
-                                                                 long long P, int W, Out out) {
+__device__ __forceinline__ void column_sum_block(const float* __restrict__ part, long long P, int W, int block,
+                                                 const Out& out) {
   __shared__ float sm[kSumRows][kSumCols];
   const int tx = threadIdx.x % kSumCols, ty = threadIdx.x / kSumCols;
-  const int col = blockIdx.x * kSumCols + tx;
+  const int col = block * kSumCols + tx;
   float acc = 0.f;
   if (col < W) {
     const float* p = part + col;
-    long long r = ty;
-    for (; r < P; r += 8 * kSumRows) {
+    for (long long r = ty; r < P; r += 8 * kSumRows) {
       float v[8];
       for (int i = 0; i < 8; ++i) {
         const long long k = r + i * kSumRows;
@@ -134,16 +133,21 @@ __global__ __launch_bounds__(kSumCols* kSumRows) void column_sum(const float* __
     }
   }
   sm[ty][tx] = acc;
-  __syncthreads();
-  if (ty == 0 && col < W) {
-    for (int i = 1; i < kSumRows; ++i) acc += sm[i][tx];
-    out(col, acc);
+  for (int step = kSumRows / 2; step > 0; step /= 2) {
+    __syncthreads();
+    if (ty < step) sm[ty][tx] += sm[ty + step][tx];
   }
+  if (ty == 0 && col < W) out(col, sm[0][tx]);
+}
+inline int column_sum_blocks(int W) { return (W + kSumCols - 1) / kSumCols; }
+
+template <class Out>
+__global__ __launch_bounds__(kSumThreads) void column_sum(const float* __restrict__ part, long long P, int W, Out out) {
+  column_sum_block(part, P, W, blockIdx.x, out);
 }
 template <class Out>
 hipError_t column_sum_launch(const float* part, long long P, int W, Out out, hipStream_t st) {
-  hipLaunchKernelGGL(column_sum<Out>, dim3((unsigned)((W + kSumCols - 1) / kSumCols)), dim3(kSumCols * kSumRows), 0,
-                     st, part, P, W, out);
+  hipLaunchKernelGGL(column_sum<Out>, dim3((unsigned)column_sum_blocks(W)), dim3(kSumThreads), 0, st, part, P, W, out);
   return hipGetLastError();
 }
 

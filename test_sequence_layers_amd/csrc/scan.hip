@@ -679,22 +679,6 @@ __global__ __launch_bounds__(64 * Bwd<S>::NW) void scan_bwd(ScanArgs a, Plan p, 
   }
 }
 
-// dB and dC: the channel blocks of a group summed. One thread per (b, n, matrix, g, s).
-template <class T>
-__global__ __launch_bounds__(256) void scan_bwd_mats(const float* __restrict__ mats, T* __restrict__ dB,
-                                                     T* __restrict__ dC, long long rows, int G, int S,
-                                                     int cbg) {
-  const long long id = wide_block() * 256 + threadIdx.x;
-  const int width = 2 * G * S;
-  if (id >= rows * width) return;
-  const long long row = id / width;
-  const int r = (int)(id - row * width), which = r / (G * S), gs = r - which * G * S, g = gs / S, s = gs - g * S;
-  const float* m = mats + ((row * G + g) * cbg * 2 + which) * S + s;
-  float acc = 0.f;
-  for (int k = 0; k < cbg; ++k) acc += m[(long long)k * 2 * S];
-  (which ? dC : dB)[row * G * S + gs] = (T)acc;
-}
-
 struct StoreScanGrads {
   float *dA, *dD, *ddb;
   int C, S;
@@ -706,6 +690,32 @@ struct StoreScanGrads {
     } else if (ddb) ddb[c] = v;
   }
 };
+
+// The sums that end the backward pass, in one launch: the first sum_blocks workgroups add the segments'
+// dA, dD and ddbias, the others the channel blocks of a group for dB and dC, one thread per
+// (b, n, matrix, g, s).
+template <class T>
+__global__ __launch_bounds__(kSumThreads) void scan_bwd_sums(const float* __restrict__ part, long long segs, int C,
+                                                             int sum_blocks, StoreScanGrads out,
+                                                             const float* __restrict__ mats, T* __restrict__ dB,
+                                                             T* __restrict__ dC, long long rows, int G, int S,
+                                                             int cbg) {
+  const long long block = wide_block();
+  if (block < sum_blocks) {
+    column_sum_block(part, segs, S * C + 2 * C, (int)block, out);
+    return;
+  }
+  const long long id = (block - sum_blocks) * kSumThreads + threadIdx.x;
+  const int width = 2 * G * S;
+  if (id >= rows * width) return;
+  const long long row = id / width;
+  const int r = (int)(id - row * width), which = r / (G * S), gs = r - which * G * S, g = gs / S, s = gs - g * S;
+  const float* m = mats + ((row * G + g) * cbg * 2 + which) * S + s;
+  float acc = 0.f;
+#pragma unroll 4
+  for (int k = 0; k < cbg; ++k) acc += m[(long long)k * 2 * S];
+  (which ? dC : dB)[row * G * S + gs] = (T)acc;
+}
 
 // Segments: at most `want` waves in all and at least min_tokens each, a multiple of `unit` tokens.
 Plan plan_of(int B, int N, int C, int G, int want, int min_tokens, int unit) {
@@ -814,12 +824,11 @@ hipError_t bwd(const ScanArgs& a, void* ws, hipStream_t st) {
   hipLaunchKernelGGL((scan_bwd<T, S>), dim3((unsigned)units), dim3(64 * Bwd<S>::NW), 0, st, a, p, w);
   e = hipGetLastError();
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(scan_bwd_mats<T>, wide_grid((mats + 255) / 256), dim3(256), 0, st, w.mats, (T*)a.dbm, (T*)a.dcm,
-                     (long long)a.B * a.N, a.G, S, p.cbg);
-  e = hipGetLastError();
-  if (e != hipSuccess) return e;
-  return column_sum_launch(w.part, (long long)a.B * p.nseg, S * a.C + 2 * a.C,
-                           StoreScanGrads{a.dA, a.dD, a.ddbias, a.C, S}, st);
+  const int sum_blocks = column_sum_blocks(S * a.C + 2 * a.C);
+  hipLaunchKernelGGL(scan_bwd_sums<T>, wide_grid(sum_blocks + (mats + kSumThreads - 1) / kSumThreads), dim3(kSumThreads),
+                     0, st, w.part, (long long)a.B * p.nseg, a.C, sum_blocks, StoreScanGrads{a.dA, a.dD, a.ddbias, a.C, S},
+                     w.mats, (T*)a.dbm, (T*)a.dcm, (long long)a.B * a.N, a.G, S, p.cbg);
+  return hipGetLastError();
 }
 
 }  // namespace
