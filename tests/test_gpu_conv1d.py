@@ -130,3 +130,21 @@ def test_conv1d_replayed_and_on_another_stream():
            *T.ttt_backward_conv1d(x, w, b, d_y, silu=True, state=st, lengths=ln, stream=side)]
     side.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+@pytest.mark.parametrize("B,N,C,dtype", [(2, 2049, 1028, "bf16"), (3, 4097, 1000, "fp32"), (2, 8193, 1032, "bf16")])
+def test_conv1d_long_runs(B, N, C, dtype):
+    """The sizes from which a thread walks 8, 16 and 32 tokens."""
+    print(f"conv1d B={B} N={N} C={C} {dtype}", flush=True)
+    x, d_y, w, b, st, ln = _inputs(B, N, C, 4, dtype, True, True, [N, N - 37, 5][:B], False, seed=N)
+    lengths = [N, N - 37, 5][:B]
+    end = torch.empty_like(st)
+    y = T.ttt_forward_conv1d(x, w, b, silu=True, state=st, lengths=ln, state_out=end)
+    got = T.ttt_backward_conv1d(x, w, b, d_y, silu=True, state=st, lengths=ln)
+    torch.cuda.synchronize()
+    ry, rend = O.conv1d(f64(x), f64(w), f64(b), True, f64(st), lengths)
+    check("y", y, ry, C_CONV)
+    check("state_out", end, rend, 0)
+    refs = O.conv1d_backward(f64(x), f64(w), f64(b), True, f64(d_y), f64(st), lengths)
+    for name, g, r, c in zip(("dx", "dw", "db", "dstate"), got, refs, (C_CONV, C_SUM, C_SUM, C_CONV)):
+        check(name, g, r, c)

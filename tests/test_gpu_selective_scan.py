@@ -222,3 +222,15 @@ def test_scan_replayed_and_on_another_stream():
            *T.ttt_backward_selective_scan(*_args(s), io, *par, stream=side, **more)]
     side.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+def test_scan_many_short_sequences():
+    """1664 blocks of channels: each runs its 60 tokens in one go."""
+    B, N, C, S = 26, 60, 4096, 8
+    s = _inputs(B, N, C, S, 1, "bf16", seed=12, lengths=[60 - i for i in range(B)])
+    end = torch.empty_like(s["h0"])
+    assert T.load_library().ttt_forward_selective_scan_workspace(T.TTT_BF16, B, N, C, S, 1) == 0
+    y = T.ttt_forward_selective_scan(*_args(s), s["D"], s["delta_bias"], s["z"], h0=s["h0"], lengths=s["lengths"], h_out=end)
+    ry, rend = _oracle(s, True, [60 - i for i in range(B)])
+    check("y", y, ry, C_SCAN)
+    check("h_out", end, rend, C_SCAN)
