@@ -38,7 +38,7 @@ extern "C" {
  *   y = (x - mean) / sqrt(var + eps) * weight[h] + bias[h],
  * mean and var (the population variance, from the centred values) over the D channels. H = 1 is the
  * ordinary layer norm of a row; H > 1 with D the head width norms queries or keys per head.
- * D in [1, 16384], H at most 65535, H * D at most 2^26, M * H at most 2^31 - 1; eps finite and not
+ * D in [1, 16384], H at most 65535, H * D at most 2^24, M * H at most 2^31 - 1; eps finite and not
  * negative. No workspace.
  */
 ttt_status ttt_forward_layernorm(ttt_dtype dt, int M, int H, int D, float eps, const void* x,
@@ -99,7 +99,8 @@ size_t ttt_backward_conv1d_workspace(ttt_dtype dt, int B, int N, int C, int K);
  * g = c / (C / G). u, delta, z (nullable), y: [B, N, C]; Bm, Cm: [B, N, G, S]; A: fp32 [C, S]; D,
  * delta_bias (nullable): fp32 [C]; h0 (nullable, zeros without it), h_out (nullable): fp32 [B, C, S],
  * the states before token 0 and after each sequence's last. S in {8, 16, 32, 64}; G divides C; B at
- * most 65535, N at most 2^22, C at most 2^20, B * C * (N + 4096) at most 2^38. For bf16, Bm and Cm are 4-byte aligned and their strides even.
+ * most 65535, N at most 2^22, C at most 2^20, B * C * (N + 4096) at most 2^38, B * G *
+ * ceil(C / G / 64) at most 2^20. For bf16, Bm and Cm are 4-byte aligned and their strides even.
  */
 ttt_status ttt_forward_selective_scan(ttt_dtype dt, int B, int N, int C, int S, int G, int softplus,
                                       const void* u, long long u_stride, const void* delta,

@@ -66,7 +66,7 @@ ttt_status add_workspace(Buffers& bufs, void* ws, size_t have, size_t need) {
 
 ttt_status check_layernorm_sizes(ttt_dtype dt, int M, int H, int D) {
   if (!known(dt) || M <= 0 || H <= 0 || D <= 0) return TTT_ERR_INVALID;
-  if (D > 16384 || H > 65535 || (long long)H * D > (1 << 26) || (long long)M * H > 0x7fffffffll)
+  if (D > 16384 || H > 65535 || (long long)H * D > (1 << 24) || (long long)M * H > 0x7fffffffll)
     return TTT_ERR_UNSUPPORTED;
   return TTT_OK;
 }
@@ -80,7 +80,8 @@ ttt_status check_conv1d_sizes(ttt_dtype dt, int B, int N, int C, int K) {
 ttt_status check_scan_sizes(ttt_dtype dt, int B, int N, int C, int S, int G) {
   if (!known(dt) || B <= 0 || N <= 0 || C <= 0 || S <= 0 || G <= 0 || C % G != 0) return TTT_ERR_INVALID;
   if (!ttt::scan_supported_s(S) || B > kMaxB || N > (1 << 22) || C > (1 << 20) ||
-      (double)B * C * ((double)N + 4096.) > (double)(1ll << 38))
+      (double)B * C * ((double)N + 4096.) > (double)(1ll << 38) ||
+      (long long)B * G * ((C / G + 63) / 64) > (1 << 20))
     return TTT_ERR_UNSUPPORTED;
   return TTT_OK;
 }

@@ -45,7 +45,7 @@ def _norm(dt=BF16, M=8, H=2, D=64, eps=1e-5, x=P[0], xs=128, w=P[1], b=P[2], y=P
     (dict(w=None), INVALID), (dict(y=None), INVALID), (dict(eps=-1.0), INVALID), (dict(eps=float("nan")), INVALID),
     (dict(xs=127), INVALID), (dict(xs=BIG), INVALID), (dict(x=P[0] + 1), INVALID), (dict(w=P[1] + 2), INVALID),
     (dict(y=P[0]), INVALID), (dict(y=P[2]), INVALID), (dict(D=16385, xs=40000), UNSUPPORTED),
-    (dict(H=65536, xs=BIG), UNSUPPORTED), (dict(M=1 << 30, H=2), UNSUPPORTED)])
+    (dict(H=65536, xs=BIG), UNSUPPORTED), (dict(H=4096, D=4097, xs=BIG), UNSUPPORTED), (dict(M=1 << 30, H=2), UNSUPPORTED)])
 def test_layernorm_refusals(kw, want):
     assert _norm(**kw) == want
 
