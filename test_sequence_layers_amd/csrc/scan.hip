@@ -62,11 +62,12 @@ template <class T, int SB>
 struct Piece {
   static constexpr int W = SB * (int)sizeof(T) / 4;
   uint32_t b[W], c[W];
+  template <bool WITH_C>
   __device__ __forceinline__ void load(const T* pb, const T* pc) {
     const ScalarPtr qb = (ScalarPtr)(uintptr_t)pb, qc = (ScalarPtr)(uintptr_t)pc;
 #pragma unroll
     for (int i = 0; i < W; ++i) b[i] = qb[i];
-    if (pc)
+    if constexpr (WITH_C)
 #pragma unroll
       for (int i = 0; i < W; ++i) c[i] = qc[i];
   }
@@ -89,13 +90,25 @@ __device__ __forceinline__ uint32_t lane_part(int c, int size) {
   return off;
 }
 template <class T>
-__device__ __forceinline__ float at(const T* row, int c) {
-  return (float)*reinterpret_cast<const T*>(reinterpret_cast<const char*>(row) + lane_part(c, sizeof(T)));
+__device__ __forceinline__ float at(const T* row, uint32_t off) {
+  return (float)*reinterpret_cast<const T*>(reinterpret_cast<const char*>(row) + off);
 }
 template <class T>
-__device__ __forceinline__ void put(T* row, int c, float v) {
-  *reinterpret_cast<T*>(reinterpret_cast<char*>(row) + lane_part(c, sizeof(T))) = (T)v;
+__device__ __forceinline__ void put(T* row, uint32_t off, float v) {
+  *reinterpret_cast<T*>(reinterpret_cast<char*>(row) + off) = (T)v;
 }
+
+// A row pointer that walks down the tokens (by 64-bit additions; the row of a token would take a 64-bit
+// product). It stays where it is when `on` is false.
+template <class T>
+struct Walk {
+  const char* p;
+  long long step;
+  __device__ __forceinline__ Walk(const void* base, long long stride, long long row, int col)
+      : p(reinterpret_cast<const char*>((const T*)base + row * stride + col)), step(stride * (long long)sizeof(T)) {}
+  __device__ __forceinline__ const T* row() const { return reinterpret_cast<const T*>(p); }
+  __device__ __forceinline__ void next(bool on = true) { p += on ? step : 0; }
+};
 
 // How a call is cut up. Channel blocks: 64 channels of one group each.
 struct Plan {
@@ -139,10 +152,6 @@ __global__ __launch_bounds__(64 * kWaves) void scan_fwd(ScanArgs a, Plan p, int 
   const int n = length_of(a.lengths, un.b, N);
   const int t0 = un.seg * p.T, t1 = min(N, t0 + p.T), te = min(t1, n);
   const long long row0 = (long long)un.b * N;
-  const T* u = (const T*)a.u + row0 * a.us;
-  const T* de = (const T*)a.delta + row0 * a.ds;
-  const T* bm = (const T*)a.bm + row0 * a.bs + (long long)un.g * S;
-  const T* cm = (const T*)a.cm + row0 * a.cs + (long long)un.g * S;
   T* y = (T*)a.y + row0 * C;
   const long long seg_at = ((long long)un.b * p.nseg + un.seg) * C;
 
@@ -161,16 +170,21 @@ __global__ __launch_bounds__(64 * kWaves) void scan_fwd(ScanArgs a, Plan p, int 
   // again), without a branch: behind one the loads would be waited for where it ends. Without a gate
   // u's row stands in for z's.
   const bool gate = FINAL && a.z;
-  const T* z = gate ? (const T*)a.z + row0 * a.zs : u;
-  const long long zs = gate ? a.zs : a.us;
+  Walk<T> wu(a.u, a.us, row0 + t0, 0), wd(a.delta, a.ds, row0 + t0, 0);
+  Walk<T> wz(gate ? a.z : a.u, gate ? a.zs : a.us, row0 + t0, 0);
+  Walk<T> wb(a.bm, a.bs, row0 + t0, un.g * S), wc(a.cm, a.cs, row0 + t0, un.g * S);
+  T* py = y + (long long)t0 * C;
   float nu[kTok], nd[kTok], nz[kTok];
-  auto fetch = [&](int t) {
+  int tf = t0;  // the token fetched next
+  auto fetch = [&](uint32_t off) {
 #pragma unroll
     for (int j = 0; j < kTok; ++j) {
-      const long long tt = min(t + j, te - 1);
-      nu[j] = at(u + tt * a.us, c);
-      nd[j] = at(de + tt * a.ds, c);
-      if (FINAL) nz[j] = at(z + tt * zs, c);
+      nu[j] = at(wu.row(), off);
+      nd[j] = at(wd.row(), off);
+      if (FINAL) nz[j] = at(wz.row(), off);
+      const bool more = ++tf < te;
+      wu.next(more), wd.next(more);
+      if (FINAL) wz.next(more);
     }
   };
   constexpr int SB = S < 16 ? S : 16;  // states per piece of B and C
@@ -179,14 +193,16 @@ __global__ __launch_bounds__(64 * kWaves) void scan_fwd(ScanArgs a, Plan p, int 
   // or may not be there is waited for together with it.
   auto chunk = [&](int t, auto full) {
     constexpr bool FULL = decltype(full)::value;
+    const uint32_t off = lane_part(c, sizeof(T));
     float cu[kTok], dt[kTok], cz[kTok], out[kTok];
     Piece<T, S> mats[kTok];
-    if constexpr (kAhead) {
+    const T *rb[kTok], *rc[kTok];
 #pragma unroll
-      for (int j = 0; j < kTok; ++j) {
-        const int tt = FULL ? t + j : min(t + j, te - 1);
-        mats[j].load(bm + tt * a.bs, FINAL ? cm + tt * a.cs : nullptr);
-      }
+    for (int j = 0; j < kTok; ++j) {
+      rb[j] = wb.row(), rc[j] = wc.row();
+      if constexpr (kAhead) mats[j].template load<FINAL>(rb[j], rc[j]);
+      const bool more = FULL || t + j < te - 1;
+      wb.next(more), wc.next(more);
     }
 #pragma unroll
     for (int j = 0; j < kTok; ++j) {
@@ -194,7 +210,7 @@ __global__ __launch_bounds__(64 * kWaves) void scan_fwd(ScanArgs a, Plan p, int 
       if (FINAL) cz[j] = nz[j];
       dt[j] = step_of(nd[j] + db, a.softplus);
     }
-    fetch(t + kTok);
+    fetch(off);
 #pragma unroll
     for (int j = 0; j < kTok; ++j) {
       if (FULL || t + j < te) {
@@ -204,7 +220,7 @@ __global__ __launch_bounds__(64 * kWaves) void scan_fwd(ScanArgs a, Plan p, int 
         for (int s0 = 0; s0 < S; s0 += SB) {
           float bv[SB], cv[SB];
           Piece<T, SB> part;
-          if constexpr (!kAhead) part.load(bm + (t + j) * a.bs + s0, FINAL ? cm + (t + j) * a.cs + s0 : nullptr);
+          if constexpr (!kAhead) part.template load<FINAL>(rb[j] + s0, rc[j] + s0);
           widen<T, SB>(kAhead ? mats[j].b + s0 * sizeof(T) / 4 : part.b, bv);
           if (FINAL) widen<T, SB>(kAhead ? mats[j].c + s0 * sizeof(T) / 4 : part.c, cv);
 #pragma unroll
@@ -226,16 +242,17 @@ __global__ __launch_bounds__(64 * kWaves) void scan_fwd(ScanArgs a, Plan p, int 
       for (int j = 0; j < kTok; ++j) {
         float o = fmaf(D, cu[j], out[j]);
         o = gate ? o * (cz[j] * sigmoid(cz[j])) : o;
-        if (FULL || t + j < te) put(y + (long long)(t + j) * C, c, o);
+        if (FULL || t + j < te) put(py, off, o);
+        py += C;
       }
     }
   };
-  if (t0 < te) fetch(t0);
+  if (t0 < te) fetch(lane_part(c, sizeof(T)));
   int t = t0;
   for (; t + kTok <= te; t += kTok) chunk(t, std::true_type{});
   if (t < te) chunk(t, std::false_type{});
   if (FINAL) {
-    for (int t = max(t0, te); t < t1; ++t) put(y + (long long)t * C, c, 0.f);
+    for (int t = max(t0, te); t < t1; ++t) put(y + (long long)t * C, lane_part(c, sizeof(T)), 0.f);
     if (a.h_out && un.seg == p.nseg - 1)
       for (int s = 0; s < S; ++s) a.h_out[((long long)un.b * C + c) * S + s] = h[s];
   } else {
@@ -373,14 +390,10 @@ __global__ __launch_bounds__(64 * kWaves) void scan_bwd_ends(ScanArgs a, Plan p,
   const int n = length_of(a.lengths, un.b, N);
   const int t0 = un.seg * p.T, t1 = min(N, t0 + p.T), te = min(t1, n);
   const long long row0 = (long long)un.b * N;
-  const T* u = (const T*)a.u + row0 * a.us;
-  const T* de = (const T*)a.delta + row0 * a.ds;
   const bool gate = a.z;
-  const T* z = gate ? (const T*)a.z + row0 * a.zs : u;
-  const long long zs = gate ? a.zs : a.us;
-  const T* dy = (const T*)a.dy + row0 * C;
-  const T* bm = (const T*)a.bm + row0 * a.bs + (long long)un.g * S + s0;
-  const T* cm = (const T*)a.cm + row0 * a.cs + (long long)un.g * S + s0;
+  Walk<T> wu(a.u, a.us, row0 + t0, 0), wd(a.delta, a.ds, row0 + t0, 0), wv(a.dy, C, row0 + t0, 0);
+  Walk<T> wz(gate ? a.z : a.u, gate ? a.zs : a.us, row0 + t0, 0);
+  Walk<T> wb(a.bm, a.bs, row0 + t0, un.g * S + s0), wc(a.cm, a.cs, row0 + t0, un.g * S + s0);
   float A2[SB], h[SB], P[SB], q[SB];
   for (int s = 0; s < SB; ++s) {
     A2[s] = a.A[(long long)c * S + s0 + s] * kLog2e;
@@ -395,14 +408,17 @@ __global__ __launch_bounds__(64 * kWaves) void scan_bwd_ends(ScanArgs a, Plan p,
     if (s0 == 0) w.cksum[k * C + c] = sum;
   };
   float nu[kTok], nd[kTok], nv[kTok], nz[kTok];
-  auto fetch = [&](int t) {
+  int tf = t0;
+  auto fetch = [&]() {
+    const uint32_t off = lane_part(c, sizeof(T));
 #pragma unroll
     for (int j = 0; j < kTok; ++j) {
-      const long long tt = min(t + j, te - 1);
-      nu[j] = at(u + tt * a.us, c);
-      nd[j] = at(de + tt * a.ds, c);
-      nv[j] = at(dy + tt * C, c);
-      nz[j] = at(z + tt * zs, c);
+      nu[j] = at(wu.row(), off);
+      nd[j] = at(wd.row(), off);
+      nv[j] = at(wv.row(), off);
+      nz[j] = at(wz.row(), off);
+      const bool more = ++tf < te;
+      wu.next(more), wd.next(more), wv.next(more), wz.next(more);
     }
   };
   auto chunk = [&](int t, auto full) {
@@ -411,8 +427,9 @@ __global__ __launch_bounds__(64 * kWaves) void scan_bwd_ends(ScanArgs a, Plan p,
     Piece<T, SB> mats[kTok];
 #pragma unroll
     for (int j = 0; j < kTok; ++j) {
-      const int tt = FULL ? t + j : min(t + j, te - 1);
-      mats[j].load(bm + tt * a.bs, cm + tt * a.cs);
+      mats[j].template load<true>(wb.row(), wc.row());
+      const bool more = FULL || t + j < te - 1;
+      wb.next(more), wc.next(more);
     }
 #pragma unroll
     for (int j = 0; j < kTok; ++j) {
@@ -422,7 +439,7 @@ __global__ __launch_bounds__(64 * kWaves) void scan_bwd_ends(ScanArgs a, Plan p,
     }
     // (the checkpoint's stores before the next loads: what is waited for next has them behind it anyway)
     if ((t - t0) % kSub == 0) checkpoint(t);
-    fetch(t + kTok);
+    fetch();
 #pragma unroll
     for (int j = 0; j < kTok; ++j) {
       if (FULL || t + j < te) {
@@ -440,7 +457,7 @@ __global__ __launch_bounds__(64 * kWaves) void scan_bwd_ends(ScanArgs a, Plan p,
       }
     }
   };
-  if (t0 < te) fetch(t0);
+  if (t0 < te) fetch();
   int t = t0;
   for (; t + kTok <= te; t += kTok) chunk(t, std::true_type{});
   if (t < te) chunk(t, std::false_type{});
@@ -521,8 +538,8 @@ __global__ __launch_bounds__(64 * Bwd<S>::NW) void scan_bwd(ScanArgs a, Plan p, 
   float A2[SW], hs[SW], q[SW], dA[SW];
   for (int s = 0; s < SW; ++s) {
     A2[s] = a.A[(long long)c * S + s0 + s] * kLog2e;
-    hs[s] = at(w.ends + (seg * S + s0 + s) * C, c);
-    q[s] = at(w.back + (seg * S + s0 + s) * C, c);  // a q of the token behind
+    hs[s] = w.ends[(seg * S + s0 + s) * C + c];
+    q[s] = w.back[(seg * S + s0 + s) * C + c];  // a q of the token behind
     dA[s] = 0.f;
   }
   const float db = a.dbias ? a.dbias[c] : 0.f, D = a.D ? a.D[c] : 0.f;
@@ -531,13 +548,14 @@ __global__ __launch_bounds__(64 * Bwd<S>::NW) void scan_bwd(ScanArgs a, Plan p, 
   // segment: its last row again); what is no token's is zeroed when it is used.
   float nu[TW], nd[TW], nv[TW], nz[TW], nb[EW], nc[EW], nck[SW], npast;
   auto fetch = [&](int tc) {
+    const uint32_t off = lane_part(c, sizeof(T)), off4 = lane_part(c, 4);
 #pragma unroll
     for (int j = 0; j < TW; ++j) {
       const long long t = min(tc + wave * TW + j, t1 - 1);
-      nu[j] = at(u + t * a.us, c);
-      nd[j] = at(de + t * a.ds, c);
-      nv[j] = at(dy + t * C, c);
-      nz[j] = at(z + t * zs, c);
+      nu[j] = at(u + t * a.us, off);
+      nd[j] = at(de + t * a.ds, off);
+      nv[j] = at(dy + t * C, off);
+      nz[j] = at(z + t * zs, off);
     }
 #pragma unroll
     for (int i = 0; i < EW; ++i) {
@@ -547,8 +565,8 @@ __global__ __launch_bounds__(64 * Bwd<S>::NW) void scan_bwd(ScanArgs a, Plan p, 
       nc[i] = (float)cm[t * a.cs + e % S];
     }
     const long long k = (long long)un.b * w.nsub + tc / kSub;
-    npast = at(w.cksum + k * C, c);
-    for (int s = 0; s < SW; ++s) nck[s] = at(w.ck + (k * S + s0 + s) * C, c);
+    npast = at(w.cksum + k * C, off4);
+    for (int s = 0; s < SW; ++s) nck[s] = at(w.ck + (k * S + s0 + s) * C, off4);
   };
   // Where the lane's sum over the channels goes: its token of the RB and its place in that token's row.
   const int tok = RB == 4 ? (l >> 5 & 1) | (l >> 4 & 1) << 1 : l >> 5, k = l / 2 % NV;
@@ -637,7 +655,7 @@ __global__ __launch_bounds__(64 * Bwd<S>::NW) void scan_bwd(ScanArgs a, Plan p, 
         __builtin_amdgcn_sched_barrier(0);
       }
       const float total = join_values<NV, NV>(x);
-      if (!(l & 1) && tc + jb + tok < t1) put(w.mats + ((row0 + tc + jb) * p.cb + un.cb) * 2 * S, mat_at, total);
+      if (!(l & 1) && tc + jb + tok < t1) put(w.mats + ((row0 + tc + jb) * p.cb + un.cb) * 2 * S, lane_part(mat_at, 4), total);
     }
     __syncthreads();
 #pragma unroll
@@ -659,9 +677,10 @@ __global__ __launch_bounds__(64 * Bwd<S>::NW) void scan_bwd(ScanArgs a, Plan p, 
           }
         }
         const long long row = (row0 + t) * C;
-        put((T*)a.du + row, c, du);
-        put((T*)a.ddelta + row, c, dd);
-        if (gate) put((T*)a.dz + row, c, dz);
+        const uint32_t off = lane_part(c, sizeof(T));
+        put((T*)a.du + row, off, du);
+        put((T*)a.ddelta + row, off, dd);
+        if (gate) put((T*)a.dz + row, off, dz);
       }
     }
   }
