@@ -509,7 +509,7 @@ __device__ __forceinline__ float join_values(float* x) {
 // passed through LDS with its rows of B and C; each wave's sums over its states come back the same
 // way. Tokens behind the sequence are passed over as tokens of no step and no gradient.
 template <class T, int S>
-__global__ __launch_bounds__(64 * Bwd<S>::NW) void scan_bwd(ScanArgs a, Plan p, BwdBufs w) {
+__global__ __launch_bounds__(64 * Bwd<S>::NW, S <= 32 ? 3 : 2) void scan_bwd(ScanArgs a, Plan p, BwdBufs w) {
   constexpr int SW = Bwd<S>::SW, NW = Bwd<S>::NW, kSub = Bwd<S>::kSub, kThreads = 64 * NW;
   constexpr int TW = kSub / NW;          // tokens a wave prepares and finishes
   constexpr int NV = 2 * SW;             // sums for dB and dC per token
@@ -614,7 +614,7 @@ __global__ __launch_bounds__(64 * Bwd<S>::NW) void scan_bwd(ScanArgs a, Plan p, 
         h[j][s] = fmaf(e[j][s], j ? h[j ? j - 1 : 0][s] : h0[s], dtu * bv[s]);
         y = fmaf(cv[s], h[j][s], y);
       }
-      if (gate) s_y[wave][j][l] = y;
+      s_y[wave][j][l] = y;  // (used with a gate; without a branch the tokens' work interleaves)
       if (j & 1) __builtin_amdgcn_sched_barrier(0);
     }
 #pragma unroll
@@ -665,7 +665,7 @@ __global__ __launch_bounds__(64 * Bwd<S>::NW) void scan_bwd(ScanArgs a, Plan p, 
         float du = 0.f, dd = 0.f, dz = 0.f;
         if (t < n) {
           float sq = 0.f, sr = 0.f, sy = 0.f;
-          for (int k = 0; k < NW; ++k) sq += s_q[k][i][l], sr += s_r[k][i][l], sy += gate ? s_y[k][i][l] : 0.f;
+          for (int k = 0; k < NW; ++k) sq += s_q[k][i][l], sr += s_r[k][i][l], sy += s_y[k][i][l];
           const float uu = s_u[i][l], v = s_v[i][l];
           du = fmaf(sq, s_dt[i][l], D * v);
           dd = fmaf(sq, uu, sr * kLn2) * s_g[i][l];  // (sr has A log2(e) for A)
