@@ -757,16 +757,18 @@ Plan plan_of(int B, int N, int C, int G, int want, int min_tokens, int unit) {
   p.nseg = (int)((N + T - 1) / T);
   return p;
 }
-// Forward: as many waves as 256 CUs hold at once (six per SIMD at S = 16; 4 x 8192 x 768 x 16: 216 us, against 237
-// with five, 250 with four, 226 with eight, where the last ones run in a second turn), of at least
-// 24 tokens (3 x 1999 x 1000 x 32, fp32: 105 us; 117 at 16, 132 at 32). One segment where a second run over
-// the tokens costs more than it gives: sequences of up to 48 tokens (768 channels: 32 tokens 19 us in one
-// launch and 23 in three, 64 tokens 35 and 28) and 1600 blocks of channels or more (512 tokens of 1536
-// blocks: 417 and 401 us, of 2040: 427 and 530).
-Plan fwd_plan(const ScanArgs& a) {
-  const int cb = (a.C / a.G + 63) / 64 * a.G;
-  if (a.N <= 48 || (long long)a.B * cb >= 1600) return plan_of(a.B, a.N, a.C, a.G, 1, a.N, kTokens);
-  return plan_of(a.B, a.N, a.C, a.G, 6144, 24, kTokens);
+// Forward: as many waves as 256 CUs hold at once (six per SIMD at S = 16; 4 x 8192 x 768 x 16: 183 us, against 189
+// with five or seven), of at least 24 tokens (3 x 1999 x 1000 x 32, fp32: 105 us; 115 at 28, 120 at 32). One
+// segment where a second run over the tokens costs more than it gives: for short sequences, the longer the
+// more blocks of channels there are (768 channels: 48 tokens of one sequence 24 us in one launch, 25 in
+// three, 64 tokens 31 and 24; of 24 sequences 64 tokens 32 and 31; of 64 96 tokens 57 and 61, 128 tokens 77 and
+// 74), and from the number of blocks on that keeps the SIMDs busy by itself (512 tokens, S = 16: 1536 blocks 369
+// and 338 us, 2040 375 and 443; S = 8: 1536 215 and 225; S = 32: 768 417 and 331, 900 424 and 428; S = 64: 648 683
+// and 633, 768 684 and 711).
+Plan fwd_plan(const ScanArgs& a, int S) {
+  const long long blocks = (long long)a.B * ((a.C / a.G + 63) / 64 * a.G);
+  const bool once = a.N <= 48 + blocks / 16 || blocks >= (S <= 8 ? 1500 : S <= 16 ? 1600 : S <= 32 ? 900 : 750);
+  return plan_of(a.B, a.N, a.C, a.G, once ? 1 : 6144, once ? a.N : 24, kTokens);
 }
 // Backward: 2 x 4096 x 768 x 16 takes 198 us with 4096 waves of scan_bwd_ends, 245 with twice as many;
 // 2 x 333 x 193 x 8 28 us with segments of 16 tokens, 36 at 24, 43 at 32.
@@ -802,7 +804,7 @@ hipError_t fold(const ScanArgs& a, int S, const Plan& p, float* ends, float* bac
 
 template <class T, int S>
 hipError_t fwd(const ScanArgs& a, void* ws, hipStream_t st) {
-  const Plan p = fwd_plan(a);
+  const Plan p = fwd_plan(a, S);
   const long long units = (long long)a.B * p.nseg * p.cb;
   if (units > 0x7fffffffll) return hipErrorInvalidValue;
   const dim3 grid((unsigned)((units + kWaves - 1) / kWaves)), block(64 * kWaves);
@@ -863,7 +865,7 @@ bool scan_supported_s(int S) { return S == 8 || S == 16 || S == 32 || S == 64; }
 size_t scan_workspace_bytes(bool, int B, int N, int C, int S, int G) {
   ScanArgs a{};
   a.B = B, a.N = N, a.C = C, a.G = G;
-  const Plan p = fwd_plan(a);
+  const Plan p = fwd_plan(a, S);
   return p.nseg > 1 ? (size_t)B * p.nseg * (S + 1) * C * sizeof(float) : 0;
 }
 
