@@ -1,12 +1,15 @@
-"""Build libttt.so (the HIP kernels and the C ABI) for gfx950 with hipcc, in-tree.
+"""Build libttt.so (the HIP kernels and the C ABI) for gfx950 with hipcc and _seq_native.so (seq.py's marshalling)
+with g++, in-tree.
 
     python -m test_sequence_layers_amd.build
 """
 from __future__ import annotations
 
+import importlib.util
 import os
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -15,6 +18,7 @@ BUILD_DIR = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libttt.so")
 SOURCES = ["abi.hip", "fullbatch.hip", "chunked.hip", "mlp.hip", "dwconv.hip", "grid.hip", "epilogue.hip",
            "abi_seq.hip", "layernorm.hip", "conv1d.hip", "scan.hip"]
+NATIVE = os.path.join(HERE, "_seq_native.so")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
 # Packed fp32 ops are disabled for all device code: hipcc would otherwise form v_pk_* fp32
@@ -41,6 +45,19 @@ SOURCE_FLAGS = {
 }
 
 
+def native_command(out: str) -> list:
+    """g++ on seq_native.cpp: host code only, against PyTorch's headers and libraries (which the process that
+    loads the module has loaded already)."""
+    torch = os.path.dirname(importlib.util.find_spec("torch").origin)  # (found, not imported)
+    return [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+            "-D__HIP_PLATFORM_AMD__=1", "-DUSE_ROCM=1", "-I", os.path.join(ROOT, "include"),
+            "-isystem", os.path.join(torch, "include"),
+            "-isystem", os.path.join(torch, "include", "torch", "csrc", "api", "include"),
+            "-isystem", "/opt/rocm/include", "-isystem", sysconfig.get_paths()["include"], "-Wall", "-Wextra",
+            os.path.join(CSRC, "seq_native.cpp"), "-o", out, "-L", os.path.join(torch, "lib"),
+            "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_hip"]
+
+
 def flags_for(src: str) -> list:
     return FLAGS + SOURCE_FLAGS.get(src, [])
 
@@ -53,27 +70,32 @@ def _run(cmd):
 
 
 def build(verbose: bool = False) -> str:
-    """Compile every source and link libttt.so; returns its path. Raises on failure."""
+    """Compile every source and link libttt.so and _seq_native.so; returns libttt.so's path. Raises on failure."""
     os.makedirs(BUILD_DIR, exist_ok=True)
     procs = []
     for src in SOURCES:
         obj = os.path.join(BUILD_DIR, src.replace(".hip", ".o"))
         cmd = [HIPCC, *flags_for(src), "-c", os.path.join(CSRC, src), "-o", obj]
         procs.append((src, obj, subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True)))
+    native = NATIVE + ".tmp"
+    procs.append(("seq_native.cpp", None, subprocess.Popen(native_command(native), stdout=subprocess.PIPE,
+                                                           stderr=subprocess.STDOUT, text=True)))
     objs = []
     for src, obj, p in procs:
         out, _ = p.communicate()
         out = "\n".join(ln for ln in out.splitlines() if "packed-fp32-ops" not in ln)
         if p.returncode != 0:
-            raise RuntimeError(f"hipcc failed on {src}:\n{out}")
+            raise RuntimeError(f"the compiler failed on {src}:\n{out}")
         if verbose and out.strip():
             print(out)
-        objs.append(obj)
+        if obj is not None:
+            objs.append(obj)
     tmp = LIB + ".tmp"
     rc, out = _run([HIPCC, "--offload-arch=gfx950", "-shared", "-fPIC", "-o", tmp, *objs])
     if rc != 0:
         raise RuntimeError(f"link failed:\n{out}")
     os.replace(tmp, LIB)
+    os.replace(native, NATIVE)
     return LIB
 
 
