@@ -16,8 +16,8 @@
  *   aligned (x, y, d_y, d_x and the weights), the 16-byte paths run; results are the same up to
  *   rounding either way.
  * Lengths.  `lengths` (nullable): int32 [B] on the device, sequence b's number of tokens, in [0, N]
- *   (values outside are taken as the nearer end). The tokens behind it are padding: they are not
- *   read, states pass over them, and their rows of y and of every gradient are written as zeros.
+ *   (values outside are taken as the nearer end). The tokens behind it are padding: nothing
+ *   depends on their values, states pass over them, and their rows of y and of every gradient are written as zeros.
  * Aliasing.  Outputs must not overlap any input or each other, except that a step's state may be
  *   updated in place.
  * Precision.  Everything is computed and summed in fp32 and rounded once, to nearest even, on

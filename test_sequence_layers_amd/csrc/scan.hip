@@ -12,8 +12,10 @@
 // the states stays inside the lane, and every access of u, delta, z and y is a contiguous run over
 // channels. What bounds it is the vector ALU: one exponential (half rate) and four multiplies or
 // multiply-adds per state and token, about 35 operations per token beside them, and the second run.
-// 4 x 8192 x 768 x 16, bf16, gated: 185 us (75 the first run, 15 the fold, 103 the last with the vector ALU
-// busy 80 % of the time), 201 MB at 1.1 TB/s; one run's operations alone take 77 us, the bytes 40.
+// 4 x 8192 x 768 x 16, bf16, gated: 180 us (traced one by one 74 the first run, 15 the fold, 102 the last, with
+// the vector ALU busy 90 % of the time in both runs: 88 and 116 instructions a token and wave, where the
+// recurrence and the sum over the states alone are 64 and 80), 201 MB at 1.1 TB/s; one run's operations alone
+// take 77 us, the bytes 40.
 //
 // Tried and not kept: a scalar row of B and C held one token ahead behind a scheduling barrier (259 against
 // 247 us); the waves of a workgroup on consecutive segments, joined through LDS so that the fold goes over
@@ -29,7 +31,8 @@ namespace ttt {
 namespace {
 
 constexpr int kWaves = 4;   // units per workgroup (forward)
-constexpr int kTokens = 2;  // tokens loaded ahead (4: 3 % slower, 1: 5 %)
+constexpr int kTokens = 2;  // tokens loaded ahead (4: 3 % slower, 1: 5 %; with 8 states 3 % faster at 2 x 4096 x 768,
+                            // 6 % slower at 2 x 333 x 193)
 constexpr float kLn2 = 0.693147180559945309417f;
 
 // log(1 + exp(x)) with e = exp(-|x|): max(x, 0) + log1p(e), and log1p(e) = 2 atanh(s) with s = e / (2 + e) <= 1/3,
@@ -358,9 +361,10 @@ __global__ __launch_bounds__(256) void scan_step(ScanArgs a) {
 // first token, sum_n (a_0 ... a_n) v_n C_n, whose running product shares the exponentials. scan_fold
 // joins the segments in both directions. scan_bwd then takes the sub-chunks of a segment from its
 // last to its first: it forms the sub-chunk's a and h in registers from the checkpoint (one more
-// exponential per state and token) and walks back through them. 2 x 4096 x 768 x 16, bf16, gated: 153 us (38
-// the ends, 15 the fold, 93 the walk at three waves per SIMD, 9 the last sums), the vector ALU busy about
-// 70 % of the time; one exponential less and no checkpoints would be 58 us of operations, the bytes 17.
+// exponential per state and token) and walks back through them. 2 x 4096 x 768 x 16, bf16, gated: 147 us (traced
+// one by one 38 the ends, 15 the fold, 92 the walk at three waves per SIMD, 9 the last sums), the vector ALU
+// busy 82 % of the walk and 65 % of the ends; one exponential less and no checkpoints would be 58 us of
+// operations, the bytes 17.
 
 // Tokens per sub-chunk, states per wave and waves of a scan_bwd workgroup: kSub * SW values of each of a
 // and h stay in a lane's registers.
