@@ -42,6 +42,7 @@ SOURCE_FLAGS = {
     "fullbatch.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=1"],
     "chunked.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=1", *SCHED_ILP],
     "mlp.hip": SCHED_ILP,
+    "scan.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=1"],
 }
 
 

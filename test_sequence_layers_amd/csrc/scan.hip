@@ -21,6 +21,7 @@
 // 247 us); the waves of a workgroup on consecutive segments, joined through LDS so that the fold goes over
 // groups of four (fold 15 -> 5.5 us, but the last run starts later by as much; wide states lose waves
 // to the registers it takes: 2 x 4096 x 768 x 32 119 -> 128 us).
+#include <algorithm>
 #include <type_traits>
 
 #include "internal.hpp"
@@ -60,22 +61,18 @@ __device__ __forceinline__ float step_grad_of(float raw, int softplus, float& gr
   return softplus ? dt : raw;
 }
 
-// A row piece of B and of C that is the same for the whole wave, as raw dwords by scalar loads: those of a
-// chunk's tokens are asked for together, before the chunk's steps are computed, as far as SGPRs hold
-// them (4 x 8192 x 768 x 16, bf16: 196 us, against 211 with each token's asked for where it is used).
+// A row piece of B or of C that is the same for the whole wave, as raw dwords by scalar loads: those of a chunk's
+// tokens are asked for together, before the chunk's steps are computed, as far as SGPRs hold them
+// (4 x 8192 x 768 x 16, bf16: 196 us, against 211 with each token's asked for where it is used).
 typedef const __attribute__((address_space(4))) uint32_t* ScalarPtr;
 template <class T, int SB>
 struct Piece {
   static constexpr int W = SB * (int)sizeof(T) / 4;
-  uint32_t b[W], c[W];
-  template <bool WITH_C>
-  __device__ __forceinline__ void load(const T* pb, const T* pc) {
-    const ScalarPtr qb = (ScalarPtr)(uintptr_t)pb, qc = (ScalarPtr)(uintptr_t)pc;
+  uint32_t w[W];
+  __device__ __forceinline__ void load(const T* p) {
+    const ScalarPtr q = (ScalarPtr)(uintptr_t)p;
 #pragma unroll
-    for (int i = 0; i < W; ++i) b[i] = qb[i];
-    if constexpr (WITH_C)
-#pragma unroll
-      for (int i = 0; i < W; ++i) c[i] = qc[i];
+    for (int i = 0; i < W; ++i) w[i] = q[i];
   }
 };
 template <class T, int SB>
@@ -86,6 +83,24 @@ __device__ __forceinline__ void widen(const uint32_t* w, float* out) {
     else out[i] = __uint_as_float(i & 1 ? w[i / 2] & 0xffff0000u : w[i / 2] << 16);
   }
 }
+
+// acc[s] += row[s] * x over 4 NB states, a lane's channel having its own x: the outer product of a row of B
+// (state s in the lanes s of 64, from 4 AT on) and the wave's channels. Four states by one v_mfma_f32_4x4x1 of 16
+// blocks: a block is four lanes, its rows four states, its columns the lanes' channels, and all blocks take the
+// rows of the one that AT names. The products are fused and rounded once, as fmaf's are.
+template <int AT, int NB>
+__device__ __forceinline__ void outer(float row, float x, f32x4* acc) {
+  acc[0] = __builtin_amdgcn_mfma_f32_4x4x1f32(row, x, acc[0], 4, AT, 0);
+  if constexpr (NB > 1) outer<AT + 1, NB - 1>(row, x, acc + 1);
+}
+
+// Where a row of B is 64 bytes or more it comes as one element per lane and through outer(): as scalars, two such
+// rows a token are more than the SGPRs hold ahead of their use. 768 channels, without and with it: 4 x 8192 tokens of
+// 32 states, bf16, 323 and 304 us; 2 x 2048 of 64 states 136 and 106 (bf16), 155 and 106 (fp32); 2 x 4096 of 16
+// states, fp32, 75 and 71. Narrower rows gain nothing, since an outer product takes as long as its four
+// multiplications (16 cycles): 32768 x 1536 of 16 states, bf16, 325 and 336; 4 x 8192 of 8, fp32, 132 and 135.
+template <class T, int S>
+constexpr bool outer_rows = S * sizeof(T) >= 64;
 
 // Channel c of a row that is the same for the whole wave: the row's address in SGPRs, the lane's part of it
 // in one 32-bit register. (The empty asm keeps the two apart: added up ahead of the loop they would be a
@@ -150,7 +165,7 @@ template <class T, int S, bool FINAL>
 __global__ __launch_bounds__(64 * kWaves) void scan_fwd(ScanArgs a, Plan p, int units, float* __restrict__ ends,
                                                         float* __restrict__ sums) {
   constexpr int kTok = S <= 16 ? kTokens : 1;  // (wide states leave no registers for more)
-  constexpr bool kAhead = 2 * kTok * S * sizeof(T) <= 256;
+  constexpr bool kOuter = outer_rows<T, S>;
   const int id = blockIdx.x * kWaves + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   if (id >= units) return;
   const Unit un = unit_of(id, p, a.C, a.G);
@@ -161,14 +176,15 @@ __global__ __launch_bounds__(64 * kWaves) void scan_fwd(ScanArgs a, Plan p, int 
   T* y = (T*)a.y + row0 * C;
   const long long seg_at = ((long long)un.b * p.nseg + un.seg) * C;
 
-  float A2[S], h[S];
+  float A2[S];
+  f32x4 h[S / 4];
   for (int s = 0; s < S; ++s) A2[s] = a.A[(long long)c * S + s] * kLog2e;
   if (FINAL && p.nseg > 1) {
-    for (int s = 0; s < S; ++s) h[s] = ends[seg_at * S + (long long)s * C + c];
+    for (int s = 0; s < S; ++s) h[s / 4][s % 4] = ends[seg_at * S + (long long)s * C + c];
   } else if (FINAL && a.h0) {
-    for (int s = 0; s < S; ++s) h[s] = a.h0[((long long)un.b * C + c) * S + s];
+    for (int s = 0; s < S; ++s) h[s / 4][s % 4] = a.h0[((long long)un.b * C + c) * S + s];
   } else {
-    for (int s = 0; s < S; ++s) h[s] = 0.f;
+    for (int s = 0; s < S; ++s) h[s / 4][s % 4] = 0.f;
   }
   const float db = a.dbias ? a.dbias[c] : 0.f, D = FINAL && a.D ? a.D[c] : 0.f;
   float sum = 0.f;
@@ -180,39 +196,41 @@ __global__ __launch_bounds__(64 * kWaves) void scan_fwd(ScanArgs a, Plan p, int 
   Walk<T> wz(gate ? a.z : a.u, gate ? a.zs : a.us, row0 + t0, 0);
   Walk<T> wb(a.bm, a.bs, row0 + t0, un.g * S), wc(a.cm, a.cs, row0 + t0, un.g * S);
   T* py = y + (long long)t0 * C;
-  float nu[kTok], nd[kTok], nz[kTok];
+  float nu[kTok], nd[kTok], nz[kTok], nb[kTok];  // nb: state l % S of the token's B in lane l, when kOuter
   int tf = t0;  // the token fetched next
   auto fetch = [&](uint32_t off) {
+    uint32_t off_b = 0;
+    if constexpr (kOuter) off_b = lane_part(lane_id() % S, sizeof(T));
 #pragma unroll
     for (int j = 0; j < kTok; ++j) {
       nu[j] = at(wu.row(), off);
       nd[j] = at(wd.row(), off);
+      if (kOuter) nb[j] = at(wb.row(), off_b);
       if (FINAL) nz[j] = at(wz.row(), off);
       const bool more = ++tf < te;
       wu.next(more), wd.next(more);
+      if (kOuter) wb.next(more);
       if (FINAL) wz.next(more);
     }
   };
-  constexpr int SB = S < 16 ? S : 16;  // states per piece of B and C
   // kTok tokens from t on (all there when FULL). Lanes past their group repeat its block's first channel
   // in everything, stores too, so that the stores need no branch either: a load behind a store that may
   // or may not be there is waited for together with it.
   auto chunk = [&](int t, auto full) {
     constexpr bool FULL = decltype(full)::value;
     const uint32_t off = lane_part(c, sizeof(T));
-    float cu[kTok], dt[kTok], cz[kTok], out[kTok];
-    Piece<T, S> mats[kTok];
-    const T *rb[kTok], *rc[kTok];
+    float cu[kTok], dt[kTok], cz[kTok], cb[kTok], out[kTok];
+    Piece<T, S> pb[kTok], pc[kTok];
 #pragma unroll
     for (int j = 0; j < kTok; ++j) {
-      rb[j] = wb.row(), rc[j] = wc.row();
-      if constexpr (kAhead) mats[j].template load<FINAL>(rb[j], rc[j]);
       const bool more = FULL || t + j < te - 1;
-      wb.next(more), wc.next(more);
+      if constexpr (!kOuter) pb[j].load(wb.row()), wb.next(more);
+      if constexpr (FINAL) pc[j].load(wc.row()), wc.next(more);
     }
 #pragma unroll
     for (int j = 0; j < kTok; ++j) {
       cu[j] = nu[j];
+      if (kOuter) cb[j] = nb[j];
       if (FINAL) cz[j] = nz[j];
       dt[j] = step_of(nd[j] + db, a.softplus);
     }
@@ -221,26 +239,28 @@ __global__ __launch_bounds__(64 * kWaves) void scan_fwd(ScanArgs a, Plan p, int 
     for (int j = 0; j < kTok; ++j) {
       if (FULL || t + j < te) {
         const float dtu = dt[j] * cu[j];
-        float o0 = 0.f, o1 = 0.f;
+        float mat[S];
+        if constexpr (kOuter) {
 #pragma unroll
-        for (int s0 = 0; s0 < S; s0 += SB) {
-          float bv[SB], cv[SB];
-          Piece<T, SB> part;
-          if constexpr (!kAhead) part.template load<FINAL>(rb[j] + s0, rc[j] + s0);
-          widen<T, SB>(kAhead ? mats[j].b + s0 * sizeof(T) / 4 : part.b, bv);
-          if (FINAL) widen<T, SB>(kAhead ? mats[j].c + s0 * sizeof(T) / 4 : part.c, cv);
+          for (int s = 0; s < S; ++s) h[s / 4][s % 4] *= exp2_hw(dt[j] * A2[s]);
+          outer<0, S / 4>(cb[j], dtu, h);
+        } else {
+          widen<T, S>(pb[j].w, mat);
 #pragma unroll
-          for (int s = 0; s < SB; ++s) {
-            float& x = h[s0 + s];
-            x = fmaf(exp2_hw(dt[j] * A2[s0 + s]), x, dtu * bv[s]);
-            if (FINAL) {
-              float& o = s & 1 ? o1 : o0;
-              o = fmaf(cv[s], x, o);
-            }
+          for (int s = 0; s < S; ++s) {
+            h[s / 4][s % 4] = fmaf(exp2_hw(dt[j] * A2[s]), h[s / 4][s % 4], dtu * mat[s]);
           }
         }
-        out[j] = o0 + o1;
+        if constexpr (FINAL) {
+          float o[2] = {};
+          widen<T, S>(pc[j].w, mat);
+#pragma unroll
+          for (int s = 0; s < S; ++s) o[s & 1] = fmaf(mat[s], h[s / 4][s % 4], o[s & 1]);
+          out[j] = o[0] + o[1];
+        }
         if (!FINAL) sum += dt[j];
+        // (64 states: 106 us with a token's work kept together, 115 mixed with the next one's)
+        if (kOuter) __builtin_amdgcn_sched_barrier(0);
       }
     }
     if (FINAL) {
@@ -260,9 +280,9 @@ __global__ __launch_bounds__(64 * kWaves) void scan_fwd(ScanArgs a, Plan p, int 
   if (FINAL) {
     for (int t = max(t0, te); t < t1; ++t) put(y + (long long)t * C, lane_part(c, sizeof(T)), 0.f);
     if (a.h_out && un.seg == p.nseg - 1)
-      for (int s = 0; s < S; ++s) a.h_out[((long long)un.b * C + c) * S + s] = h[s];
+      for (int s = 0; s < S; ++s) a.h_out[((long long)un.b * C + c) * S + s] = h[s / 4][s % 4];
   } else {
-    for (int s = 0; s < S; ++s) ends[seg_at * S + (long long)s * C + c] = h[s];
+    for (int s = 0; s < S; ++s) ends[seg_at * S + (long long)s * C + c] = h[s / 4][s % 4];
     sums[seg_at + c] = sum;
   }
 }
@@ -434,10 +454,11 @@ __global__ __launch_bounds__(64 * kWaves) void scan_bwd_ends(ScanArgs a, Plan p,
   auto chunk = [&](int t, auto full) {
     constexpr bool FULL = decltype(full)::value;
     float dtu[kTok], dt[kTok], v[kTok];
-    Piece<T, SB> mats[kTok];
+    Piece<T, SB> pb[kTok], pc[kTok];
 #pragma unroll
     for (int j = 0; j < kTok; ++j) {
-      mats[j].template load<true>(wb.row(), wc.row());
+      pb[j].load(wb.row());
+      pc[j].load(wc.row());
       const bool more = FULL || t + j < te - 1;
       wb.next(more), wc.next(more);
     }
@@ -454,8 +475,8 @@ __global__ __launch_bounds__(64 * kWaves) void scan_bwd_ends(ScanArgs a, Plan p,
     for (int j = 0; j < kTok; ++j) {
       if (FULL || t + j < te) {
         float bv[SB], cv[SB];
-        widen<T, SB>(mats[j].b, bv);
-        widen<T, SB>(mats[j].c, cv);
+        widen<T, SB>(pb[j].w, bv);
+        widen<T, SB>(pc[j].w, cv);
 #pragma unroll
         for (int s = 0; s < SB; ++s) {
           const float e = exp2_hw(dt[j] * A2[s]);
@@ -761,8 +782,10 @@ Plan plan_of(int B, int N, int C, int G, int want, int min_tokens, int unit) {
   p.nseg = (int)((N + T - 1) / T);
   return p;
 }
-// Forward: as many waves as 256 CUs hold at once (six per SIMD at S = 16; 4 x 8192 x 768 x 16: 183 us, against 189
-// with five or seven), of at least 24 tokens (3 x 1999 x 1000 x 32, fp32: 105 us; 115 at 28, 120 at 32). One
+// Forward: three waves per SIMD, and more where segments stay longer than 64 tokens, up to six: segments cost
+// the fold's traffic and their start, waves hide what a token waits for (768 channels, bf16, 16 states, three and
+// six: 2 x 4096 tokens 68 and 72 us, 4 x 8192 189 and 183). Sequences of their own lengths end early, and their waves
+// with them: there four, of at least 24 tokens (3 x <= 1999 x 1000 x 32, fp32: 90 us, 100 with three). One
 // segment where a second run over the tokens costs more than it gives: for short sequences, the longer the
 // more blocks of channels there are (768 channels: 48 tokens of one sequence 24 us in one launch, 25 in
 // three, 64 tokens 31 and 24; of 24 sequences 64 tokens 32 and 31; of 64 96 tokens 57 and 61, 128 tokens 77 and
@@ -772,7 +795,9 @@ Plan plan_of(int B, int N, int C, int G, int want, int min_tokens, int unit) {
 Plan fwd_plan(const ScanArgs& a, int S) {
   const long long blocks = (long long)a.B * ((a.C / a.G + 63) / 64 * a.G);
   const bool once = a.N <= 48 + blocks / 16 || blocks >= (S <= 8 ? 1500 : S <= 16 ? 1600 : S <= 32 ? 900 : 750);
-  return plan_of(a.B, a.N, a.C, a.G, once ? 1 : 6144, once ? a.N : 24, kTokens);
+  if (once) return plan_of(a.B, a.N, a.C, a.G, 1, a.N, kTokens);
+  const long long by_length = std::min(6144ll, blocks * (a.N / 64));
+  return plan_of(a.B, a.N, a.C, a.G, (int)std::max(by_length, a.lengths ? 4096ll : 3072ll), 24, kTokens);
 }
 // Backward: 2 x 4096 x 768 x 16 takes 198 us with 4096 waves of scan_bwd_ends, 245 with twice as many;
 // 2 x 333 x 193 x 8 28 us with segments of 16 tokens, 36 at 24, 43 at 32.
@@ -869,8 +894,11 @@ bool scan_supported_s(int S) { return S == 8 || S == 16 || S == 32 || S == 64; }
 size_t scan_workspace_bytes(bool, int B, int N, int C, int S, int G) {
   ScanArgs a{};
   a.B = B, a.N = N, a.C = C, a.G = G;
-  const Plan p = fwd_plan(a, S);
-  return p.nseg > 1 ? (size_t)B * p.nseg * (S + 1) * C * sizeof(float) : 0;
+  const int any = 0;
+  int nseg = fwd_plan(a, S).nseg;
+  a.lengths = &any;  // (not read: the plan of a call with lengths may have more segments)
+  nseg = std::max(nseg, fwd_plan(a, S).nseg);
+  return nseg > 1 ? (size_t)B * nseg * (S + 1) * C * sizeof(float) : 0;
 }
 
 size_t scan_bwd_workspace_bytes(bool, int B, int N, int C, int S, int G) {

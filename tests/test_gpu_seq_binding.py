@@ -130,3 +130,30 @@ def test_calls_from_several_threads():
     for t in threads:
         t.join()
     assert not bad
+
+
+@pytest.mark.parametrize("B,N,C,S,G,dtype", [(1, 700, 130, 8, 2, "bf16"), (2, 1000, 64, 16, 1, "fp32"), (3, 257, 100, 32, 1, "bf16"),
+                                             (1, 5000, 64, 64, 1, "fp32"), (2, 49, 65, 64, 1, "bf16")])
+def test_workspaces_are_enough_and_not_left(B, N, C, S, G, dtype):
+    """Each call with a workspace of exactly the size that is asked for, inside a larger buffer: the same results as with
+    a workspace of the binding's own, and the bytes around it as they were. With lengths as without."""
+    print(f"workspaces B={B} N={N} C={C} S={S} G={G} {dtype}", flush=True)
+    io, code, lib = (torch.bfloat16, T.TTT_BF16, T.load_library()) if dtype == "bf16" else (torch.float32, T.TTT_F32, T.load_library())
+    s = {k: v if k in ("A", "D", "delta_bias") else v.to(io) for k, v in _scan(B, N, C, S, G).items()}
+    lengths = torch.tensor([N - 3 * b for b in range(B)], dtype=torch.int32, device="cuda")
+    u, w, cw, dy = s["u"], torch.ones(C, device="cuda"), torch.ones(C, 4, device="cuda"), s["z"]
+    for need, call in (
+            (lib.ttt_forward_selective_scan_workspace(code, B, N, C, S, G), lambda **k: (T.ttt_forward_selective_scan(**s, **k),)),
+            (lib.ttt_forward_selective_scan_workspace(code, B, N, C, S, G),
+             lambda **k: (T.ttt_forward_selective_scan(**s, lengths=lengths, **k),)),
+            (lib.ttt_backward_selective_scan_workspace(code, B, N, C, S, G),
+             lambda **k: T.ttt_backward_selective_scan(**s, d_y=dy, lengths=lengths, **k)),
+            (lib.ttt_backward_conv1d_workspace(code, B, N, C, 4), lambda **k: T.ttt_backward_conv1d(u, cw, w, dy, silu=True, **k)),
+            (lib.ttt_backward_layernorm_workspace(code, B * N, 1, C), lambda **k: T.ttt_backward_layernorm(u, w, dy, **k))):
+        around = torch.full((need + 8192,), 0x5A, dtype=torch.uint8, device="cuda")
+        got, want = call(workspace=around[4096:4096 + need] if need else None), call()
+        assert all((a is None and b is None) or torch.equal(a, b) for a, b in zip(got, want))
+        assert bool((around[:4096] == 0x5A).all()) and bool((around[4096 + need:] == 0x5A).all())
+        if need:
+            with pytest.raises(T.TTTError):
+                call(workspace=around[4096:4096 + need - 256])
