@@ -94,13 +94,14 @@ __device__ __forceinline__ void outer(float row, float x, f32x4* acc) {
   if constexpr (NB > 1) outer<AT + 1, NB - 1>(row, x, acc + 1);
 }
 
-// Where a row of B is 64 bytes or more it comes as one element per lane and through outer(): as scalars, two such
-// rows a token are more than the SGPRs hold ahead of their use. 768 channels, without and with it: 4 x 8192 tokens of
-// 32 states, bf16, 323 and 304 us; 2 x 2048 of 64 states 136 and 106 (bf16), 155 and 106 (fp32); 2 x 4096 of 16
-// states, fp32, 75 and 71. Narrower rows gain nothing, since an outer product takes as long as its four
-// multiplications (16 cycles): 32768 x 1536 of 16 states, bf16, 325 and 336; 4 x 8192 of 8, fp32, 132 and 135.
-template <class T, int S>
-constexpr bool outer_rows = S * sizeof(T) >= 64;
+// Where B comes as one element per lane and through outer(), instead of as scalars: where a token's scalars would be
+// more than the SGPRs hold ahead of their use. In the last run, which has C's as well, always (768 channels, bf16,
+// without and with it: 2 x 4096 tokens of 8 states 52 and 48 us, of 16 69 and 66; 3 x 1999 x 1000 of 32, fp32, its last
+// run 52 and 36; but 32768 x 1536 of 16 320 and 327). In the first from 64 bytes on (2 x 2048 tokens of 64 states, bf16, 121
+// and 107 us, 4 x 8192 of 32, bf16, 307 and 303; but of 16, traced, 75 and 79): an outer product takes as long as its
+// four multiplications (16 cycles).
+template <class T, int S, bool FINAL>
+constexpr bool outer_rows = FINAL || S * sizeof(T) >= 64;
 
 // Channel c of a row that is the same for the whole wave: the row's address in SGPRs, the lane's part of it
 // in one 32-bit register. (The empty asm keeps the two apart: added up ahead of the loop they would be a
@@ -165,7 +166,7 @@ template <class T, int S, bool FINAL>
 __global__ __launch_bounds__(64 * kWaves) void scan_fwd(ScanArgs a, Plan p, int units, float* __restrict__ ends,
                                                         float* __restrict__ sums) {
   constexpr int kTok = S <= 16 ? kTokens : 1;  // (wide states leave no registers for more)
-  constexpr bool kOuter = outer_rows<T, S>;
+  constexpr bool kOuter = outer_rows<T, S, FINAL>;
   const int id = blockIdx.x * kWaves + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   if (id >= units) return;
   const Unit un = unit_of(id, p, a.C, a.G);
@@ -799,9 +800,24 @@ Plan fwd_plan(const ScanArgs& a, int S) {
   const long long by_length = std::min(6144ll, blocks * (a.N / 64));
   return plan_of(a.B, a.N, a.C, a.G, (int)std::max(by_length, a.lengths ? 4096ll : 3072ll), 24, kTokens);
 }
-// Backward: 2 x 4096 x 768 x 16 takes 198 us with 4096 waves of scan_bwd_ends, 245 with twice as many;
-// 2 x 333 x 193 x 8 28 us with segments of 16 tokens, 36 at 24, 43 at 32.
-Plan bwd_plan(const ScanArgs& a) { return plan_of(a.B, a.N, a.C, a.G, 4096, 16, kBwdSub); }
+// Backward. The walk's workgroups come in rounds of as many as the CUs hold (by its registers 12 waves a CU, 8 with 64
+// states; a workgroup is S / 4 waves, or 8), and a round takes as long as its segments: of the segment lengths from
+// the shortest to twice that, the one whose rounds take the fewest tokens in all. The shortest is 16 tokens (2 x 333 x
+// 193 x 8 28 us, 36 at 24, 43 at 32) or what 4096 segments leave, 1536 of wide states, whose segments cost more in the
+// fold and in partial sums: 2 x 4096 x 768 x 32, bf16, 280 us, 309 with 4096; x 64 485 and 538; 8 x 1024 x 512 x 32, where
+// 22 segments of 48 tokens are 5.5 rounds and 16 of 64 are 4, 213 and 191.
+Plan bwd_plan(const ScanArgs& a, int S) {
+  Plan p = plan_of(a.B, a.N, a.C, a.G, S <= 16 ? 4096 : 1536, 16, kBwdSub);
+  const long long blocks = (long long)a.B * p.cb, slots = 256 * (S <= 8 ? 6 : S <= 16 ? 3 : 1);
+  const int shortest = p.T, step = (shortest / 32 + kBwdSub) / kBwdSub * kBwdSub;
+  long long best = -1;
+  for (int T = shortest; T <= 2 * shortest; T += step) {
+    const int nseg = (a.N + T - 1) / T;
+    const long long tokens = (blocks * nseg + slots - 1) / slots * std::min(T, a.N);
+    if (best < 0 || tokens < best) best = tokens, p.T = T, p.nseg = nseg;
+  }
+  return p;
+}
 
 size_t align_up(size_t x) { return (x + 255) / 256 * 256; }
 
@@ -864,7 +880,7 @@ hipError_t step(const ScanArgs& a, hipStream_t st) {
 template <class T, int S>
 hipError_t bwd(const ScanArgs& a, void* ws, hipStream_t st) {
   constexpr int SB = S < 16 ? S : 16;
-  const Plan p = bwd_plan(a);
+  const Plan p = bwd_plan(a, S);
   BwdBufs w;
   bwd_layout(a, S, p, static_cast<char*>(ws), &w);
   const long long units = (long long)a.B * p.nseg * p.cb;
@@ -905,7 +921,7 @@ size_t scan_bwd_workspace_bytes(bool, int B, int N, int C, int S, int G) {
   ScanArgs a{};
   a.B = B, a.N = N, a.C = C, a.G = G;
   BwdBufs w;
-  return bwd_layout(a, S, bwd_plan(a), nullptr, &w);
+  return bwd_layout(a, S, bwd_plan(a, S), nullptr, &w);
 }
 
 #define TTT_SCAN(fn, ...)                                               \
