@@ -165,7 +165,7 @@ __device__ __forceinline__ int length_of(const int* lengths, int b, int N) {
 template <class T, int S, bool FINAL>
 __global__ __launch_bounds__(64 * kWaves) void scan_fwd(ScanArgs a, Plan p, int units, float* __restrict__ ends,
                                                         float* __restrict__ sums) {
-  constexpr int kTok = S <= 16 ? kTokens : 1;  // (wide states leave no registers for more)
+  constexpr int kTok = S <= 32 ? kTokens : 1;  // (64 states leave no registers for more: 107 us, 113 with two)
   constexpr bool kOuter = outer_rows<T, S, FINAL>;
   const int id = blockIdx.x * kWaves + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   if (id >= units) return;
