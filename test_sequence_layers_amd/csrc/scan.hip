@@ -787,15 +787,15 @@ Plan plan_of(int B, int N, int C, int G, int want, int min_tokens, int unit) {
 // the fold's traffic and their start, waves hide what a token waits for (768 channels, bf16, 16 states, three and
 // six: 2 x 4096 tokens 68 and 72 us, 4 x 8192 189 and 183). Sequences of their own lengths end early, and their waves
 // with them: there four, of at least 24 tokens (3 x <= 1999 x 1000 x 32, fp32: 90 us, 100 with three). One
-// segment where a second run over the tokens costs more than it gives: for short sequences, the longer the
-// more blocks of channels there are (768 channels: 48 tokens of one sequence 24 us in one launch, 25 in
-// three, 64 tokens 31 and 24; of 24 sequences 64 tokens 32 and 31; of 64 96 tokens 57 and 61, 128 tokens 77 and
-// 74), and from the number of blocks on that keeps the SIMDs busy by itself (512 tokens, S = 16: 1536 blocks 369
-// and 338 us, 2040 375 and 443; S = 8: 1536 215 and 225; S = 32: 768 417 and 331, 900 424 and 428; S = 64: 648 683
-// and 633, 768 684 and 711).
+// segment where a second run over the tokens costs more than it gives. That is so for short sequences, the longer
+// the more blocks of channels there are (768 channels, bf16, 16 states, one launch and three: one sequence of 48 tokens
+// 19 and 23 us, of 64 25 and 21; 24 of 96 37 and 39; 64 of 160 72 and 79), and from the number of blocks on that keeps
+// the SIMDs busy by itself (2048 tokens: 8 states 1536 blocks 873 and 780, 1728 883 and 1008; 16 1248 1179 and 1039,
+// 1344 1184 and 1200; 32 672 1085 and 965, 768 1084 and 1083; 64 768 2358 and 2014, 864 2365 and 2305; 512 tokens: 32
+// 576 266 and 255, 768 266 and 307; 64 576 546 and 472, 768 548 and 569).
 Plan fwd_plan(const ScanArgs& a, int S) {
   const long long blocks = (long long)a.B * ((a.C / a.G + 63) / 64 * a.G);
-  const bool once = a.N <= 48 + blocks / 16 || blocks >= (S <= 8 ? 1500 : S <= 16 ? 1600 : S <= 32 ? 900 : 750);
+  const bool once = a.N <= 48 + blocks / 6 || blocks >= (S <= 8 ? 1600 : S <= 16 ? 1300 : S <= 32 ? 720 : 820);
   if (once) return plan_of(a.B, a.N, a.C, a.G, 1, a.N, kTokens);
   const long long by_length = std::min(6144ll, blocks * (a.N / 64));
   return plan_of(a.B, a.N, a.C, a.G, (int)std::max(by_length, a.lengths ? 4096ll : 3072ll), 24, kTokens);
