@@ -56,7 +56,7 @@ def native_command(out: str) -> list:
             "-isystem", os.path.join(torch, "include", "torch", "csrc", "api", "include"),
             "-isystem", "/opt/rocm/include", "-isystem", sysconfig.get_paths()["include"], "-Wall", "-Wextra",
             os.path.join(CSRC, "seq_native.cpp"), "-o", out, "-L", os.path.join(torch, "lib"),
-            "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_hip"]
+            "-ltorch_python", "-ltorch_hip", "-ltorch_cpu", "-lc10", "-lc10_hip"]
 
 
 def flags_for(src: str) -> list:

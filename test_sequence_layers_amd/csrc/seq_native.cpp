@@ -11,8 +11,8 @@
 #include <Python.h>
 
 #include <ATen/core/LegacyTypeDispatch.h>
-#include <ATen/ops/empty.h>
-#include <ATen/ops/empty_like.h>
+#include <ATen/hip/EmptyTensor.h>
+#include <c10/core/Allocator.h>
 #include <c10/core/DeviceGuard.h>
 #include <c10/hip/HIPStream.h>
 #include <dlfcn.h>
@@ -143,7 +143,8 @@ class Call {
     return {t.data_ptr(), step};
   }
 
-  // An output of `like`'s shape and dtype.
+  // An output of `like`'s shape and dtype. (From the allocator directly, as the workspace is: through the
+  // dispatcher it takes longer.)
   Out out(const char* name, PyObject* given, const Tensor& like) const {
     Out o;
     if (given != Py_None) {
@@ -152,7 +153,7 @@ class Call {
       o.given = given;
     } else {
       const NoGil free;
-      o.t = at::empty_like(like, like.options().requires_grad(false), at::MemoryFormat::Contiguous);
+      o.t = at::detail::empty_cuda(like.sizes(), like.scalar_type(), device_, c10::nullopt);
       o.p = o.t.data_ptr();
     }
     return o;
@@ -166,7 +167,7 @@ class Call {
 
   // Pointer and bytes; `held` keeps a new one until the call is enqueued (its memory is given back in the order
   // of the stream).
-  void* workspace(PyObject* given, size_t need, size_t& bytes, Tensor& held) const {
+  void* workspace(PyObject* given, size_t need, size_t& bytes, c10::DataPtr& held) const {
     bytes = 0;
     if (given != Py_None) {
       TORCH_CHECK_VALUE(THPVariable_Check(given) && THPVariable_Unpack(given).device() == device_ &&
@@ -178,9 +179,9 @@ class Call {
     }
     if (need == 0) return nullptr;
     const NoGil free;
-    held = at::empty({(int64_t)need}, at::TensorOptions().dtype(at::kByte).device(device_));
+    held = c10::GetAllocator(c10::DeviceType::CUDA)->allocate(need);
     bytes = need;
-    return held.data_ptr();
+    return held.get();
   }
 
   ttt_dtype dt;
@@ -275,7 +276,7 @@ PyObject* layernorm_backward(PyObject*, PyObject* const* a, Py_ssize_t count) {
   const void* pdy = c.io("d_y", dy, x.sizes());
   const Out o[3] = {c.out("d_x", a[4], x), c.out("d_weight", a[5], w), c.out("d_bias", a[6], w)};
   size_t bytes;
-  Tensor held;
+  c10::DataPtr held;
   void* ws = c.workspace(a[7], api.ttt_backward_layernorm_workspace(c.dt, n.M, n.H, n.D), bytes, held);
   const float eps = number(a[3]);
   const ttt_status st = enqueue(api.ttt_backward_layernorm, c.dt, n.M, n.H, n.D, eps, px.p, px.stride, pw, pdy,
@@ -356,7 +357,7 @@ PyObject* conv1d_backward(PyObject*, PyObject* const* a, Py_ssize_t count) {
   const Out o[4] = {c.out("d_x", a[7], x), c.out("d_weight", a[8], w), c.grad("d_bias", a[9], b),
                     c.grad("d_state", a[10], state)};
   size_t bytes;
-  Tensor held;
+  c10::DataPtr held;
   void* ws = c.workspace(a[11], api.ttt_backward_conv1d_workspace(c.dt, n.B, n.N, n.C, n.K), bytes, held);
   const int silu = truth(a[4]);
   const ttt_status st = enqueue(api.ttt_backward_conv1d, c.dt, n.B, n.N, n.C, n.K, silu, px.p, px.stride, pw, pb, ps,
@@ -415,7 +416,7 @@ PyObject* scan_forward(PyObject*, PyObject* const* a, Py_ssize_t count) {
   const int* pl = c.lengths(len, s.B);
   const Out y = c.out("y", a[12], s.u);
   size_t bytes;
-  Tensor held;
+  c10::DataPtr held;
   void* ws = c.workspace(a[13], api.ttt_forward_selective_scan_workspace(c.dt, s.B, s.N, s.C, s.S, s.G), bytes, held);
   const int softplus = truth(a[8]);
   const ttt_status st = enqueue(api.ttt_forward_selective_scan, c.dt, s.B, s.N, s.C, s.S, s.G, softplus,
@@ -462,7 +463,7 @@ PyObject* scan_backward(PyObject*, PyObject* const* a, Py_ssize_t count) {
                     c.grad("d_delta_bias", a[18], s.delta_bias), c.grad("d_z", a[19], s.z),
                     c.grad("d_h0", a[20], h0)};
   size_t bytes;
-  Tensor held;
+  c10::DataPtr held;
   void* ws = c.workspace(a[21], api.ttt_backward_selective_scan_workspace(c.dt, s.B, s.N, s.C, s.S, s.G), bytes, held);
   const int softplus = truth(a[8]);
   const ttt_status st = enqueue(api.ttt_backward_selective_scan, c.dt, s.B, s.N, s.C, s.S, s.G, softplus,
