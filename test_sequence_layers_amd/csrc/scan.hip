@@ -8,19 +8,22 @@
 // last only.
 //
 // A lane owns one channel with all its S states in registers, a wave 64 channels of one segment: B
-// and C are then the same for the whole wave and come through scalar loads into SGPRs, the sum over
-// the states stays inside the lane, and every access of u, delta, z and y is a contiguous run over
-// channels. What bounds it is the vector ALU: one exponential (half rate) and four multiplies or
+// and C are then the same for the whole wave and come through scalar loads into SGPRs (B also as one element
+// per lane, see outer()), the sum over the states stays inside the lane, and every access of u, delta, z and y is
+// a contiguous run over channels. What bounds it is the vector ALU: one exponential (half rate) and four multiplies or
 // multiply-adds per state and token, about 35 operations per token beside them, and the second run.
-// 4 x 8192 x 768 x 16, bf16, gated: 180 us (traced one by one 74 the first run, 15 the fold, 102 the last, with
-// the vector ALU busy 90 % of the time in both runs: 88 and 116 instructions a token and wave, where the
-// recurrence and the sum over the states alone are 64 and 80), 201 MB at 1.1 TB/s; one run's operations alone
-// take 77 us, the bytes 40.
+// 4 x 8192 x 768 x 16, bf16, gated: 179 us (traced one by one 74 the first run, 15 the fold, 100 the last, with
+// the vector ALU and the matrix core busy 90 % of the time in both runs: 84 and 103 instructions a token and wave,
+// where the recurrence and the sum over the states alone are 64 and 68), 201 MB at 1.1 TB/s; one run's operations
+// alone take 77 us, the bytes 40. 3 x <= 1999 x 1000 x 32, fp32: 85 us (31, 17 and 37), of which 22 are the 129 MB of
+// the segments' states.
 //
 // Tried and not kept: a scalar row of B and C held one token ahead behind a scheduling barrier (259 against
 // 247 us); the waves of a workgroup on consecutive segments, joined through LDS so that the fold goes over
 // groups of four (fold 15 -> 5.5 us, but the last run starts later by as much; wide states lose waves
-// to the registers it takes: 2 x 4096 x 768 x 32 119 -> 128 us).
+// to the registers it takes: 2 x 4096 x 768 x 32 119 -> 128 us); the backward pass's products with B and C as
+// outer products on the matrix core (7 to 17 % fewer instructions, the same times within 1 %); the sum over the
+// states there (a matrix instruction per state, since a lane holds its channel's states: slower).
 #include <algorithm>
 #include <type_traits>
 
@@ -165,7 +168,9 @@ __device__ __forceinline__ int length_of(const int* lengths, int b, int N) {
 template <class T, int S, bool FINAL>
 __global__ __launch_bounds__(64 * kWaves) void scan_fwd(ScanArgs a, Plan p, int units, float* __restrict__ ends,
                                                         float* __restrict__ sums) {
-  constexpr int kTok = S <= 32 ? kTokens : 1;  // (64 states leave no registers for more: 107 us, 113 with two)
+  // (64 states leave no registers for more: 107 us, 113 with two. Nor do two of C's rows of 128 bytes leave SGPRs:
+  // 4 x 8192 x 768 x 32, fp32, 297 us, 306 with two in the last run as well.)
+  constexpr int kTok = S <= 32 && (!FINAL || S * sizeof(T) <= 64) ? kTokens : 1;
   constexpr bool kOuter = outer_rows<T, S, FINAL>;
   const int id = blockIdx.x * kWaves + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   if (id >= units) return;
@@ -786,7 +791,7 @@ Plan plan_of(int B, int N, int C, int G, int want, int min_tokens, int unit) {
 // Forward: three waves per SIMD, and more where segments stay longer than 64 tokens, up to six: segments cost
 // the fold's traffic and their start, waves hide what a token waits for (768 channels, bf16, 16 states, three and
 // six: 2 x 4096 tokens 68 and 72 us, 4 x 8192 189 and 183). Sequences of their own lengths end early, and their waves
-// with them: there four, of at least 24 tokens (3 x <= 1999 x 1000 x 32, fp32: 90 us, 100 with three). One
+// with them: there four, of at least 24 tokens (3 x <= 1999 x 1000 x 32, fp32: a tenth less than with three). One
 // segment where a second run over the tokens costs more than it gives. That is so for short sequences, the longer
 // the more blocks of channels there are (768 channels, bf16, 16 states, one launch and three: one sequence of 48 tokens
 // 19 and 23 us, of 64 25 and 21; 24 of 96 37 and 39; 64 of 160 72 and 79), and from the number of blocks on that keeps
