@@ -100,9 +100,9 @@ __device__ __forceinline__ void outer(float row, float x, f32x4* acc) {
 // Where B comes as one element per lane and through outer(), instead of as scalars: where a token's scalars would be
 // more than the SGPRs hold ahead of their use. In the last run, which has C's as well, always (768 channels, bf16,
 // without and with it: 2 x 4096 tokens of 8 states 52 and 48 us, of 16 69 and 66; 3 x 1999 x 1000 of 32, fp32, its last
-// run 52 and 36; but 32768 x 1536 of 16 320 and 327). In the first from 64 bytes on (2 x 2048 tokens of 64 states, bf16, 121
-// and 107 us, 4 x 8192 of 32, bf16, 307 and 303; but of 16, traced, 75 and 79): an outer product takes as long as its
-// four multiplications (16 cycles).
+// run 52 and 36; but 32768 x 1536 of 16 320 and 327). In the first from 64 bytes on (2 x 2048 tokens of 64 states, bf16,
+// 121 and 107 us, 4 x 8192 of 32, bf16, 307 and 303; but of 16, traced, 75 and 79): an outer product takes as long as
+// its four multiplications (16 cycles).
 template <class T, int S, bool FINAL>
 constexpr bool outer_rows = FINAL || S * sizeof(T) >= 64;
 
@@ -393,10 +393,11 @@ __global__ __launch_bounds__(256) void scan_step(ScanArgs a) {
 // operations, the bytes 17.
 
 // Tokens per sub-chunk, states per wave and waves of a scan_bwd workgroup: kSub * SW values of each of a
-// and h stay in a lane's registers.
+// and h stay in a lane's registers. Eight states a wave share what a token costs a wave, but leave two waves per
+// SIMD, where four leave three (2 x 4096 x 768, bf16, four and eight: 16 states 154 and 197 us, 32 279 and 250).
 template <int S>
 struct Bwd {
-  static constexpr int SW = S == 64 ? 8 : 4;
+  static constexpr int SW = S >= 32 ? 8 : 4;
   static constexpr int NW = S / SW;
   static constexpr int kSub = 8;
 };
@@ -546,7 +547,7 @@ __device__ __forceinline__ float join_values(float* x) {
 // passed through LDS with its rows of B and C; each wave's sums over its states come back the same
 // way. Tokens behind the sequence are passed over as tokens of no step and no gradient.
 template <class T, int S>
-__global__ __launch_bounds__(64 * Bwd<S>::NW, S <= 32 ? 3 : 2) void scan_bwd(ScanArgs a, Plan p, BwdBufs w) {
+__global__ __launch_bounds__(64 * Bwd<S>::NW, S <= 16 ? 3 : 2) void scan_bwd(ScanArgs a, Plan p, BwdBufs w) {
   constexpr int SW = Bwd<S>::SW, NW = Bwd<S>::NW, kSub = Bwd<S>::kSub, kThreads = 64 * NW;
   constexpr int TW = kSub / NW;          // tokens a wave prepares and finishes
   constexpr int NV = 2 * SW;             // sums for dB and dC per token
@@ -805,15 +806,15 @@ Plan fwd_plan(const ScanArgs& a, int S) {
   const long long by_length = std::min(6144ll, blocks * (a.N / 64));
   return plan_of(a.B, a.N, a.C, a.G, (int)std::max(by_length, a.lengths ? 4096ll : 3072ll), 24, kTokens);
 }
-// Backward. The walk's workgroups come in rounds of as many as the CUs hold (by its registers 12 waves a CU, 8 with 64
-// states; a workgroup is S / 4 waves, or 8), and a round takes as long as its segments: of the segment lengths from
+// Backward. The walk's workgroups come in rounds of as many as the CUs hold (by its registers 12 waves a CU, 8 of wide
+// states; a workgroup is S / 4 or S / 8 waves), and a round takes as long as its segments: of the segment lengths from
 // the shortest to twice that, the one whose rounds take the fewest tokens in all. The shortest is 16 tokens (2 x 333 x
-// 193 x 8 28 us, 36 at 24, 43 at 32) or what 4096 segments leave, 1536 of wide states, whose segments cost more in the
-// fold and in partial sums: 2 x 4096 x 768 x 32, bf16, 280 us, 309 with 4096; x 64 485 and 538; 8 x 1024 x 512 x 32, where
-// 22 segments of 48 tokens are 5.5 rounds and 16 of 64 are 4, 213 and 191.
+// 193 x 8 28 us, 36 at 24, 43 at 32) or what 4096 blocks' segments leave, 1536 of wide states, whose segments cost more
+// in the fold and in partial sums: 2 x 4096 x 768 x 32, bf16, 252 us, 275 with 3072; x 64 486 and 537; 8 x 1024 x 512 x
+// 64, where 22 segments of 48 tokens are 5.5 rounds and 16 of 64 are 4, 363 and 319.
 Plan bwd_plan(const ScanArgs& a, int S) {
   Plan p = plan_of(a.B, a.N, a.C, a.G, S <= 16 ? 4096 : 1536, 16, kBwdSub);
-  const long long blocks = (long long)a.B * p.cb, slots = 256 * (S <= 8 ? 6 : S <= 16 ? 3 : 1);
+  const long long blocks = (long long)a.B * p.cb, slots = 256 * (S <= 8 ? 6 : S <= 16 ? 3 : S <= 32 ? 2 : 1);
   const int shortest = p.T, step = (shortest / 32 + kBwdSub) / kBwdSub * kBwdSub;
   long long best = -1;
   for (int T = shortest; T <= 2 * shortest; T += step) {
