@@ -234,3 +234,13 @@ def test_scan_many_short_sequences():
     ry, rend = _oracle(s, True, [60 - i for i in range(B)])
     check("y", y, ry, C_SCAN)
     check("h_out", end, rend, C_SCAN)
+
+
+@pytest.mark.parametrize("B,N,C,S,G,dtype,opt", [
+    (2, 700, 66, 64, 1, "fp32", dict(lengths=[700, 333], cut=True)), (1, 515, 130, 32, 2, "fp32", dict(cut=True)),
+    (3, 400, 64, 32, 1, "bf16", dict(lengths=[400, 0, 77])), (2, 611, 40, 64, 4, "bf16", dict(cut=True)),
+    (40, 90, 100, 16, 1, "bf16", {}), (2, 1200, 70, 8, 1, "fp32", dict(cut=True, lengths=[1200, 1199]))], ids=lambda v: str(v))
+def test_scan_many_segments(B, N, C, S, G, dtype, opt):
+    """Wide states and many segments, with rows of B and C that are slices of wider ones."""
+    test_scan_forward(B, N, C, S, G, dtype, opt)
+    test_scan_backward(B, N, C, S, G, dtype, opt)
