@@ -24,6 +24,8 @@
 // to the registers it takes: 2 x 4096 x 768 x 32 119 -> 128 us); the backward pass's products with B and C as
 // outer products on the matrix core (7 to 17 % fewer instructions, the same times within 1 %); the sum over the
 // states there (a matrix instruction per state, since a lane holds its channel's states: slower).
+#include <math.h>
+
 #include <algorithm>
 #include <type_traits>
 
@@ -792,19 +794,23 @@ Plan plan_of(int B, int N, int C, int G, int want, int min_tokens, int unit) {
 // Forward: three waves per SIMD, and more where segments stay longer than 64 tokens, up to six: segments cost
 // the fold's traffic and their start, waves hide what a token waits for (768 channels, bf16, 16 states, three and
 // six: 2 x 4096 tokens 68 and 72 us, 4 x 8192 189 and 183). Sequences of their own lengths end early, and their waves
-// with them: there four, of at least 24 tokens (3 x <= 1999 x 1000 x 32, fp32: a tenth less than with three). One
+// with them: there four (3 x <= 1999 x 1000 x 32, fp32: a tenth less than with three). The shortest segment goes with
+// the root of the length, from 8 to 24 tokens, since the fold takes longer the more there are (16 states, 24, 12 and 8
+// tokens: 1 x 102 x 64 21, 16 and 14 us; 2 x 333 x 193 23, 17 and 17; 1 x 1024 x 768 28, 26 and 31). One
 // segment where a second run over the tokens costs more than it gives. That is so for short sequences, the longer
-// the more blocks of channels there are (768 channels, bf16, 16 states, one launch and three: one sequence of 48 tokens
-// 19 and 23 us, of 64 25 and 21; 24 of 96 37 and 39; 64 of 160 72 and 79), and from the number of blocks on that keeps
+// the more blocks of channels there are (768 channels, bf16, 16 states, one launch and three: one sequence of 24 tokens
+// 11.5 and 14.0 us, of 32 14.2 and 14.0; 8 of 32 14.4 and 16.6, of 48 19.9 and 17.3; 24 of 64 26 and 33, of 96 37 and 35;
+// 64 of 160 71 and 79), and from the number of blocks on that keeps
 // the SIMDs busy by itself (2048 tokens: 8 states 1536 blocks 873 and 780, 1728 883 and 1008; 16 1248 1179 and 1039,
 // 1344 1184 and 1200; 32 672 1085 and 965, 768 1084 and 1083; 64 768 2358 and 2014, 864 2365 and 2305; 512 tokens: 32
 // 576 266 and 255, 768 266 and 307; 64 576 546 and 472, 768 548 and 569).
 Plan fwd_plan(const ScanArgs& a, int S) {
   const long long blocks = (long long)a.B * ((a.C / a.G + 63) / 64 * a.G);
-  const bool once = a.N <= 48 + blocks / 6 || blocks >= (S <= 8 ? 1600 : S <= 16 ? 1300 : S <= 32 ? 720 : 820);
+  const bool once = a.N <= 26 + blocks / 5 || blocks >= (S <= 8 ? 1600 : S <= 16 ? 1300 : S <= 32 ? 720 : 820);
   if (once) return plan_of(a.B, a.N, a.C, a.G, 1, a.N, kTokens);
   const long long by_length = std::min(6144ll, blocks * (a.N / 64));
-  return plan_of(a.B, a.N, a.C, a.G, (int)std::max(by_length, a.lengths ? 4096ll : 3072ll), 24, kTokens);
+  const int shortest = std::min(24, std::max(8, (int)(0.45 * sqrt((double)a.N))));
+  return plan_of(a.B, a.N, a.C, a.G, (int)std::max(by_length, a.lengths ? 4096ll : 3072ll), shortest, kTokens);
 }
 // Backward. The walk's workgroups come in rounds of as many as the CUs hold (by its registers 12 waves a CU, 8 of wide
 // states; a workgroup is S / 4 or S / 8 waves), and a round takes as long as its segments: of the segment lengths from
