@@ -791,12 +791,27 @@ Plan plan_of(int B, int N, int C, int G, int want, int min_tokens, int unit) {
   p.nseg = (int)((N + T - 1) / T);
   return p;
 }
+// Of the segment lengths from p's to `longest`, in steps of `unit` tokens or a 32nd, the one whose units (one per
+// segment and block of channels, `slots` of them at a time) take the fewest tokens in all, one round after the other.
+Plan full_rounds(Plan p, int B, int N, int slots, int longest, int unit) {
+  const long long blocks = (long long)B * p.cb;
+  const int step = (p.T / 32 + unit) / unit * unit;
+  long long best = -1;
+  for (int T = p.T; T <= longest; T += step) {
+    const int nseg = (N + T - 1) / T;
+    const long long tokens = (blocks * nseg + slots - 1) / slots * std::min(T, N);
+    if (best < 0 || tokens < best) best = tokens, p.T = T, p.nseg = nseg;
+  }
+  return p;
+}
+
 // Forward: three waves per SIMD, and more where segments stay longer than 64 tokens, up to six: segments cost
 // the fold's traffic and their start, waves hide what a token waits for (768 channels, bf16, 16 states, three and
 // six: 2 x 4096 tokens 68 and 72 us, 4 x 8192 189 and 183). Sequences of their own lengths end early, and their waves
 // with them: there four (3 x <= 1999 x 1000 x 32, fp32: a tenth less than with three). The shortest segment goes with
 // the root of the length, from 8 to 24 tokens, since the fold takes longer the more there are (16 states, 24, 12 and 8
-// tokens: 1 x 102 x 64 21, 16 and 14 us; 2 x 333 x 193 23, 17 and 17; 1 x 1024 x 768 28, 26 and 31). One
+// tokens: 1 x 102 x 64 21, 16 and 14 us; 2 x 333 x 193 23, 17 and 17; 1 x 1024 x 768 28, 26 and 31); it may be half longer
+// where that fills rounds of a wave on each SIMD (2 x 2048 x 768, 16 states: 44 us, 49 without, 64 states 108 and 119). One
 // segment where a second run over the tokens costs more than it gives. That is so for short sequences, the longer
 // the more blocks of channels there are (768 channels, bf16, 16 states, one launch and three: one sequence of 24 tokens
 // 11.5 and 14.0 us, of 32 14.2 and 14.0; 8 of 32 14.4 and 16.6, of 48 19.9 and 17.3; 24 of 64 26 and 33, of 96 37 and 35;
@@ -810,7 +825,9 @@ Plan fwd_plan(const ScanArgs& a, int S) {
   if (once) return plan_of(a.B, a.N, a.C, a.G, 1, a.N, kTokens);
   const long long by_length = std::min(6144ll, blocks * (a.N / 64));
   const int shortest = std::min(24, std::max(8, (int)(0.45 * sqrt((double)a.N))));
-  return plan_of(a.B, a.N, a.C, a.G, (int)std::max(by_length, a.lengths ? 4096ll : 3072ll), shortest, kTokens);
+  const Plan p =
+      plan_of(a.B, a.N, a.C, a.G, (int)std::max(by_length, a.lengths ? 4096ll : 3072ll), shortest, kTokens);
+  return full_rounds(p, a.B, a.N, 1024, p.T + p.T / 2, kTokens);
 }
 // Backward. The walk's workgroups come in rounds of as many as the CUs hold (by its registers 12 waves a CU, 8 of wide
 // states; a workgroup is S / 4 or S / 8 waves), and a round takes as long as its segments: of the segment lengths from
@@ -819,16 +836,8 @@ Plan fwd_plan(const ScanArgs& a, int S) {
 // in the fold and in partial sums: 2 x 4096 x 768 x 32, bf16, 252 us, 275 with 3072; x 64 486 and 537; 8 x 1024 x 512 x
 // 64, where 22 segments of 48 tokens are 5.5 rounds and 16 of 64 are 4, 363 and 319.
 Plan bwd_plan(const ScanArgs& a, int S) {
-  Plan p = plan_of(a.B, a.N, a.C, a.G, S <= 16 ? 4096 : 1536, 16, kBwdSub);
-  const long long blocks = (long long)a.B * p.cb, slots = 256 * (S <= 8 ? 6 : S <= 16 ? 3 : S <= 32 ? 2 : 1);
-  const int shortest = p.T, step = (shortest / 32 + kBwdSub) / kBwdSub * kBwdSub;
-  long long best = -1;
-  for (int T = shortest; T <= 2 * shortest; T += step) {
-    const int nseg = (a.N + T - 1) / T;
-    const long long tokens = (blocks * nseg + slots - 1) / slots * std::min(T, a.N);
-    if (best < 0 || tokens < best) best = tokens, p.T = T, p.nseg = nseg;
-  }
-  return p;
+  const Plan p = plan_of(a.B, a.N, a.C, a.G, S <= 16 ? 4096 : 1536, 16, kBwdSub);
+  return full_rounds(p, a.B, a.N, 256 * (S <= 8 ? 6 : S <= 16 ? 3 : S <= 32 ? 2 : 1), 2 * p.T, kBwdSub);
 }
 
 size_t align_up(size_t x) { return (x + 255) / 256 * 256; }
