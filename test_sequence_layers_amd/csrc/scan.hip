@@ -137,6 +137,7 @@ struct Walk {
   __device__ __forceinline__ void next(bool on = true) { p += on ? step : 0; }
 };
 
+constexpr long long kSimds = 1024;  // of 256 CUs
 // How a call is cut up. Channel blocks: 64 channels of one group each.
 struct Plan {
   int cbg, cb;      // channel blocks per group, in all
@@ -823,17 +824,17 @@ Plan fwd_plan(const ScanArgs& a, int S) {
   const long long blocks = (long long)a.B * ((a.C / a.G + 63) / 64 * a.G);
   const bool once = a.N <= 26 + blocks / 5 || blocks >= (S <= 8 ? 1600 : S <= 16 ? 1300 : S <= 32 ? 720 : 820);
   if (once) return plan_of(a.B, a.N, a.C, a.G, 1, a.N, kTokens);
-  const long long by_length = std::min(6144ll, blocks * (a.N / 64));
+  const long long by_length = std::min(6 * kSimds, blocks * (a.N / 64));
   const int shortest = std::min(24, std::max(8, (int)(0.45 * sqrt((double)a.N))));
-  const Plan p =
-      plan_of(a.B, a.N, a.C, a.G, (int)std::max(by_length, a.lengths ? 4096ll : 3072ll), shortest, kTokens);
-  return full_rounds(p, a.B, a.N, 1024, p.T + p.T / 2, kTokens);
+  const long long want = std::max(by_length, (a.lengths ? 4 : 3) * kSimds);
+  const Plan p = plan_of(a.B, a.N, a.C, a.G, (int)want, shortest, kTokens);
+  return full_rounds(p, a.B, a.N, (int)kSimds, p.T + p.T / 2, kTokens);
 }
 // Backward. The walk's workgroups come in rounds of as many as the CUs hold (by its registers 12 waves a CU, 8 of wide
 // states; a workgroup is S / 4 or S / 8 waves), and a round takes as long as its segments: of the segment lengths from
 // the shortest to twice that, the one whose rounds take the fewest tokens in all. The shortest is 16 tokens (2 x 333 x
 // 193 x 8 28 us, 36 at 24, 43 at 32) or what 4096 blocks' segments leave, 1536 of wide states, whose segments cost more
-// in the fold and in partial sums: 2 x 4096 x 768 x 32, bf16, 252 us, 275 with 3072; x 64 486 and 537; 8 x 1024 x 512 x
+// in the fold and in partial sums: 2 x 4096 x 768 x 32, bf16, 252 us, 275 with twice as many; x 64 486 and 537; 8 x 1024 x 512 x
 // 64, where 22 segments of 48 tokens are 5.5 rounds and 16 of 64 are 4, 363 and 319.
 Plan bwd_plan(const ScanArgs& a, int S) {
   const Plan p = plan_of(a.B, a.N, a.C, a.G, S <= 16 ? 4096 : 1536, 16, kBwdSub);
