@@ -309,7 +309,7 @@ BwdPlan bwd_plan(Shape s, int M, int H) {
   p.HB = H < groups ? H : groups;
   p.R = groups / p.HB;
   p.gy = (H + p.HB - 1) / p.HB;
-  p.P = (M + p.R - 1) / p.R;
+  p.P = ((long long)M + p.R - 1) / p.R;
   // Workgroups: four waves per SIMD of 256 CUs with 1024 threads each, two with fewer (8192 x 4096: 50.5 us
   // with 512 workgroups, 55.8 with 768, 63 with 1024; 65536 x 768: 66.6, 63.7 and 67.1).
   const long long wgs = threads >= 1024 ? 256 : 512, most = wgs > p.gy ? wgs / p.gy : 1;

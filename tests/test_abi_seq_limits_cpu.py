@@ -1,0 +1,17 @@
+"""The block operators' plans at the largest sizes that are accepted, through the workspaces they ask for (no GPU)."""
+import pytest
+
+import test_sequence_layers_amd as T
+
+F32, BF16 = T.TTT_F32, T.TTT_BF16
+
+
+@pytest.mark.parametrize("dt", [F32, BF16])
+@pytest.mark.parametrize("D", [1, 8, 64, 100, 4096, 16384])
+@pytest.mark.parametrize("M", [(1 << 31) - 1 - k for k in (0, 1, 7, 15, 127, 128)])
+def test_layernorm_backward_workspace_of_the_most_rows(dt, M, D):
+    """Partial rows of at most 512 workgroups (1024 threads: 256), two of D fp32 values each, rounded up to 256 bytes;
+    and no fewer than for half the rows."""
+    need = T.load_library().ttt_backward_layernorm_workspace
+    assert 0 < need(dt, M, 1, D) <= 512 * 2 * D * 4 + 255
+    assert need(dt, M, 1, D) >= need(dt, 1 << 14, 1, D) // 2
