@@ -150,7 +150,7 @@ __global__ __launch_bounds__(kThreads) void conv1d_bwd(Conv1dArgs a, int pieces,
     const T* state = a.state ? (const T*)a.state + (long long)b * (K - 1) * C + c0 : nullptr;
     const T* dy = (const T*)a.dy + (long long)b * a.N * C + c0;
     T* dx = (T*)a.dx + (long long)b * a.N * C + c0;
-    const int t0 = (int)first, t1 = min(a.N, t0 + len);
+    const int t0 = (int)first, t1 = min(a.N, t0 + len), te = min(t1, n);
     Raw<T, V> nx[kAhead], nd[kAhead];
     auto fetch = [&](int t) {
 #pragma unroll
@@ -165,7 +165,8 @@ __global__ __launch_bounds__(kThreads) void conv1d_bwd(Conv1dArgs a, int pieces,
     load_taps<V, K>(a.w, a.bias, c0, wt, bs);
     for (int k = 0; k < K - 1; ++k) input<T, V, K>(x, a.xs, state, C, min(t0, n) - (K - 1) + k, win[k]);
     // One token: its dpre (none behind the sequence), its part of the parameters' gradients (of the run's
-    // own tokens), and o = dx[t - (K - 1)], which then has all it needs:
+    // own tokens; not those behind the sequence, whose windows may hold a state or a last input that is not
+    // finite), and o = dx[t - (K - 1)], which then has all it needs:
     // dp[k] = dpre[t - (K - 1) + k], dx[t - (K - 1)] = sum_k w[K - 1 - k] dp[k].
     auto token = [&](int t, const Raw<T, V>& rx, const Raw<T, V>& rd, float* out) {
       float d[V];
@@ -182,7 +183,7 @@ __global__ __launch_bounds__(kThreads) void conv1d_bwd(Conv1dArgs a, int pieces,
         }
         d[i] = in ? d[i] : 0.f;
       }
-      if (t < t1)
+      if (t < te)
         for (int i = 0; i < V; ++i) {
           acc[K][i] += d[i];
           for (int k = 0; k < K; ++k) acc[k][i] = fmaf(d[i], win[k][i], acc[k][i]);

@@ -1,0 +1,41 @@
+"""The block operators where states or inputs hold infinities or NaN that the formulas do not reach: a sequence of
+no tokens, the tokens behind a sequence's end, decays past fp32's range."""
+import pytest
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+if torch.cuda.is_available():
+    import test_sequence_layers_amd as T
+from seq_helpers import DT, Inputs
+
+NAN, INF = float("nan"), float("inf")
+
+
+@pytest.mark.parametrize("N,C,K,dtype,silu", [(9, 64, 4, "bf16", True), (70, 33, 3, "fp32", False), (300, 40, 2, "bf16", False)])
+def test_conv1d_gradients_of_an_empty_sequence(N, C, K, dtype, silu):
+    """Its state is in no product: whatever it holds, every gradient is that of a state of zeros."""
+    i = Inputs(N, dtype)
+    x, d_y, state = i.normal(3, N, C), i.normal(3, N, C), i.normal(3, K - 1, C)
+    w, b = i.param(C, K), i.param(C)
+    lengths = torch.tensor([N, 0, 1], dtype=torch.int32, device="cuda")
+    state[1] = 0.0
+    want = T.ttt_backward_conv1d(x, w, b, d_y, silu=silu, state=state, lengths=lengths)
+    for value in (NAN, INF):
+        state[1] = value
+        got = T.ttt_backward_conv1d(x, w, b, d_y, silu=silu, state=state, lengths=lengths)
+        for name, g, r in zip(("d_x", "d_weight", "d_bias", "d_state"), got, want):
+            assert torch.isfinite(r).all() and torch.equal(g, r), (name, value)
+
+
+@pytest.mark.parametrize("N,n,K,dtype", [(9, 9, 4, "fp32"), (9, 6, 3, "bf16"), (100, 64, 4, "bf16"), (64, 64, 2, "fp32")])
+def test_conv1d_gradients_behind_an_infinite_last_input(N, n, K, dtype):
+    """The last input meets the last tap alone: d_weight of the others has no part of it."""
+    i = Inputs(N + K, dtype)
+    x, d_y, w = i.normal(1, N, 40), i.normal(1, N, 40), i.param(40, K)
+    lengths = torch.tensor([n], dtype=torch.int32, device="cuda")
+    want = T.ttt_backward_conv1d(x, w, None, d_y, lengths=lengths)
+    x[0, n - 1] = INF
+    got = T.ttt_backward_conv1d(x, w, None, d_y, lengths=lengths)
+    assert torch.equal(got[1][:, :K - 1], want[1][:, :K - 1]) and not torch.isfinite(got[1][:, K - 1]).any()
+    assert torch.equal(got[0], want[0])
