@@ -1,0 +1,48 @@
+"""The block operators' sums where fp32 loses the most: rows far from zero, sums over very many tokens."""
+import numpy as np
+import pytest
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+if torch.cuda.is_available():
+    import test_sequence_layers_amd as T
+from oracle import seq_oracle as O
+from seq_helpers import Inputs, U, f64
+
+EPS = 1e-5
+
+
+@pytest.mark.parametrize("H,D,dtype", [(1, 64, "fp32"), (12, 64, "fp32"), (1, 300, "fp32"), (1, 768, "fp32"), (1, 1001, "fp32"),
+                                       (1, 1001, "bf16"), (1, 4096, "fp32"), (1, 4100, "fp32"), (1, 16384, "fp32")])
+def test_layernorm_of_constant_rows_is_the_bias(H, D, dtype):
+    """x - mean is 0 whatever the row's value: y is the bias, d_x is rstd (g - mean(g)), d_weight 0."""
+    i = Inputs(D, dtype)
+    shape = (H, D) if H > 1 else (D,)
+    values = torch.tensor([0.1, -7.3, 1000.1, 1000000.5, -3.3e7, 1e-20], device="cuda").to(i.io)
+    x = values.view(-1, *[1] * len(shape)).expand(-1, *shape).contiguous()
+    w, b, d_y = i.param(*shape, mean=1.0), i.param(*shape), i.normal(*x.shape)
+    assert torch.equal(T.ttt_forward_layernorm(x, w, b, EPS), b.expand_as(x).to(i.io))
+    dx, dw, _ = T.ttt_backward_layernorm(x, w, d_y, EPS)
+    assert not dw.any() and torch.isfinite(dx).all()
+
+
+@pytest.mark.parametrize("D,dtype,sliced", [(64, "fp32", 0), (768, "fp32", 0), (768, "fp32", 1), (2050, "fp32", 0), (4096, "fp32", 0)])
+def test_layernorm_of_rows_far_from_zero(D, dtype, sliced):
+    """Rows 1e5 deviations from zero. x is exact, and only differences of its elements enter: with |x - mean| <= 5
+    deviations (asserted), a difference x - x' is off by u times 10 deviations, and the mean of D of them by as much and by 72 u
+    (at most 64 terms in a lane and 8 levels) of their mean magnitude, at most 6: below 450 u of a deviation, in xhat and,
+    twice, relatively in rstd: |y - ref| <= u |ref| + 450 u (1 + 2 * 5) |w| + 4 u |b|, the result's own rounding first."""
+    i = Inputs(D, dtype)
+    w, b = i.param(D, mean=1.0, scale=0.2), i.param(D)
+    x = i.normal(20, D).clamp_(-4, 4) + 1e5
+    if sliced:
+        x = torch.cat([x, x], 1)[:, 1:1 + D]
+    ref = O.layernorm(f64(x), f64(w), f64(b), EPS)
+    dev = f64(x) - f64(x).mean(-1, keepdims=True)
+    assert np.abs(dev).max() <= 5 * dev.std(-1).min()
+    got = f64(T.ttt_forward_layernorm(x, w, b, EPS))
+    bound = U * np.abs(ref) + 450 * 11 * U * np.abs(f64(w)) + 4 * U * np.abs(f64(b))
+    worst = (np.abs(got - ref) / bound).max()
+    print(f"  {worst:.3f} of the bound", flush=True)
+    assert worst <= 1.0
