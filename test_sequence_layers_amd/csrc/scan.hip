@@ -638,7 +638,8 @@ __global__ __launch_bounds__(64 * Bwd<S>::NW, S <= 16 ? 3 : 2) void scan_bwd(Sca
         (&s_c[0][0])[e] = in ? nc[i] : 0.f;
       }
     }
-    for (int s = 0; s < SW; ++s) h0[s] = fmaf(exp2_hw(A2[s] * npast), hs[s], nck[s]);
+    // (Behind the sequence zeros: its states may not be finite, and are multiplied by gradients of 0 there.)
+    for (int s = 0; s < SW; ++s) h0[s] = tc < te ? fmaf(exp2_hw(A2[s] * npast), hs[s], nck[s]) : 0.f;
     __syncthreads();
     if (tc > t0) fetch(tc - kSub);
     float e[kSub][SW], h[kSub][SW];
@@ -695,7 +696,7 @@ __global__ __launch_bounds__(64 * Bwd<S>::NW, S <= 16 ? 3 : 2) void scan_bwd(Sca
         }
         __builtin_amdgcn_sched_barrier(0);
       }
-      const float total = join_values<NV, NV>(x);
+      const float total = tc + jb + tok < te ? join_values<NV, NV>(x) : 0.f;
       if (!(l & 1) && tc + jb + tok < t1) put(w.mats + ((row0 + tc + jb) * p.cb + un.cb) * 2 * S, lane_part(mat_at, 4), total);
     }
     __syncthreads();

@@ -39,3 +39,40 @@ def test_conv1d_gradients_behind_an_infinite_last_input(N, n, K, dtype):
     got = T.ttt_backward_conv1d(x, w, None, d_y, lengths=lengths)
     assert torch.equal(got[1][:, :K - 1], want[1][:, :K - 1]) and not torch.isfinite(got[1][:, K - 1]).any()
     assert torch.equal(got[0], want[0])
+
+
+def _scan(B, N, C, S, G, dtype, seed):
+    i = Inputs(seed, dtype)
+    s = dict(u=i.normal(B, N, C), delta=i.normal(B, N, C, scale=0.5), A=-i.param(C, S).abs() - 0.5, Bm=i.normal(B, N, G, S),
+             Cm=i.normal(B, N, G, S), D=i.param(C), delta_bias=i.param(C, mean=-3.0), z=i.normal(B, N, C))
+    return s, i.normal(B, N, C), i.param(B, C, S)
+
+
+NAMES = ("d_u", "d_delta", "d_A", "d_B", "d_C", "d_D", "d_delta_bias", "d_z", "d_h0")
+
+
+@pytest.mark.parametrize("N,C,S,G,dtype", [(1, 64, 8, 1, "fp32"), (7, 70, 16, 1, "bf16"), (50, 66, 32, 2, "fp32"),
+                                           (300, 64, 64, 1, "bf16"), (700, 40, 16, 1, "fp32")])
+def test_scan_gradients_of_an_empty_sequence(N, C, S, G, dtype):
+    """Its start state is in no product: whatever it holds, every gradient is that of a state of zeros, its own are zeros."""
+    s, d_y, h0 = _scan(3, N, C, S, G, dtype, N + S)
+    lengths = torch.tensor([N, 0, (N + 1) // 2], dtype=torch.int32, device="cuda")
+    h0[1] = 0.0
+    want = T.ttt_backward_selective_scan(**s, d_y=d_y, h0=h0, lengths=lengths)
+    for value in (NAN, INF):
+        h0[1] = value
+        got = T.ttt_backward_selective_scan(**s, d_y=d_y, h0=h0, lengths=lengths)
+        for name, g, r in zip(NAMES, got, want):
+            assert torch.isfinite(r).all() and torch.equal(g, r), (name, value)
+        assert not got[8][1].any()
+
+
+@pytest.mark.parametrize("N,n,S,dtype", [(8, 3, 16, "bf16"), (40, 20, 8, "fp32"), (100, 64, 32, "bf16"), (90, 41, 64, "fp32")])
+def test_scan_padding_behind_an_infinite_state(N, n, S, dtype):
+    """A sequence whose states are infinite: its padding's rows of every gradient are zeros all the same."""
+    s, d_y, h0 = _scan(2, N, 66, S, 1, dtype, N + S)
+    h0[1, 5] = INF
+    lengths = torch.tensor([N, n], dtype=torch.int32, device="cuda")
+    got = dict(zip(NAMES, T.ttt_backward_selective_scan(**s, d_y=d_y, h0=h0, lengths=lengths)))
+    for name in ("d_u", "d_delta", "d_B", "d_C", "d_z"):
+        assert torch.isfinite(got[name][0]).all() and not got[name][1, n:].any(), name
