@@ -100,7 +100,9 @@ size_t ttt_backward_conv1d_workspace(ttt_dtype dt, int B, int N, int C, int K);
  * delta_bias (nullable): fp32 [C]; h0 (nullable, zeros without it), h_out (nullable): fp32 [B, C, S],
  * the states before token 0 and after each sequence's last. S in {8, 16, 32, 64}; G divides C; B at
  * most 65535, N at most 2^22, C at most 2^20, B * C * (N + 4096) at most 2^38, B * G *
- * ceil(C / G / 64) at most 2^20. For bf16, Bm and Cm are 4-byte aligned and their strides even.
+ * ceil(C / G / 64) at most 2^20. For bf16, Bm and Cm are 4-byte aligned and their strides even, in every
+ * form. Tokens are taken in segments at once, from the states that products of decays give: where step * A is
+ * positive and exp of its sum over some tokens is not finite in fp32, states other than zero are not either.
  */
 ttt_status ttt_forward_selective_scan(ttt_dtype dt, int B, int N, int C, int S, int G, int softplus,
                                       const void* u, long long u_stride, const void* delta,
@@ -133,7 +135,9 @@ ttt_status ttt_step_selective_scan(ttt_dtype dt, int B, int C, int S, int G, int
  *   d_z = d_y (sum_s Cm h + D u) (z sigmoid(z))'.
  * d_u, d_delta, d_z: [B, N, C]; d_B, d_C: [B, N, G, S] of dtype dt; d_A: fp32 [C, S]; d_D, d_delta_bias:
  * fp32 [C]; d_h0: fp32 [B, C, S]. d_z is given exactly when z is; d_D, d_delta_bias and d_h0 may be
- * NULL. The forward pass is recomputed from the inputs, nothing of it has to be kept.
+ * NULL. The forward pass is recomputed from the inputs, nothing of it has to be kept. step * A must not be
+ * positive by so much that exp of its sum over a run of tokens is infinite in fp32: gradients are NaN then, also
+ * where states or d_y are zeros.
  */
 ttt_status ttt_backward_selective_scan(ttt_dtype dt, int B, int N, int C, int S, int G, int softplus,
                                        const void* u, long long u_stride, const void* delta,

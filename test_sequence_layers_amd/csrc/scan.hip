@@ -327,16 +327,22 @@ __global__ __launch_bounds__(kFoldThreads) void scan_fold(const float* __restric
   };
   fetch(0);
   for (int i0 = 0; i0 < nseg; i0 += kFold) {
-    float o[kFold], d[kFold];
+    float o[kFold], d[kFold], top = 0.f;
 #pragma unroll
-    for (int i = 0; i < kFold; ++i) o[i] = own[i], d[i] = exp2_hw(A2 * dec[i]);
+    for (int i = 0; i < kFold; ++i) o[i] = own[i], d[i] = exp2_hw(A2 * dec[i]), top = fmaxf(top, d[i]);
     if (i0 + kFold < nseg) fetch(i0 + kFold);
+    // ZERO: a state of zero stays out of the product, whose decay may be infinite (where steps times A are
+    // positive). Chosen here and not at every segment, where it doubles the chain: the call above 174 us, not 172.
+    auto chain = [&](auto zero) {
 #pragma unroll
-    for (int i = 0; i < kFold; ++i)
-      if (i0 + i < nseg) {
-        f[(rev ? nseg - 1 - i0 - i : i0 + i) * step] = x;
-        x = fmaf(d[i], x, o[i]);
-      }
+      for (int i = 0; i < kFold; ++i)
+        if (i0 + i < nseg) {
+          f[(rev ? nseg - 1 - i0 - i : i0 + i) * step] = x;
+          x = decltype(zero)::value && x == 0.f ? o[i] : fmaf(d[i], x, o[i]);
+        }
+    };
+    if (top <= 3.4028234e38f) chain(std::false_type{});
+    else chain(std::true_type{});
   }
   if (rev && dh0) dh0[hat] = x;
 }

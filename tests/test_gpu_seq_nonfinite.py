@@ -76,3 +76,26 @@ def test_scan_padding_behind_an_infinite_state(N, n, S, dtype):
     got = dict(zip(NAMES, T.ttt_backward_selective_scan(**s, d_y=d_y, h0=h0, lengths=lengths)))
     for name in ("d_u", "d_delta", "d_B", "d_C", "d_z"):
         assert torch.isfinite(got[name][0]).all() and not got[name][1, n:].any(), name
+
+
+@pytest.mark.parametrize("N,dtype", [(400, "fp32"), (3000, "bf16")])
+def test_scan_states_of_zero_under_growing_decays(N, dtype):
+    """step A = 8 a token: over a segment the decays' product is infinite, but states are zero until the last two tokens,
+    where h = step B u and then exp(8) h + step B u. Off by the rounding of exp(8) (8 * 2 u + 2 u), of three products and
+    of the sum over 8 states: 40 u of the sum of magnitudes, and the output's own rounding."""
+    i = Inputs(N, dtype)
+    C, S = 64, 8
+    u, Bm, Cm = i.normal(1, N, C), i.normal(1, N, 1, S), i.normal(1, N, 1, S)
+    u[:, :-2] = 0.0
+    delta = torch.full((1, N, C), -4.0, dtype=DT[dtype], device="cuda")
+    A = torch.full((C, S), -2.0, device="cuda")
+    end = torch.empty(1, C, S, device="cuda")
+    y = T.ttt_forward_selective_scan(u, delta, A, Bm, Cm, softplus=False, h_out=end)
+    assert not y[:, :-2].any()
+    drive = -4.0 * u[0, -2:].double()[..., None] * Bm[0, -2:].double()          # [2, C, S]
+    last = 2.718281828459045 ** 8 * drive[0] + drive[1]
+    most = 2.718281828459045 ** 8 * drive[0].abs() + drive[1].abs()
+    unit = 2.0 ** -24
+    assert ((end[0] - last).abs() <= 40 * unit * most).all()
+    want, size = (last * Cm[0, -1].double()).sum(-1), (most * Cm[0, -1].double().abs()).sum(-1)
+    assert ((y[0, -1] - want).abs() <= torch.finfo(DT[dtype]).eps / 2 * want.abs() + 40 * unit * size).all()
