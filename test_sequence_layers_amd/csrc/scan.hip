@@ -582,10 +582,15 @@ __global__ __launch_bounds__(64 * Bwd<S>::NW, S <= 16 ? 3 : 2) void scan_bwd(Sca
   const T* bm = (const T*)a.bm + row0 * a.bs + (long long)un.g * S;
   const T* cm = (const T*)a.cm + row0 * a.cs + (long long)un.g * S;
   const long long seg = (long long)un.b * p.nseg + un.seg;
+  // The padding's sums are zeros: with its states, which may not be finite, they would be 0 times those.
+  for (int t = max(te, t0); t < t1; ++t)
+    if (l < 2 * SW) w.mats[((row0 + t) * p.cb + un.cb) * 2 * S + 2 * SW * wave + l] = 0.f;
   float A2[SW], hs[SW], q[SW], dA[SW];
   for (int s = 0; s < SW; ++s) {
     A2[s] = a.A[(long long)c * S + s0 + s] * kLog2e;
-    hs[s] = w.ends[(seg * S + s0 + s) * C + c];
+    // (Zeros where the sequence ends before: its states may not be finite, and meet gradients of 0 here.)
+    const float start = w.ends[(seg * S + s0 + s) * C + c];
+    hs[s] = t0 < te ? start : 0.f;
     q[s] = w.back[(seg * S + s0 + s) * C + c];  // a q of the token behind
     dA[s] = 0.f;
   }
@@ -644,8 +649,7 @@ __global__ __launch_bounds__(64 * Bwd<S>::NW, S <= 16 ? 3 : 2) void scan_bwd(Sca
         (&s_c[0][0])[e] = in ? nc[i] : 0.f;
       }
     }
-    // (Behind the sequence zeros: its states may not be finite, and are multiplied by gradients of 0 there.)
-    for (int s = 0; s < SW; ++s) h0[s] = tc < te ? fmaf(exp2_hw(A2[s] * npast), hs[s], nck[s]) : 0.f;
+    for (int s = 0; s < SW; ++s) h0[s] = fmaf(exp2_hw(A2[s] * npast), hs[s], nck[s]);
     __syncthreads();
     if (tc > t0) fetch(tc - kSub);
     float e[kSub][SW], h[kSub][SW];
@@ -702,8 +706,8 @@ __global__ __launch_bounds__(64 * Bwd<S>::NW, S <= 16 ? 3 : 2) void scan_bwd(Sca
         }
         __builtin_amdgcn_sched_barrier(0);
       }
-      const float total = tc + jb + tok < te ? join_values<NV, NV>(x) : 0.f;
-      if (!(l & 1) && tc + jb + tok < t1) put(w.mats + ((row0 + tc + jb) * p.cb + un.cb) * 2 * S, lane_part(mat_at, 4), total);
+      const float total = join_values<NV, NV>(x);
+      if (!(l & 1) && tc + jb + tok < te) put(w.mats + ((row0 + tc + jb) * p.cb + un.cb) * 2 * S, lane_part(mat_at, 4), total);
     }
     __syncthreads();
 #pragma unroll

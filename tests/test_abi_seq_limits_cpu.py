@@ -2,6 +2,7 @@
 import pytest
 
 import test_sequence_layers_amd as T
+from seq_plans import scan_segments
 
 F32, BF16 = T.TTT_F32, T.TTT_BF16
 
@@ -15,3 +16,14 @@ def test_layernorm_backward_workspace_of_the_most_rows(dt, M, D):
     need = T.load_library().ttt_backward_layernorm_workspace
     assert 0 < need(dt, M, 1, D) <= 512 * 2 * D * 4 + 255
     assert need(dt, M, 1, D) >= need(dt, 1 << 14, 1, D) // 2
+
+
+@pytest.mark.parametrize("B,N,C,S,G", [(4096, 32768, 1, 8, 1), (4096, 32767, 1, 16, 1), (24, 16384, 4096, 32, 1), (1, 1 << 22, 64, 16, 1),
+                                       (64, 4096, 768, 64, 1), (1, 1 << 17, 1 << 20, 8, 1),
+                                       (60000, 4096, 16, 8, 16), (65535, 3000, 64, 64, 1)])
+def test_scan_segments_are_no_longer_than_sums_allow(B, N, C, S, G):
+    """2048 tokens, in the forward pass where there is more than one."""
+    nseg, tokens = scan_segments(B, N, C, S, G, backward=True)
+    assert tokens <= 2048
+    nseg, tokens = scan_segments(B, N, C, S, G)
+    assert nseg == 1 or tokens <= 2048

@@ -46,3 +46,29 @@ def test_layernorm_of_rows_far_from_zero(D, dtype, sliced):
     worst = (np.abs(got - ref) / bound).max()
     print(f"  {worst:.3f} of the bound", flush=True)
     assert worst <= 1.0
+
+
+def test_scan_gradients_of_very_long_sequences():
+    """4096 sequences of one channel, 32768 tokens each: as many blocks of channels as segments are wanted. All inputs
+    constant, so that every sum is known, and one by one in fp32 it would drift (32768 times 0.003: 98.27 for 98.30,
+    5900 u). Partial sums of at most 2048 tokens, each addition off by at most u of what is held, 65536 of them added
+    1024 in a row and 6 levels: d_D within 3200 u. d_C is v h: h = exp(A sum step), |A| sum step <= 6.6, the sum of a segment's
+    2048 steps within 2048 u and 15 segments' decays multiplied, and 2 u and an exponential each token of the last: (2048 +
+    2) 6.6 + 2 * 2048 + 2 * 15 u < 18000 u."""
+    B, N, S = 4096, 32768, 8
+    full = lambda value, *shape: torch.full(shape, value, device="cuda")  # noqa: E731
+    u, delta, v, a = 0.06, 0.003, 0.05, -0.067
+    d_y = full(v, B, N, 1)
+    got = T.ttt_backward_selective_scan(full(u, B, N, 1), full(delta, B, N, 1), full(a, 1, S), torch.zeros(B, N, 1, S, device="cuda"),
+                                        torch.zeros(B, N, 1, S, device="cuda"), d_y, torch.ones(1, device="cuda"),
+                                        softplus=False, h0=torch.ones(B, 1, S, device="cuda"))
+    r = np.float32
+    v, u, delta, a = (float(r(q)) for q in (v, u, delta, a))
+    d_D, want = float(got[5]), B * N * v * u
+    print(f"  d_D {d_D:.6g}, {want:.6g}: off by {abs(d_D / want - 1) / U:.0f} u", flush=True)
+    d_C = got[4][::512, :, 0, :].double()
+    h = torch.exp(a * delta * torch.arange(1, N + 1, device="cuda", dtype=torch.float64))[None, :, None]
+    off = float((d_C / (v * h) - 1).abs().max())
+    print(f"  d_C off by {off / U:.0f} u", flush=True)
+    assert abs(d_D / want - 1) <= 3200 * U
+    assert off <= 18000 * U
