@@ -138,6 +138,11 @@ struct Walk {
 };
 
 constexpr long long kSimds = 1024;  // of 256 CUs
+// No segment is longer where there is more than one, and none of the backward pass: its sums over tokens (the steps',
+// and those of d_A, d_D and d_delta_bias) take one after the other in fp32, and further ones would drift. (32768 steps
+// of 0.003: off by 5900 times 2^-24. A segment's 16 states, written and read three times, are 2 % of its rows' bytes.)
+constexpr int kLongest = 2048;
+constexpr long long kMostUnits = 1 << 22;
 // How a call is cut up. Channel blocks: 64 channels of one group each.
 struct Plan {
   int cbg, cb;      // channel blocks per group, in all
@@ -788,8 +793,9 @@ __global__ __launch_bounds__(kSumThreads) void scan_bwd_sums(const float* __rest
   (which ? dC : dB)[row * G * S + gs] = (T)acc;
 }
 
-// Segments: at most `want` waves in all and at least min_tokens each, a multiple of `unit` tokens.
-Plan plan_of(int B, int N, int C, int G, int want, int min_tokens, int unit) {
+// Segments: at most `want` waves in all, and at least min_tokens and at most max_tokens each (which goes before
+// `want`), a multiple of `unit` tokens.
+Plan plan_of(int B, int N, int C, int G, int want, int min_tokens, int max_tokens, int unit) {
   Plan p;
   p.cbg = (C / G + 63) / 64;
   p.cb = p.cbg * G;
@@ -797,7 +803,8 @@ Plan plan_of(int B, int N, int C, int G, int want, int min_tokens, int unit) {
   long long nseg = want / blocks;
   const long long most = (N + min_tokens - 1) / min_tokens;
   if (nseg > most) nseg = most;
-  if (nseg < 1) nseg = 1;
+  // (kMostUnits: a launch has fewer than 2^32 threads. Calls that fit the memory stay far below it.)
+  nseg = std::max(nseg, std::min(((long long)N + max_tokens - 1) / max_tokens, std::max(1ll, kMostUnits / blocks)));
   const long long T = ((N + nseg - 1) / nseg + unit - 1) / unit * unit;
   p.T = (int)T;
   p.nseg = (int)((N + T - 1) / T);
@@ -834,12 +841,12 @@ Plan full_rounds(Plan p, int B, int N, int slots, int longest, int unit) {
 Plan fwd_plan(const ScanArgs& a, int S) {
   const long long blocks = (long long)a.B * ((a.C / a.G + 63) / 64 * a.G);
   const bool once = a.N <= 26 + blocks / 5 || blocks >= (S <= 8 ? 1600 : S <= 16 ? 1300 : S <= 32 ? 720 : 820);
-  if (once) return plan_of(a.B, a.N, a.C, a.G, 1, a.N, kTokens);
+  if (once) return plan_of(a.B, a.N, a.C, a.G, 1, a.N, a.N, kTokens);
   const long long by_length = std::min(6 * kSimds, blocks * (a.N / 64));
   const int shortest = std::min(24, std::max(8, (int)(0.45 * sqrt((double)a.N))));
   const long long want = std::max(by_length, (a.lengths ? 4 : 3) * kSimds);
-  const Plan p = plan_of(a.B, a.N, a.C, a.G, (int)want, shortest, kTokens);
-  return full_rounds(p, a.B, a.N, (int)kSimds, p.T + p.T / 2, kTokens);
+  const Plan p = plan_of(a.B, a.N, a.C, a.G, (int)want, shortest, kLongest, kTokens);
+  return full_rounds(p, a.B, a.N, (int)kSimds, std::max(p.T, std::min(p.T + p.T / 2, kLongest)), kTokens);
 }
 // Backward. The walk's workgroups come in rounds of as many as the CUs hold (by its registers 12 waves a CU, 8 of wide
 // states; a workgroup is S / 4 or S / 8 waves), and a round takes as long as its segments: of the segment lengths from
@@ -848,8 +855,9 @@ Plan fwd_plan(const ScanArgs& a, int S) {
 // in the fold and in partial sums: 2 x 4096 x 768 x 32, bf16, 252 us, 275 with twice as many; x 64 486 and 537; 8 x 1024 x 512 x
 // 64, where 22 segments of 48 tokens are 5.5 rounds and 16 of 64 are 4, 363 and 319.
 Plan bwd_plan(const ScanArgs& a, int S) {
-  const Plan p = plan_of(a.B, a.N, a.C, a.G, S <= 16 ? 4096 : 1536, 16, kBwdSub);
-  return full_rounds(p, a.B, a.N, 256 * (S <= 8 ? 6 : S <= 16 ? 3 : S <= 32 ? 2 : 1), 2 * p.T, kBwdSub);
+  const Plan p = plan_of(a.B, a.N, a.C, a.G, S <= 16 ? 4096 : 1536, 16, kLongest, kBwdSub);
+  const int slots = 256 * (S <= 8 ? 6 : S <= 16 ? 3 : S <= 32 ? 2 : 1);
+  return full_rounds(p, a.B, a.N, slots, std::max(p.T, std::min(2 * p.T, kLongest)), kBwdSub);
 }
 
 size_t align_up(size_t x) { return (x + 255) / 256 * 256; }
