@@ -74,14 +74,20 @@ ttt_status enqueue(F* f, A... a) {
   return f(a...);
 }
 
+// A tensor of the caller's that a call has written counts as changed: autograd refuses a gradient that needs its old
+// values. (Tensors made in inference mode have no count.)
+void written(const Tensor& t) {
+  if (!t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
+}
+
 // An output: the caller's tensor or a new one.
 struct Out {
   Tensor t;
   PyObject* given = nullptr;
   void* p = nullptr;
-  PyObject* object() const {  // a new reference
+  PyObject* object() const {  // a new reference, of an output that has been written
     if (!p) Py_RETURN_NONE;
-    if (given) return Py_INCREF(given), given;
+    if (given) return written(THPVariable_Unpack(given)), Py_INCREF(given), given;
     return THPVariable_Wrap(t);
   }
 };
@@ -315,6 +321,7 @@ PyObject* conv1d_forward(PyObject*, PyObject* const* a, Py_ssize_t count) {
   const int silu = truth(a[3]);
   const ttt_status st = enqueue(api.ttt_forward_conv1d, c.dt, n.B, n.N, n.C, n.K, silu, px.p, px.stride, pw, pb, ps,
                                 pl, y.p, pso, c.stream);
+  if (st == TTT_OK && so) written(*so);
   return st == TTT_OK ? y.object() : status(st);
   END_HANDLE_TH_ERRORS
 }
@@ -336,6 +343,7 @@ PyObject* conv1d_step(PyObject*, PyObject* const* a, Py_ssize_t count) {
   const int silu = truth(a[3]);
   const ttt_status st = enqueue(api.ttt_step_conv1d, c.dt, n.B, n.C, n.K, silu, px.p, px.stride, pw, pb, ps, y.p, pso,
                                 c.stream);
+  if (st == TTT_OK) written(so ? *so : state);
   return st == TTT_OK ? y.object() : status(st);
   END_HANDLE_TH_ERRORS
 }
@@ -421,6 +429,7 @@ PyObject* scan_forward(PyObject*, PyObject* const* a, Py_ssize_t count) {
   const int softplus = truth(a[8]);
   const ttt_status st = enqueue(api.ttt_forward_selective_scan, c.dt, s.B, s.N, s.C, s.S, s.G, softplus,
                                 TTT_SCAN_INPUTS(s), ph, pl, y.p, const_cast<float*>(pho), ws, bytes, c.stream);
+  if (st == TTT_OK && ho) written(*ho);
   return st == TTT_OK ? y.object() : status(st);
   END_HANDLE_TH_ERRORS
 }
@@ -441,6 +450,7 @@ PyObject* scan_step(PyObject*, PyObject* const* a, Py_ssize_t count) {
   const int softplus = truth(a[8]);
   const ttt_status st = enqueue(api.ttt_step_selective_scan, c.dt, s.B, s.C, s.S, s.G, softplus, TTT_SCAN_INPUTS(s),
                                 ph, y.p, const_cast<float*>(pho), c.stream);
+  if (st == TTT_OK) written(ho ? *ho : h);
   return st == TTT_OK ? y.object() : status(st);
   END_HANDLE_TH_ERRORS
 }

@@ -6,6 +6,11 @@ operators take 3 us and up on the device, and a host that marshals with ctypes t
 is checked against the layout that the C ABI assumes; wrong ones raise TypeError or ValueError, and what the C ABI
 itself refuses raises TTTError. Outputs and workspaces that are not passed in are allocated. A call runs on the
 current stream of its tensors' device, or on `stream`; buffers it allocates belong to that stream.
+
+As with the layers of ttt.py, autograd has no part in a call: outputs carry no gradient function (nor a forward-mode
+tangent) even where an input requires gradients; a torch.autograd.Function made of a forward and a backward call gives
+them one. Tensors that a call writes, states in place among them, count as changed in place, so that autograd refuses
+gradients that need their old values.
 """
 from __future__ import annotations
 
