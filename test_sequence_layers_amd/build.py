@@ -1,5 +1,5 @@
-"""Build libttt.so (the HIP kernels and the C ABI) for gfx950 with hipcc and _seq_native.so (seq.py's marshalling)
-with g++, in-tree.
+"""Build libttt.so (the HIP kernels and the C ABI) for gfx950 with hipcc and, for Python, _seq_native.so (seq.py's
+marshalling) with g++ against PyTorch, in-tree. libttt.so needs hipcc alone.
 
     python -m test_sequence_layers_amd.build
 """
@@ -46,10 +46,13 @@ SOURCE_FLAGS = {
 }
 
 
-def native_command(out: str) -> list:
+def native_command(out: str):
     """g++ on seq_native.cpp: host code only, against PyTorch's headers and libraries (which the process that
-    loads the module has loaded already)."""
-    torch = os.path.dirname(importlib.util.find_spec("torch").origin)  # (found, not imported)
+    loads the module has loaded already). None where there is no PyTorch."""
+    spec = importlib.util.find_spec("torch")  # (found, not imported)
+    if spec is None or spec.origin is None:
+        return None
+    torch = os.path.dirname(spec.origin)
     return [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
             "-D__HIP_PLATFORM_AMD__=1", "-DUSE_ROCM=1", "-I", os.path.join(ROOT, "include"),
             "-isystem", os.path.join(torch, "include"),
@@ -63,40 +66,63 @@ def flags_for(src: str) -> list:
     return FLAGS + SOURCE_FLAGS.get(src, [])
 
 
-def _run(cmd):
-    p = subprocess.run(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True)
+def _start(cmd):
+    """The command's process, or what kept it from starting."""
+    try:
+        return subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True)
+    except OSError as e:
+        return str(e)
+
+
+def _end(p):
+    """Waits for a started command: (it succeeded, what it said)."""
+    if isinstance(p, str):
+        return False, p
+    out = p.communicate()[0]
     # hipcc's host pass warns that it does not know the packed-fp32 feature; drop that noise.
-    lines = [ln for ln in p.stdout.splitlines() if "packed-fp32-ops" not in ln]
-    return p.returncode, "\n".join(lines)
+    return p.returncode == 0, "\n".join(ln for ln in out.splitlines() if "packed-fp32-ops" not in ln)
+
+
+def _put(tmp, path):
+    """tmp in path's place, or, without a tmp, neither of them."""
+    if tmp is not None:
+        os.replace(tmp, path)
+    else:
+        for f in (path, path + ".tmp"):
+            if os.path.exists(f):
+                os.remove(f)
 
 
 def build(verbose: bool = False) -> str:
-    """Compile every source and link libttt.so and _seq_native.so; returns libttt.so's path. Raises on failure."""
+    """Compile every source and link libttt.so and, where there is PyTorch, _seq_native.so; returns libttt.so's path.
+    Raises on failure: of a HIP source with what was built before left as it was, of the binding with libttt.so in
+    place and no binding."""
     os.makedirs(BUILD_DIR, exist_ok=True)
-    procs = []
-    for src in SOURCES:
-        obj = os.path.join(BUILD_DIR, src.replace(".hip", ".o"))
-        cmd = [HIPCC, *flags_for(src), "-c", os.path.join(CSRC, src), "-o", obj]
-        procs.append((src, obj, subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True)))
-    native = NATIVE + ".tmp"
-    procs.append(("seq_native.cpp", None, subprocess.Popen(native_command(native), stdout=subprocess.PIPE,
-                                                           stderr=subprocess.STDOUT, text=True)))
-    objs = []
-    for src, obj, p in procs:
-        out, _ = p.communicate()
-        out = "\n".join(ln for ln in out.splitlines() if "packed-fp32-ops" not in ln)
-        if p.returncode != 0:
+    objs = [os.path.join(BUILD_DIR, src.replace(".hip", ".o")) for src in SOURCES]
+    procs = [_start([HIPCC, *flags_for(src), "-c", os.path.join(CSRC, src), "-o", obj]) for src, obj in zip(SOURCES, objs)]
+    native, tmp = NATIVE + ".tmp", LIB + ".tmp"
+    command = native_command(native)
+    binding = _start(command) if command else None
+    said = [(src, *_end(p)) for src, p in zip(SOURCES, procs)]  # (all of them: none is left running)
+    bound, bound_said = _end(binding) if command else (False, "")
+    for src, ok, out in said:
+        if not ok:
+            if os.path.exists(native):
+                os.remove(native)
             raise RuntimeError(f"the compiler failed on {src}:\n{out}")
         if verbose and out.strip():
             print(out)
-        if obj is not None:
-            objs.append(obj)
-    tmp = LIB + ".tmp"
-    rc, out = _run([HIPCC, "--offload-arch=gfx950", "-shared", "-fPIC", "-o", tmp, *objs])
-    if rc != 0:
+    ok, out = _end(_start([HIPCC, "--offload-arch=gfx950", "-shared", "-fPIC", "-o", tmp, *objs]))
+    if not ok:
         raise RuntimeError(f"link failed:\n{out}")
-    os.replace(tmp, LIB)
-    os.replace(native, NATIVE)
+    _put(tmp, LIB)
+    _put(native if bound else None, NATIVE)
+    if not command:
+        print("no PyTorch: _seq_native.so (the block operators' Python binding) is left out", file=sys.stderr)
+    elif not bound:
+        raise RuntimeError(f"the compiler failed on seq_native.cpp:\n{bound_said}")
+    elif verbose and bound_said.strip():
+        print(bound_said)
     return LIB
 
 
