@@ -2,7 +2,7 @@
 import pytest
 
 import test_sequence_layers_amd as T
-from seq_plans import scan_segments
+from seq_plans import SCAN_CASES, scan_segments
 
 F32, BF16 = T.TTT_F32, T.TTT_BF16
 
@@ -27,3 +27,13 @@ def test_scan_segments_are_no_longer_than_sums_allow(B, N, C, S, G):
     assert tokens <= 2048
     nseg, tokens = scan_segments(B, N, C, S, G)
     assert nseg == 1 or tokens <= 2048
+
+
+@pytest.mark.parametrize("case", SCAN_CASES, ids=lambda c: "-".join(map(str, c[:6])))
+def test_scan_cases_take_the_plans_that_they_are_for(case):
+    B, N, C, S, G, dtype, _, forward, backward = case
+    dt = F32 if dtype == "fp32" else BF16
+    nseg, tokens = scan_segments(B, N, C, S, G, dtype=dt)
+    assert tokens >= forward and (nseg == 1) == (forward == N)
+    nseg, tokens = scan_segments(B, N, C, S, G, backward=True, dtype=dt)
+    assert tokens >= backward and (nseg == 1) == (backward == N)
