@@ -6,7 +6,7 @@
 // A stream of rows, bound by HBM: each row is read once into registers by a group of L lanes (8 lanes
 // for a head of 64 bf16 channels, a wave, or a workgroup of 256 threads for wide rows), the
 // statistics are taken there in two passes over the registers (the mean, then the centred squares:
-// no cancellation; for the mean see Row), and the result is written from them. The backward pass recomputes the
+// no cancellation; for the mean see RowX), and the result is written from them. The backward pass recomputes the
 // statistics, since it has to read x anyway; each group keeps the same channels over the rows it
 // walks, so that dw and db stay in registers until its last row; a workgroup's groups are joined in
 // LDS, and a second launch sums the workgroups' partial rows in a fixed order. bf16: forward of 32768 x 12
@@ -45,49 +45,65 @@ __device__ __forceinline__ float row_sum(float v, float (*red)[16], int slot) {
 }
 
 // One row: element (k L + lane) V + i is v[k V + i]. Past D the row's first elements are loaded again,
-// and zeroed when they are used. X: x's, which in fp32 are taken less the row's first element, so that their sums
-// lose what 24 bits of the differences lose and not of the values, and a constant row is centred to zeros
-// (1e5 + N(0, 1): y off by 1e-2 without, 1e-6 with it; 1537 x 1001 backward 13.9 us, 13.8 without). In bf16 a row so far
-// from zero for its spread has neighbouring values, and their sums are exact.
-template <class T, int L, int K, int V, bool X>
+// and made `past` when they are used.
+template <class T, int L, int K, int V>
 struct Row {
-  static constexpr bool kLess = X && sizeof(T) == 4;
   Raw<T, V> r[K];
-  float first;
   __device__ __forceinline__ void load(const T* p, int lane, int D) {
-    if (kLess) first = p[0];
 #pragma unroll
     for (int k = 0; k < K; ++k) {
       const int at = (k * L + lane) * V;
       r[k].load(p + (at < D ? at : 0));
     }
   }
-  __device__ __forceinline__ void widen(float* v, int lane, int D, bool in = true) const {
+  __device__ __forceinline__ void widen(float* v, int lane, int D, bool in = true, float past = 0.f) const {
 #pragma unroll
     for (int k = 0; k < K; ++k) {
       r[k].widen(v + k * V);
       const bool ok = in && (k * L + lane) * V < D;
-      for (int i = 0; i < V; ++i) {
-        const float x = kLess ? v[k * V + i] - first : v[k * V + i];
-        v[k * V + i] = ok || (kLess && V == 1) ? x : 0.f;  // (the first element less itself needs no choice)
-      }
+      for (int i = 0; i < V; ++i) v[k * V + i] = ok ? v[k * V + i] : past;
     }
   }
 };
 
-// v -> v - mean (zero past D); returns rstd.
-template <int L, int K, int V>
-__device__ __forceinline__ float centre(float* v, int lane, int D, float eps, float (*red)[16]) {
+// A row of x. In fp32 its first element comes along: the mean is taken of what the elements differ from it, so that a
+// row far from zero loses what 24 bits of its differences lose and not of its values, and a constant row is centred to
+// zeros (1e5 + N(0, 1): y off by 1e-2 without, 1e-6 with it; 1537 x 1001 backward 13.8 us with and without). In bf16 a row so
+// far from zero for its spread has neighbouring values, and their sums are exact.
+template <class T, int L, int K, int V>
+struct RowX : Row<T, L, K, V> {
+  static constexpr bool kFirst = sizeof(T) == 4;
+  float first;
+  __device__ __forceinline__ void load(const T* p, int lane, int D) {
+    first = kFirst ? (float)p[0] : 0.f;
+    Row<T, L, K, V>::load(p, lane, D);
+  }
+  // Row::widen, with the first element past D, which single elements are there already.
+  __device__ __forceinline__ void widen(float* v, int lane, int D) const {
+    if constexpr (kFirst && V == 1) {
+#pragma unroll
+      for (int k = 0; k < K; ++k) this->r[k].widen(v + k);
+    } else {
+      Row<T, L, K, V>::widen(v, lane, D, true, first);
+    }
+  }
+};
+
+// v -> v - mean (zero past D); returns rstd. With a first element the mean is the sum of two numbers, hi + lo, since
+// as one it would be off by half a step of it.
+template <bool FIRST, int L, int K, int V>
+__device__ __forceinline__ float centre(float* v, float first, int lane, int D, float eps, float (*red)[16]) {
   float s = 0.f;
 #pragma unroll
-  for (int j = 0; j < K * V; ++j) s += v[j];
+  for (int j = 0; j < K * V; ++j) s += FIRST ? v[j] - first : v[j];
   const float mean = row_sum<L>(s, red, 0) / (float)D;
+  const float hi = FIRST ? first + mean : mean, lo = FIRST ? (first - hi) + mean : 0.f;
   float q = 0.f;
 #pragma unroll
   for (int k = 0; k < K; ++k)
     for (int i = 0; i < V; ++i) {
       float& x = v[k * V + i];
-      x = (k * L + lane) * V < D ? x - mean : 0.f;
+      x = (k * L + lane) * V < D ? (FIRST ? (x - hi) - lo : x - hi) : 0.f;
       q = fmaf(x, x, q);
     }
   return rcp_hw(sqrtf(fmaf(row_sum<L>(q, red, 1), rcp_hw((float)D), eps)));
@@ -103,11 +119,11 @@ __global__ __launch_bounds__(threads_of<L>) void layernorm_fwd(const T* __restri
   const long long row = wide_block() * (threads_of<L> / L) + threadIdx.x / L;
   if (row >= rows) return;  // (whole groups; for L > 64 the whole workgroup)
   const int m = (int)(row / H), h = (int)(row - (long long)m * H);
-  Row<T, L, K, V, true> raw;
+  RowX<T, L, K, V> raw;
   raw.load(x + (long long)m * xs + (long long)h * D, lane, D);
   float v[K * V];
   raw.widen(v, lane, D);
-  const float rstd = centre<L, K, V>(v, lane, D, eps, red);
+  const float rstd = centre<raw.kFirst, L, K, V>(v, raw.first, lane, D, eps, red);
   T* py = y + row * D;
 #pragma unroll
   for (int k = 0; k < K; ++k) {
@@ -150,8 +166,8 @@ __global__ __launch_bounds__(bwd_threads(L, K* V)) void layernorm_bwd(const T* _
     }
   };
   if (kRoom) weights();
-  Row<T, L, K, V, true> rx;
-  Row<T, L, K, V, false> rd;
+  RowX<T, L, K, V> rx;
+  Row<T, L, K, V> rd;
   auto fetch = [&](long long m) {  // (past the last token: the last again)
     const long long t = m < M ? m : M - 1;
     rx.load(x + t * xs + (long long)h * D, lane, D);
@@ -166,8 +182,9 @@ __global__ __launch_bounds__(bwd_threads(L, K* V)) void layernorm_bwd(const T* _
     if (!kRoom) fetch(m);
     rx.widen(v, lane, D);
     rd.widen(d, lane, D, in);
+    const float first = rx.first;
     if (kRoom) fetch(m + step);
-    const float rstd = centre<L, K, V>(v, lane, D, eps, red);
+    const float rstd = centre<rx.kFirst, L, K, V>(v, first, lane, D, eps, red);
     if (!kRoom) weights();
     float s1 = 0.f, s2 = 0.f;
 #pragma unroll

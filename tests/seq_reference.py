@@ -36,14 +36,14 @@ def _silu(x):
 
 # ---------------------------------------------------------------------------------- layer norm
 def layernorm(x, w, b, d_y, eps, depth, rows_depth):
-    """{y, d_x, d_weight, d_bias: (value, bound)}; x [..., D] with w [D], or [..., H, D] with [H, D]. fp32 rows are
-    summed less their first element. depth: additions in a row's sums; rows_depth: in a parameter's."""
+    """{y, d_x, d_weight, d_bias: (value, bound)}; x [..., D] with w [D], or [..., H, D] with [H, D]. The
+    mean of an fp32 row is its first element and the mean of what the others differ from it, kept as two numbers. depth: additions in a row's sums; rows_depth: in a parameter's."""
     fp32 = x.dtype == torch.float32
     x, w, b, d_y = _d(x), _d(w), _d(b), _d(d_y)
     mean = lambda t: t.mean(-1, keepdim=True)  # noqa: E731
     e = (x - x[..., :1]) if fp32 else x
     c = x - mean(x)
-    off = U * c.abs() + U * e.abs() * fp32 + (depth + 3) * U * mean(e.abs())
+    off = (1 + fp32) * U * c.abs() + (depth + 3) * U * mean(e.abs())
     var = mean(c * c)
     off_var = 2 * mean(c.abs() * off) + (depth + 4) * U * var
     rstd = 1 / torch.sqrt(var + eps)
