@@ -332,22 +332,26 @@ __global__ __launch_bounds__(kFoldThreads) void scan_fold(const float* __restric
   };
   fetch(0);
   for (int i0 = 0; i0 < nseg; i0 += kFold) {
-    float o[kFold], d[kFold], top = 0.f;
+    float o[kFold], d[kFold];
 #pragma unroll
-    for (int i = 0; i < kFold; ++i) o[i] = own[i], d[i] = exp2_hw(A2 * dec[i]), top = fmaxf(top, d[i]);
+    for (int i = 0; i < kFold; ++i) o[i] = own[i], d[i] = exp2_hw(A2 * dec[i]);
     if (i0 + kFold < nseg) fetch(i0 + kFold);
-    // ZERO: a state of zero stays out of the product, whose decay may be infinite (where steps times A are
-    // positive). Chosen here and not at every segment, where it doubles the chain: the call above 174 us, not 172.
     auto chain = [&](auto zero) {
+      int left = nseg - i0;
+      // (Its own in either chain: conditions shared by the two would take 64 SGPRs.)
+      asm volatile("" : "+s"(left));
 #pragma unroll
       for (int i = 0; i < kFold; ++i)
-        if (i0 + i < nseg) {
+        if (i < left) {
           f[(rev ? nseg - 1 - i0 - i : i0 + i) * step] = x;
           x = decltype(zero)::value && x == 0.f ? o[i] : fmaf(d[i], x, o[i]);
         }
     };
-    if (top <= 3.4028234e38f) chain(std::false_type{});
-    else chain(std::true_type{});
+    // Where steps times A are positive a decay may be infinite, and NaN with a state of zero, which has no part of it:
+    // then these segments again, zeros kept out. (Chosen at every segment the choice is a third of the chain.)
+    const float start = x;
+    chain(std::false_type{});
+    if (x != x) x = start, chain(std::true_type{});
   }
   if (rev && dh0) dh0[hat] = x;
 }
