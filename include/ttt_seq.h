@@ -138,6 +138,9 @@ ttt_status ttt_step_selective_scan(ttt_dtype dt, int B, int C, int S, int G, int
  * NULL. The forward pass is recomputed from the inputs, nothing of it has to be kept. step * A must not be
  * positive by so much that exp of its sum over a run of tokens is infinite in fp32: gradients are NaN then, also
  * where states or d_y are zeros.
+ * The workspace holds states every 8 tokens and each block of 64 channels' sums for d_B and d_C: about 5 S / 8 + 1 bytes per
+ * token and channel where a group's channels are whole blocks (the sums are 8 S bytes per token and block), and 12 (S + 1)
+ * per channel and segment of 16 to 2048 tokens: 106 MB for bf16 2 x 4096 x 768 x 16, 5.5 GB for 8 x 8192 x 2048 x 64.
  */
 ttt_status ttt_backward_selective_scan(ttt_dtype dt, int B, int N, int C, int S, int G, int softplus,
                                        const void* u, long long u_stride, const void* delta,

@@ -3,8 +3,8 @@
 //   pre[n] = bias + sum_k w[k] x[n - (K - 1) + k],   y = pre or pre sigmoid(pre)
 //   dpre = dy act'(pre),  dx[n] = sum_k w[k] dpre[n + K - 1 - k],  dw[k] = sum dpre[n] x[n - (K - 1) + k]
 //
-// A stream bound by HBM. A thread owns 8 bytes of channels (one channel where rows are not 8-byte
-// aligned) and walks down a run of tokens with the last K inputs in registers, so that every
+// A stream bound by HBM. A thread owns four channels, 8 bytes of bf16 or 16 of fp32 (one channel where rows are not
+// whole such pieces), and walks down a run of tokens with the last K inputs in registers, so that every
 // input is read once but for the K - 1 tokens before each run (from L2). The next tokens are loaded while
 // the last are worked on, and nothing in the walk branches: loads are clamped to the sequence and
 // their values chosen, stores past the run write its last row again with the same value, so that no

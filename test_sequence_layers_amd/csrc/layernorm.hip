@@ -149,7 +149,9 @@ __global__ __launch_bounds__(bwd_threads(L, K* V)) void layernorm_bwd(const T* _
                                                                int HB, int R, float eps) {
   constexpr int LKV = L * K * V;
   // A workgroup of 1024 threads has 128 registers a lane: there the weights are read again for each row,
-  // and rows are not loaded ahead.
+  // and rows are not loaded ahead. It is too few all the same for the widest rows, whose accumulators are partly
+  // held in memory: 84 (fp32) and 73 registers of single elements, from 4097 channels on that are not whole
+  // 16-byte pieces, 20 and 11 of aligned rows wider than 8192.
   constexpr bool kRoom = L <= 256;
   __shared__ float red[4][16];
   __shared__ float join[L <= 64 ? bwd_threads(L, K * V) * K * V : 1];
@@ -323,8 +325,8 @@ struct FwdCall {
   }
 };
 
-// The backward's grid: heads per workgroup, tokens at a time, workgroups along the tokens. It does not
-// depend on whether the vector path is taken (both fit the workspace sized for the larger).
+// The backward's grid: heads per workgroup, tokens at a time, workgroups along the tokens. It goes by the shape, so
+// the 16-byte path and the other have different ones, and the workspace is sized for the larger.
 struct BwdPlan {
   int HB, R, gy;
   long long P;

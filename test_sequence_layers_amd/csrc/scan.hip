@@ -53,7 +53,7 @@ __device__ __forceinline__ float softplus_of(float x, float& e) {
   for (int i = 3; i >= 0; --i) p = fmaf(p, q, kLog1pP[i]);
   return fmaf(s, p, fmaxf(x, 0.f));
 }
-// The step and its derivative by delta.
+// The step; below with its derivative by delta.
 __device__ __forceinline__ float step_of(float raw, int softplus) {
   float e;
   const float dt = softplus_of(raw, e);  // (chosen, not branched to: a branch would part the tokens of a chunk)
@@ -99,12 +99,17 @@ __device__ __forceinline__ void outer(float row, float x, f32x4* acc) {
   if constexpr (NB > 1) outer<AT + 1, NB - 1>(row, x, acc + 1);
 }
 
-// Where B comes as one element per lane and through outer(), instead of as scalars: where a token's scalars would be
-// more than the SGPRs hold ahead of their use. In the last run, which has C's as well, always (768 channels, bf16,
-// without and with it: 2 x 4096 tokens of 8 states 52 and 48 us, of 16 69 and 66; 3 x 1999 x 1000 of 32, fp32, its last
-// run 52 and 36; but 32768 x 1536 of 16 320 and 327). In the first from 64 bytes on (2 x 2048 tokens of 64 states, bf16,
-// 121 and 107 us, 4 x 8192 of 32, bf16, 307 and 303; but of 16, traced, 75 and 79): an outer product takes as long as
-// its four multiplications (16 cycles).
+// Where B comes as one element per lane and through outer(), instead of as scalars. An outer product takes as long as its
+// four multiplications (16 cycles), so it gains only where a token's scalars are more than the SGPRs hold ahead of
+// their use: in the last run, which has C's as well, always; in the first from rows of 64 bytes on.
+//                                              scalars   outer()
+//   last run   2 x 4096 x 768 x 8, bf16           52 us      48 us
+//              2 x 4096 x 768 x 16, bf16          69         66
+//              3 x 1999 x 1000 x 32, fp32         52         36    (the run alone)
+//              1 x 32768 x 1536 x 16, bf16       320        327    (the other way, by 2 %)
+//   first run  2 x 2048 x 768 x 64, bf16         121        107
+//              4 x 8192 x 768 x 32, bf16         307        303
+//              4 x 8192 x 768 x 16, bf16          75         79    (the run alone; 32 bytes: scalars)
 template <class T, int S, bool FINAL>
 constexpr bool outer_rows = FINAL || S * sizeof(T) >= 64;
 
@@ -828,20 +833,30 @@ Plan full_rounds(Plan p, int B, int N, int slots, int longest, int unit) {
   return p;
 }
 
-// Forward: three waves per SIMD, and more where segments stay longer than 64 tokens, up to six: segments cost
-// the fold's traffic and their start, waves hide what a token waits for (768 channels, bf16, 16 states, three and
-// six: 2 x 4096 tokens 68 and 72 us, 4 x 8192 189 and 183). Sequences of their own lengths end early, and their waves
-// with them: there four (3 x <= 1999 x 1000 x 32, fp32: a tenth less than with three). The shortest segment goes with
-// the root of the length, from 8 to 24 tokens, since the fold takes longer the more there are (16 states, 24, 12 and 8
-// tokens: 1 x 102 x 64 21, 16 and 14 us; 2 x 333 x 193 23, 17 and 17; 1 x 1024 x 768 28, 26 and 31); it may be half longer
-// where that fills rounds of a wave on each SIMD (2 x 2048 x 768, 16 states: 44 us, 49 without, 64 states 108 and 119). One
-// segment where a second run over the tokens costs more than it gives. That is so for short sequences, the longer
-// the more blocks of channels there are (768 channels, bf16, 16 states, one launch and three: one sequence of 24 tokens
-// 11.5 and 14.0 us, of 32 14.2 and 14.0; 8 of 32 14.4 and 16.6, of 48 19.9 and 17.3; 24 of 64 26 and 33, of 96 37 and 35;
-// 64 of 160 71 and 79), and from the number of blocks on that keeps
-// the SIMDs busy by itself (2048 tokens: 8 states 1536 blocks 873 and 780, 1728 883 and 1008; 16 1248 1179 and 1039,
-// 1344 1184 and 1200; 32 672 1085 and 965, 768 1084 and 1083; 64 768 2358 and 2014, 864 2365 and 2305; 512 tokens: 32
-// 576 266 and 255, 768 266 and 307; 64 576 546 and 472, 768 548 and 569).
+// Forward.
+//
+// One segment, and one launch, where a second run over the tokens costs more than it gives:
+//  * sequences of at most 26 tokens and one more for every 5 blocks of channels (768 channels, bf16, 16 states; one
+//    launch and three, us): 1 x 24 tokens 11.5, 14.0; 1 x 32 14.2, 14.0; 8 x 32 14.4, 16.6; 8 x 48 19.9, 17.3; 24 x 64 26, 33;
+//    24 x 96 37, 35; 64 x 160 71, 79;
+//  * as many blocks as keep the SIMDs busy by themselves, found at 2048 tokens of 768 channels in bf16 (one and three):
+//       8 states   1536 blocks  873,  780     1728  883, 1008     from 1600
+//      16          1248        1179, 1039     1344 1184, 1200     from 1300
+//      32           672        1085,  965      768 1084, 1083     from  720
+//      64           768        2358, 2014      864 2365, 2305     from  820
+//    It is not a law of the states alone: at 512 tokens 32 states change over between 576 (266, 255) and 768 (266, 307) as
+//    well, but 64 between 576 (546, 472) and 768 (548, 569), so that up to 820 blocks of short sequences take 4 % longer.
+//
+// Otherwise segments for a number of waves, since segments cost the fold's traffic and their start, and waves hide what a
+// token waits for:
+//  * three per SIMD, and up to six while segments stay longer than 64 tokens (16 states, bf16, three and six: 2 x 4096 x
+//    768 68, 72; 4 x 8192 x 768 189, 183);
+//  * four with lengths, whose sequences end early, and their waves with them (from one case, 3 x <= 1999 x 1000 x 32, fp32:
+//    a tenth less than three);
+//  * none shorter than 8 to 24 tokens by the root of the length, since the fold takes longer the more there are (16 states;
+//    24, 12 and 8 tokens: 1 x 102 x 64 21, 16, 14; 2 x 333 x 193 23, 17, 17; 1 x 1024 x 768 28, 26, 31);
+//  * up to half longer where that fills rounds of a wave on each SIMD (2 x 2048 x 768, without and with: 16 states 49, 44;
+//    64 states 119, 108), none longer than kLongest.
 Plan fwd_plan(const ScanArgs& a, int S) {
   const long long blocks = (long long)a.B * ((a.C / a.G + 63) / 64 * a.G);
   const bool once = a.N <= 26 + blocks / 5 || blocks >= (S <= 8 ? 1600 : S <= 16 ? 1300 : S <= 32 ? 720 : 820);
@@ -852,12 +867,12 @@ Plan fwd_plan(const ScanArgs& a, int S) {
   const Plan p = plan_of(a.B, a.N, a.C, a.G, (int)want, shortest, kLongest, kTokens);
   return full_rounds(p, a.B, a.N, (int)kSimds, std::max(p.T, std::min(p.T + p.T / 2, kLongest)), kTokens);
 }
-// Backward. The walk's workgroups come in rounds of as many as the CUs hold (by its registers 12 waves a CU, 8 of wide
-// states; a workgroup is S / 4 or S / 8 waves), and a round takes as long as its segments: of the segment lengths from
-// the shortest to twice that, the one whose rounds take the fewest tokens in all. The shortest is 16 tokens (2 x 333 x
-// 193 x 8 28 us, 36 at 24, 43 at 32) or what 4096 blocks' segments leave, 1536 of wide states, whose segments cost more
-// in the fold and in partial sums: 2 x 4096 x 768 x 32, bf16, 252 us, 275 with twice as many; x 64 486 and 537; 8 x 1024 x 512 x
-// 64, where 22 segments of 48 tokens are 5.5 rounds and 16 of 64 are 4, 363 and 319.
+// Backward. The walk's workgroups (S / 4 or, of wide states, S / 8 waves) come in rounds of as many as the CUs hold (12 waves a
+// CU by its registers, 8 of wide states), and a round takes as long as its segments. So of the segment lengths from a
+// shortest to twice that, the one whose rounds take the fewest tokens in all (8 x 1024 x 512 x 64: 22 segments of 48 tokens
+// are 5.5 rounds, 363 us, 16 of 64 are 4, 319 us). The shortest is 16 tokens (2 x 333 x 193 x 8 28 us; 24 36, 32 43) or what 4096
+// blocks' segments leave, 1536 of wide states, whose segments cost more in the fold and in partial sums (1536 and twice
+// as many, 2 x 4096 x 768, bf16: 32 states 252, 275; 64 486, 537); the longest kLongest.
 Plan bwd_plan(const ScanArgs& a, int S) {
   const Plan p = plan_of(a.B, a.N, a.C, a.G, S <= 16 ? 4096 : 1536, 16, kLongest, kBwdSub);
   const int slots = 256 * (S <= 8 ? 6 : S <= 16 ? 3 : S <= 32 ? 2 : 1);
