@@ -13,6 +13,8 @@
 // heads x 64 18.9 us (101 MB at 5.3 TB/s, the rate of a large copy), of 65536 x 768 34.7 us; backward of 65536 x
 // 768 66.6 us (302 MB at 4.5 TB/s), of 12544 x 384 14.7 us, where the start and end of the two launches are
 // most of it.
+#include <algorithm>
+
 #include "internal.hpp"
 #include "rowops.hpp"
 #include "seq.hpp"
@@ -331,6 +333,7 @@ struct BwdPlan {
   int HB, R, gy;
   long long P;
 };
+constexpr long long kTurns = 2048;
 BwdPlan bwd_plan(Shape s, int M, int H) {
   const int threads = bwd_threads(s.L, s.K * s.V), groups = s.L <= 64 ? threads / s.L : 1;
   BwdPlan p;
@@ -340,7 +343,10 @@ BwdPlan bwd_plan(Shape s, int M, int H) {
   p.P = ((long long)M + p.R - 1) / p.R;
   // Workgroups: four waves per SIMD of 256 CUs with 1024 threads each, two with fewer (8192 x 4096: 50.5 us
   // with 512 workgroups, 55.8 with 768, 63 with 1024; 65536 x 768: 66.6, 63.7 and 67.1).
-  const long long wgs = threads >= 1024 ? 256 : 512, most = wgs > p.gy ? wgs / p.gy : 1;
+  // More where a group would walk further than kTurns rows, whose sums are one after the other: 32768 times 0.77 came
+  // out off by 6770 times 2^-24, 16 times 2048 by 253.
+  const long long wgs = threads >= 1024 ? 256 : 512;
+  const long long most = std::max({1ll, wgs / p.gy, (p.P + kTurns - 1) / kTurns});
   if (p.P > most) {  // as many turns each, up to one
     const long long turns = (p.P + most - 1) / most;
     p.P = (p.P + turns - 1) / turns;
