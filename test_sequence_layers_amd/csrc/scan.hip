@@ -796,9 +796,14 @@ __global__ __launch_bounds__(kSumThreads) void scan_bwd_sums(const float* __rest
   const long long row = id / width;
   const int r = (int)(id - row * width), which = r / (G * S), gs = r - which * G * S, g = gs / S, s = gs - g * S;
   const float* m = mats + ((row * G + g) * cbg * 2 + which) * S + s;
+  // (64 blocks at a time: one after the other 16384 of them drift.)
   float acc = 0.f;
+  for (int k0 = 0; k0 < cbg; k0 += 64) {
+    float part = 0.f;
 #pragma unroll 4
-  for (int k = 0; k < cbg; ++k) acc += m[(long long)k * 2 * S];
+    for (int k = k0; k < min(k0 + 64, cbg); ++k) part += m[(long long)k * 2 * S];
+    acc += part;
+  }
   (which ? dC : dB)[row * G * S + gs] = (T)acc;
 }
 

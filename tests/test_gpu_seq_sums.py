@@ -83,3 +83,16 @@ def test_layernorm_gradients_of_many_heads_and_rows():
     off = float((d_bias.double() / (M * float(np.float32(0.77))) - 1).abs().max())
     print(f"  off by {off / U:.0f} u", flush=True)
     assert off <= 2200 * U
+
+
+def test_scan_gradients_of_very_many_channels():
+    """d_B and d_C of 2^20 channels whose products are all 0.77: blocks of 64 without rounding, then 16384 blocks, 64 at a
+    time: 64 and 256 additions and a few more, 350 u. (One after the other they are 3300 u off.)"""
+    C, S = 1 << 20, 8
+    one = lambda *shape: torch.ones(*shape, device="cuda")  # noqa: E731
+    got = T.ttt_backward_selective_scan(one(1, 1, C), one(1, 1, C), torch.zeros(C, S, device="cuda"), one(1, 1, 1, S), one(1, 1, 1, S),
+                                        0.77 * one(1, 1, C), softplus=False)
+    for name, t in (("d_B", got[3]), ("d_C", got[4])):
+        off = float((t.double() / (C * float(np.float32(0.77))) - 1).abs().max())
+        print(f"  {name} off by {off / U:.0f} u", flush=True)
+        assert off <= 350 * U, name
