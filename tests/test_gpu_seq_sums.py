@@ -96,3 +96,14 @@ def test_scan_gradients_of_very_many_channels():
         off = float((t.double() / (C * float(np.float32(0.77))) - 1).abs().max())
         print(f"  {name} off by {off / U:.0f} u", flush=True)
         assert off <= 350 * U, name
+
+
+def test_conv1d_gradients_of_very_many_tokens():
+    """d_bias of 2^28 tokens of 0.77: runs of 32 tokens, 8 of a workgroup, and 2^20 partial rows, 64 threads to a column with
+    2048 sums of 8 each and 6 levels: within 2110 u. (16384 rows one after the other are 3300 u off.)"""
+    B, N, C = 64, 1 << 22, 4
+    x, d_y = torch.zeros(B, N, C, device="cuda"), torch.full((B, N, C), 0.77, device="cuda")
+    d_bias = T.ttt_backward_conv1d(x, torch.ones(C, 4, device="cuda"), torch.zeros(C, device="cuda"), d_y)[2]
+    off = float((d_bias.double() / (B * N * float(np.float32(0.77))) - 1).abs().max())
+    print(f"  off by {off / U:.0f} u", flush=True)
+    assert off <= 2110 * U
