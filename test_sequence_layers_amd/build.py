@@ -114,6 +114,8 @@ def build(verbose: bool = False) -> str:
             print(out)
     ok, out = _end(_start([HIPCC, "--offload-arch=gfx950", "-shared", "-fPIC", "-o", tmp, *objs]))
     if not ok:
+        if os.path.exists(native):
+            os.remove(native)
         raise RuntimeError(f"link failed:\n{out}")
     _put(tmp, LIB)
     _put(native if bound else None, NATIVE)

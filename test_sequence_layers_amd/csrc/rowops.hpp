@@ -111,8 +111,9 @@ inline dim3 wide_grid(long long blocks) {
 __device__ __forceinline__ long long wide_block() { return (long long)blockIdx.y * gridDim.x + blockIdx.x; }
 
 // Sum of P rows of W fp32 values in a fixed order: thread row ty of kSumRows adds rows ty, ty + kSumRows, ..., eight at
-// a time (2^20 rows of equal values: off by 253 times 2^-24, 3327 one by one), then the thread rows are added pairwise. out(column, sum) stores it. Few columns per workgroup: a
-// narrow matrix of many rows is spread over more CUs, and a thread has a few rounds of loads at most.
+// a time (2^20 rows of equal values: off by 253 times 2^-24, 3327 one by one), then the thread rows are added
+// pairwise. out(column, sum) stores it. Few columns per workgroup: a narrow matrix of many rows is spread over more
+// CUs, and a thread has a few rounds of loads at most.
 constexpr int kSumCols = 16, kSumRows = 64, kSumThreads = kSumCols * kSumRows;
 template <class Out>
 __device__ __forceinline__ void column_sum_block(const float* __restrict__ part, long long P, int W, int block,

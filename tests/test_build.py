@@ -70,3 +70,13 @@ def test_a_failing_source_leaves_what_was_built(at, hipcc):
     with pytest.raises(RuntimeError, match=r"\.hip"):
         B.build()
     assert (d / "libttt.so").read_text() == "as it was" and (d / "_seq_native.so").read_text() == "as it was"
+
+
+def test_a_failing_link_leaves_what_was_built(at):
+    d = at(hipcc="#!/bin/sh\ncase \"$*\" in *-shared*) echo no space; exit 1;; esac\n" + OK.split("\n", 1)[1])
+    (d / "libttt.so").write_text("as it was")
+    (d / "_seq_native.so").write_text("as it was")
+    with pytest.raises(RuntimeError, match="link failed"):
+        B.build()
+    assert (d / "libttt.so").read_text() == "as it was" and (d / "_seq_native.so").read_text() == "as it was"
+    assert not (d / "_seq_native.so.tmp").exists()

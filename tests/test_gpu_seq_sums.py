@@ -13,6 +13,12 @@ from seq_helpers import Inputs, U, f64
 EPS = 1e-5
 
 
+@pytest.fixture(autouse=True)
+def _memory():
+    yield
+    torch.cuda.empty_cache()
+
+
 @pytest.mark.parametrize("H,D,dtype", [(1, 64, "fp32"), (12, 64, "fp32"), (1, 300, "fp32"), (1, 768, "fp32"), (1, 1001, "fp32"),
                                        (1, 1001, "bf16"), (1, 4096, "fp32"), (1, 4100, "fp32"), (1, 16384, "fp32")])
 def test_layernorm_of_constant_rows_is_the_bias(H, D, dtype):
