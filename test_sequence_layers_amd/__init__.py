@@ -18,6 +18,13 @@ backward pass (seq.py):
   * ttt_forward_conv1d, ttt_step_conv1d, ttt_backward_conv1d (short causal depth-wise convolution);
   * ttt_forward_selective_scan, ttt_step_selective_scan, ttt_backward_selective_scan (selective state
     space scan); the step forms take one token of every sequence and update its state.
+
+Those of include/ttt_lm.h, the operators of a language model's residual block (lm.py):
+  * ttt_forward_rmsnorm, ttt_forward_rmsnorm_e4m3, ttt_backward_rmsnorm (RMS norm with the residual's
+    addition, dropout of what is added, and an output in 8 bits);
+  * ttt_forward_dropout, ttt_backward_dropout, dropout_counters (dropout whose mask is never stored);
+  * ttt_forward_gated_recurrence, ttt_step_gated_recurrence, ttt_backward_gated_recurrence (gated linear
+    recurrence, one state per channel).
 """
 from .ttt import (  # noqa: F401
     TTT_BF16, TTT_F32, TTT_NOALLOC_SCRATCH_BYTES, TTT_OP_BIDIR, TTT_OP_CAUSAL, TTT_OP_FULLBATCH,
@@ -28,3 +35,6 @@ from .ttt import (  # noqa: F401
 from .seq import (  # noqa: F401
     ttt_backward_conv1d, ttt_backward_layernorm, ttt_backward_selective_scan, ttt_forward_conv1d, ttt_forward_layernorm,
     ttt_forward_selective_scan, ttt_step_conv1d, ttt_step_selective_scan)
+from .lm import (  # noqa: F401
+    dropout_counters, ttt_backward_dropout, ttt_backward_gated_recurrence, ttt_backward_rmsnorm, ttt_forward_dropout,
+    ttt_forward_gated_recurrence, ttt_forward_rmsnorm, ttt_forward_rmsnorm_e4m3, ttt_step_gated_recurrence)

@@ -1,5 +1,5 @@
 """Build libttt.so (the HIP kernels and the C ABI) for gfx950 with hipcc and, for Python, _seq_native.so (seq.py's
-marshalling) with g++ against PyTorch, in-tree. libttt.so needs hipcc alone.
+and lm.py's marshalling) with g++ against PyTorch, in-tree. libttt.so needs hipcc alone.
 
     python -m test_sequence_layers_amd.build
 """
@@ -17,7 +17,8 @@ CSRC = os.path.join(HERE, "csrc")
 BUILD_DIR = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libttt.so")
 SOURCES = ["abi.hip", "fullbatch.hip", "chunked.hip", "mlp.hip", "dwconv.hip", "grid.hip", "epilogue.hip",
-           "abi_seq.hip", "layernorm.hip", "conv1d.hip", "scan.hip"]
+           "abi_seq.hip", "layernorm.hip", "conv1d.hip", "scan.hip",
+           "abi_lm.hip", "rmsnorm.hip", "dropout.hip", "recurrence.hip"]
 NATIVE = os.path.join(HERE, "_seq_native.so")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
@@ -47,7 +48,7 @@ SOURCE_FLAGS = {
 
 
 def native_command(out: str):
-    """g++ on seq_native.cpp: host code only, against PyTorch's headers and libraries (which the process that
+    """g++ on seq_native.cpp and lm_native.cpp: host code only, against PyTorch's headers and libraries (which the process that
     loads the module has loaded already). None where there is no PyTorch."""
     spec = importlib.util.find_spec("torch")  # (found, not imported)
     if spec is None or spec.origin is None:
@@ -58,7 +59,7 @@ def native_command(out: str):
             "-isystem", os.path.join(torch, "include"),
             "-isystem", os.path.join(torch, "include", "torch", "csrc", "api", "include"),
             "-isystem", "/opt/rocm/include", "-isystem", sysconfig.get_paths()["include"], "-Wall", "-Wextra",
-            os.path.join(CSRC, "seq_native.cpp"), "-o", out, "-L", os.path.join(torch, "lib"),
+            os.path.join(CSRC, "seq_native.cpp"), os.path.join(CSRC, "lm_native.cpp"), "-o", out, "-L", os.path.join(torch, "lib"),
             "-ltorch_python", "-ltorch_hip", "-ltorch_cpu", "-lc10", "-lc10_hip"]
 
 
@@ -122,7 +123,7 @@ def build(verbose: bool = False) -> str:
     if not command:
         print("no PyTorch: _seq_native.so (the block operators' Python binding) is left out", file=sys.stderr)
     elif not bound:
-        raise RuntimeError(f"the compiler failed on seq_native.cpp:\n{bound_said}")
+        raise RuntimeError(f"the compiler failed on seq_native.cpp or lm_native.cpp:\n{bound_said}")
     elif verbose and bound_said.strip():
         print(bound_said)
     return LIB

@@ -18,10 +18,13 @@ TTT_F32, TTT_BF16 = 0, 1
  TTT_OP_BIDIR_BWD) = range(8)
 TTT_NOALLOC_SCRATCH_BYTES = 32 << 20  # static scratch of ttt_forward_fullbatch_noalloc, per device
 
-# Every symbol include/ttt.h and include/ttt_seq.h declare, with its ctypes signature.
+# Every symbol include/ttt.h, include/ttt_seq.h and include/ttt_lm.h declare, with its ctypes signature.
 _c_int, _c_float, _c_ll, _vp, _sz = ctypes.c_int, ctypes.c_float, ctypes.c_longlong, ctypes.c_void_p, ctypes.c_size_t
+_c_double = ctypes.c_double
 # the scan's inputs in order: u, delta, A, Bm, Cm, D, delta_bias, z, the strided ones each with their stride
 _SCAN_INPUTS = [_vp, _c_ll, _vp, _c_ll, _vp, _vp, _c_ll, _vp, _c_ll, _vp, _vp, _vp, _c_ll]
+# the recurrence's: x, r, i, each with its stride, lam
+_GATED_INPUTS = [_vp, _c_ll, _vp, _c_ll, _vp, _c_ll, _vp]
 SIGNATURES = {
     "ttt_forward_fullbatch": (_c_int, [_c_int, _c_int, _c_int, _c_int, _c_int, _c_float, _vp, _vp, _vp, _vp, _c_ll,
                                        _vp, _vp, _vp, _sz, _vp]),
@@ -60,6 +63,19 @@ SIGNATURES = {
     "ttt_step_selective_scan": (_c_int, [_c_int] * 6 + _SCAN_INPUTS + [_vp] * 4),
     "ttt_backward_selective_scan": (_c_int, [_c_int] * 7 + _SCAN_INPUTS + [_vp] * 13 + [_sz, _vp]),
     "ttt_backward_selective_scan_workspace": (_sz, [_c_int] * 6),
+    # include/ttt_lm.h
+    "ttt_forward_rmsnorm": (_c_int, [_c_int] * 4 + [_c_float, _vp, _c_ll, _vp, _c_double] + [_vp] * 5),
+    "ttt_forward_rmsnorm_e4m3": (_c_int, [_c_int] * 5 + [_c_float, _vp, _c_ll] + [_vp] * 6),
+    "ttt_backward_rmsnorm": (_c_int, [_c_int] * 4 + [_c_float, _vp, _c_ll, _vp, _vp, _vp, _c_double] + [_vp] * 5 + [_sz, _vp]),
+    "ttt_backward_rmsnorm_workspace": (_sz, [_c_int] * 4),
+    "ttt_forward_dropout": (_c_int, [_c_int] * 3 + [_c_double, _vp, _vp, _c_ll, _vp, _vp, _vp]),
+    "ttt_backward_dropout": (_c_int, [_c_int] * 3 + [_c_double] + [_vp] * 4),
+    "ttt_dropout_counters": (_c_ll, [_c_int] * 2),
+    "ttt_forward_gated_recurrence": (_c_int, [_c_int] * 4 + [_c_float] + _GATED_INPUTS + [_vp] * 6 + [_sz, _vp]),
+    "ttt_forward_gated_recurrence_workspace": (_sz, [_c_int] * 4),
+    "ttt_step_gated_recurrence": (_c_int, [_c_int] * 3 + [_c_float] + _GATED_INPUTS + [_vp] * 4),
+    "ttt_backward_gated_recurrence": (_c_int, [_c_int] * 4 + [_c_float] + _GATED_INPUTS + [_vp] * 10 + [_sz, _vp]),
+    "ttt_backward_gated_recurrence_workspace": (_sz, [_c_int] * 5),
 }
 
 _lib = None
