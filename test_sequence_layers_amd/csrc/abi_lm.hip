@@ -23,7 +23,8 @@ ttt_status check_rmsnorm_sizes(ttt_dtype dt, int M, int H, int D) {
 
 ttt_status check_recurrence_sizes(ttt_dtype dt, int B, int N, int C) {
   if (!known(dt) || B <= 0 || N <= 0 || C <= 0) return TTT_ERR_INVALID;
-  if (B > kMaxB || N > (1 << 22) || C > (1 << 20) || (double)B * N * C > (double)(1ll << 40)) return TTT_ERR_UNSUPPORTED;
+  if (B > kMaxB || N > (1 << 22) || C > (1 << 20) || (double)B * (N + 128.) * (C + 64.) > (double)(1ll << 38))
+    return TTT_ERR_UNSUPPORTED;
   return TTT_OK;
 }
 
