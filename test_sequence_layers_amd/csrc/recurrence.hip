@@ -7,6 +7,7 @@
 // with the root of la.
 //
 // A thread walks a channel of a sequence from end to end.
+#include <algorithm>
 #include <type_traits>
 
 #include "internal.hpp"
@@ -19,27 +20,56 @@ namespace {
 constexpr int kThreads = 64;
 constexpr int kKept = 64;  // tokens between kept states
 
-// 1 - exp(u) for u <= 0: by -u times a polynomial for u > -1/2 (within 1.1 * 2^-24 of it, found by Chebyshev's nodes), where the
-// difference would lose bits; e is exp(u).
-__device__ __forceinline__ float one_minus(float u, float e) {
+// (exp(u) - 1) / u for -1/2 <= u <= 0, within 1.1 * 2^-24 of it (a polynomial through Chebyshev's nodes), and 1 - exp(u) for
+// u <= 0: by that where the difference would lose bits; e is exp(u).
+__device__ __forceinline__ float expm1_part(float u) {
   float p = 0.0011237150756642222f;
   p = fmaf(p, u, 0.008190003223717213f);
   p = fmaf(p, u, 0.04163024201989174f);
   p = fmaf(p, u, 0.16666245460510254f);
   p = fmaf(p, u, 0.4999998211860657f);
-  p = fmaf(p, u, 1.f);
-  return u > -0.5f ? -u * p : 1.f - e;
+  return fmaf(p, u, 1.f);
+}
+__device__ __forceinline__ float one_minus(float u, float e) { return u > -0.5f ? -u * expm1_part(u) : 1.f - e; }
+__device__ __forceinline__ float root(float v) { return __builtin_amdgcn_sqrtf(v); }
+
+// log(1 + exp(v)): exp(-|v|) from its base-2 exponent in two parts (as one it would lose 2 |v| 2^-24 of itself), log1p(e) = s P(s^2)
+// with s = e / (2 + e), P within 4e-9 over e in (0, 1].
+__device__ __forceinline__ float softplus(float v) {
+  const float w = fmaxf(-fabsf(v), -200.f), hi = w * kLog2e;
+  const float lo = fmaf(w, kLog2e, -hi) + w * 1.925962991e-8f;  // (log2(e) less kLog2e)
+  const float e = exp2_hw(hi) * fmaf(lo, 0.69314718f, 1.f);
+  const float s = e / (2.f + e), q = s * s;
+  float p = 0.2817465662956238f;
+  p = fmaf(p, q, 0.2796141803264618f);
+  p = fmaf(p, q, 0.40024852752685547f);
+  p = fmaf(p, q, 0.6666631698608398f);
+  p = fmaf(p, q, 2.f);
+  return v == v ? fmaf(s, p, fmaxf(v, 0.f)) : v;
 }
 
-__device__ __forceinline__ float softplus(float v) { return v > 20.f ? v : log1pf(expf(v)); }
+// The decay's largest exponent: k = scale softplus(lam). Where it is at most kSmall for a whole wave, as ordinary decays are (0.78 a
+// token and slower), E = a - 1 is la times a polynomial (within 3e-9), a = 1 + E and 1 - a^2 = -E (2 + E), without an
+// exponential or a choice.
+constexpr float kSmall = 0.25f;
 
 struct Gates {
   float gr, gi, la, a, w;  // sigmoid(r), sigmoid(i), log a, a, 1 - a^2
-  __device__ __forceinline__ Gates(float r, float i, float k) {
+  __device__ __forceinline__ Gates(float r, float i, float k, bool small = false) {
     gr = sigmoid(r), gi = sigmoid(i);
     la = -k * gr;
-    a = exp2_hw(kLog2e * la);
-    w = one_minus(2.f * la, a * a);
+    if (small) {
+      float p = 0.007514301221817732f;
+      p = fmaf(p, la, 0.04149100184440613f);
+      p = fmaf(p, la, 0.16665112972259521f);
+      p = fmaf(p, la, 0.4999995231628418f);
+      const float E = la * fmaf(p, la, 1.f);
+      a = 1.f + E;
+      w = -E * (2.f + E);
+    } else {
+      a = exp2_hw(kLog2e * la);
+      w = one_minus(2.f * la, a * a);
+    }
   }
 };
 
@@ -47,20 +77,42 @@ __device__ __forceinline__ int length_of(const int* lengths, int b, int N) {
   return lengths ? min(max(lengths[b], 0), N) : N;
 }
 
+// A lane's part of a row that is the same for the whole wave: the row's address stays in SGPRs, the lane's offset in one 32-bit
+// register. (The empty asm keeps the two apart: added up they would be a 64-bit address per lane and row.)
+__device__ __forceinline__ uint32_t lane_part(int c, int size) {
+  uint32_t off = (uint32_t)c * (uint32_t)size;
+  asm volatile("" : "+v"(off));
+  return off;
+}
+
 // V neighbouring channels of one token as they are loaded (V = 2: 4 or 8 bytes), and stores of them.
 template <class T, int V>
 struct Pair {
   typedef typename std::conditional<sizeof(T) * V == 8, uint2, typename std::conditional<sizeof(T) * V == 4, uint32_t, uint16_t>::type>::type Bits;
   Bits b;
-  __device__ __forceinline__ void load(const T* p) { b = *reinterpret_cast<const Bits*>(p); }
+  __device__ __forceinline__ void load(const T* row, uint32_t off) {
+    b = *reinterpret_cast<const Bits*>(reinterpret_cast<const char*>(row) + off);
+  }
+  // To be looked at anew.
+  __device__ __forceinline__ void hide() {
+    if constexpr (sizeof(Bits) == 8) asm volatile("" : "+v"(b.x), "+v"(b.y));
+    else asm volatile("" : "+v"(b));
+  }
+  // Not to be looked at before v is there.
+  __device__ __forceinline__ void behind(float& v) {
+    if constexpr (sizeof(Bits) == 8) asm volatile("" : "+v"(b.x), "+v"(b.y), "+v"(v));
+    else asm volatile("" : "+v"(b), "+v"(v));
+  }
   __device__ __forceinline__ float get(int i) const {
     if constexpr (sizeof(Bits) == 8) return __uint_as_float(i ? b.y : b.x);
     else if constexpr (sizeof(T) == 4) return __uint_as_float(b);
     else return __uint_as_float(i ? (uint32_t)b & 0xffff0000u : (uint32_t)b << 16);
   }
-  static __device__ __forceinline__ void store(T* p, const float* v) {
+  static __device__ __forceinline__ void store(T* row, uint32_t off, const float* v) {
+    asm volatile("" : "+v"(off));  // (in the store's own block, or the compiler keeps the offset as 64 bits and adds the row to it)
+    char* p = reinterpret_cast<char*>(row) + off;
     if constexpr (V == 1) {
-      p[0] = (T)v[0];
+      *reinterpret_cast<T*>(p) = (T)v[0];
     } else if constexpr (sizeof(T) == 4) {
       *reinterpret_cast<float2*>(p) = make_float2(v[0], v[1]);
     } else {
@@ -75,7 +127,7 @@ struct Pair {
 // A tile of a column (64 V channels of a sequence) tells the later ones its (decay, end) pairs, and every kGroup-th its
 // end state: 64-bit words that are all ones until they are there, written and read whole by device-scope atomics, so that a word
 // says by itself that it has come. A NaN is told as the one NaN that is not all ones.
-constexpr int kGroup = 32;
+constexpr int kGroup = 16;
 constexpr unsigned long long kNotYet = ~0ull;
 constexpr int kMostPolls = 1 << 22;
 
@@ -92,154 +144,203 @@ struct Board {
   unsigned* ticket;
   unsigned long long *pairs, *states;
 };
-__global__ void clear_board(unsigned long long* p, long long words) {
+// Two boards, one behind the other; `second`: where that starts (and its ticket counter is), or the end.
+__global__ void clear_board(unsigned long long* p, long long second, long long words) {
   for (long long k = (long long)blockIdx.x * blockDim.x + threadIdx.x; k < words; k += (long long)gridDim.x * blockDim.x)
-    p[k] = k == 0 ? 0ull : kNotYet;
+    p[k] = k == 0 || k == second ? 0ull : kNotYet;
 }
 
-constexpr int kWaves = 8;  // of a workgroup
-template <class T>
-constexpr int kTokens = sizeof(T) == 2 ? 16 : 8;  // of a lane
+constexpr int kWaves = 16;  // of a workgroup
 
-template <class T, int V>
-__global__ __launch_bounds__(64 * kWaves) void recurrence_fwd(RecurrenceArgs a, int tiles, int columns, Board board) {
-  constexpr int TW = kTokens<T>, W = kWaves, TILE = TW * W, CH = 64 * V;
-  __shared__ float2 part[W][CH], back[kGroup][CH];
-  __shared__ float begin[CH];
-  __shared__ unsigned drawn;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, C = a.C, N = a.N;
-  // Tickets are drawn in the order in which workgroups start, and a tile waits for tiles of smaller tickets alone: they have
-  // started and wait for still smaller ones, so that every wait ends.
-  unsigned id = (unsigned)wide_block();
-  if (tiles > 1) {
-    if (threadIdx.x == 0) drawn = atomicAdd(board.ticket, 1u);
-    __syncthreads();
-    id = __builtin_amdgcn_readfirstlane(drawn);
+// Tile `tile` of column `column` of sequence b. Ids go through the columns first.
+struct Tile {
+  int tile, b, column;
+  __device__ __forceinline__ Tile(unsigned id, int columns, int B) {
+    tile = (int)(id / (unsigned)(columns * B));
+    const int rest = (int)(id - (unsigned)tile * (unsigned)(columns * B));
+    b = rest / columns, column = rest - b * columns;
   }
-  if (id >= (unsigned)(tiles * columns) * a.B) return;
-  const int tile = id / (unsigned)(columns * a.B), rest = id - tile * (columns * a.B);
-  const int b = rest / columns, column = rest - b * columns;
-  const int c0 = column * CH + lane * V, c = min(c0, C - V);  // (past the last channel: the last ones again)
+};
+
+// A workgroup's tile. Tickets are drawn in the order in which workgroups start, and a tile waits for tiles of smaller tickets alone: they
+// have started and wait for still smaller ones, so that every wait ends.
+__device__ __forceinline__ unsigned draw(const Board& board, int tiles) {
+  if (tiles == 1) return (unsigned)wide_block();
+  __shared__ unsigned drawn;
+  if (threadIdx.x == 0) drawn = atomicAdd(board.ticket, 1u);
+  __syncthreads();
+  return __builtin_amdgcn_readfirstlane(drawn);
+}
+
+// K times V neighbouring words, `step` apart, the first `count` of them asked for until they have come: all at once, and again only
+// those that had not.
+template <int K, int V>
+__device__ __forceinline__ void ask_all(unsigned long long (&v)[K][V], const unsigned long long* p, long long step, int count) {
+#pragma unroll
+  for (int q = 0; q < K; ++q)
+    for (int i = 0; i < V; ++i) v[q][i] = q < count ? kNotYet : 0;
+  for (int polls = 0; polls < kMostPolls; ++polls) {
+    bool there = true;
+#pragma unroll
+    for (int q = 0; q < K; ++q)
+      for (int i = 0; i < V; ++i)
+        if (v[q][i] == kNotYet) v[q][i] = ask(p + q * step + i);
+#pragma unroll
+    for (int q = 0; q < K; ++q)
+      for (int i = 0; i < V; ++i) there = there && v[q][i] != kNotYet;
+    if (__all(there)) return;
+    __builtin_amdgcn_s_sleep(1);
+  }
+}
+__device__ __forceinline__ float2 pair_of(unsigned long long w) {
+  return make_float2(__uint_as_float((uint32_t)w), __uint_as_float((uint32_t)(w >> 32)));
+}
+
+// What the waves of a workgroup share.
+template <int CH>
+struct Desk {
+  float2 part[kWaves][CH], back[kGroup][CH];
+  float begin[CH];
+};
+
+// A wave's run of TW tokens of a tile, from t0 on; n: the sequence's tokens.
+enum class Run {
+  kPadding,  // all of them behind the sequence's end
+  kPlain,    // none behind it, and decays slow enough for the polynomial
+  kAny,
+};
+// (Each kind is a whole path to the kernel's end: where they joined, the results of one would be held through the other, 64 registers of 128.
+// The barriers are met by whole waves, as often in each.)
+template <class T, int V, int TW, Run RUN>
+__device__ __forceinline__ void forward_run(const RecurrenceArgs& a, const Tile& k, int tiles, int columns, const Board& board, int wave,
+                                            int lane, int n, Desk<64 * V>& desk, const float (&kk)[V]) {
+  constexpr int W = kWaves, TILE = TW * W, CH = 64 * V;
+  const int C = a.C, N = a.N, wide = columns * CH, rows = (N + kKept - 1) / kKept;
+  const int c0 = k.column * CH + lane * V, c = min(c0, C - V);
   const bool mine = c0 < C;
-  const int n = length_of(a.lengths, b, N), t0 = tile * TILE + wave * TW;
-  const long long row0 = (long long)b * N;
-  T* y = (T*)a.y;
-  float A[V], e[V];
-  float av[TW][V], bv[TW][V];
-  if (t0 < n) {
+  const int t0 = k.tile * TILE + wave * TW;
+  const long long row = (long long)k.b * N + t0;
+  const uint32_t off = lane_part(c, sizeof(T));
+  float A[V], e[V], av[TW][V], bv[TW][V];
+  for (int i = 0; i < V; ++i) A[i] = 1.f, e[i] = 0.f;
+  if constexpr (RUN != Run::kPadding) {
     Pair<T, V> x[TW], r[TW], g[TW];
+    const T *px = (const T*)a.x + row * a.xs, *pr = (const T*)a.r + row * a.rs, *pi = (const T*)a.i + row * a.is;
 #pragma unroll
     for (int t = 0; t < TW; ++t) {
-      const long long at = row0 + min(t0 + t, N - 1);
-      x[t].load((const T*)a.x + at * a.xs + c);
-      r[t].load((const T*)a.r + at * a.rs + c);
-      g[t].load((const T*)a.i + at * a.is + c);
+      x[t].load(px, off), r[t].load(pr, off), g[t].load(pi, off);
+      if (RUN == Run::kPlain || t0 + t + 1 < N) px += a.xs, pr += a.rs, pi += a.is;  // (past the last token: the last again)
     }
-    float k[V];
-    for (int i = 0; i < V; ++i) k[i] = a.scale * softplus(a.lam[c + i]), A[i] = 1.f, e[i] = 0.f;
 #pragma unroll
     for (int t = 0; t < TW; ++t)
       for (int i = 0; i < V; ++i) {
-        const Gates q(r[t].get(i), g[t].get(i), k[i]);
-        const bool live = t0 + t < n;
+        const Gates q(r[t].get(i), g[t].get(i), kk[i], RUN == Run::kPlain);
+        const bool live = RUN == Run::kPlain || t0 + t < n;
         av[t][i] = live ? q.a : 1.f;
-        bv[t][i] = live ? sqrtf(q.w) * q.gi * x[t].get(i) : 0.f;
+        bv[t][i] = live ? root(q.w) * q.gi * x[t].get(i) : 0.f;
         A[i] *= av[t][i];
         e[i] = fmaf(av[t][i], e[i], bv[t][i]);
       }
-  } else {
-    for (int i = 0; i < V; ++i) A[i] = 1.f, e[i] = 0.f;
   }
-  const bool dead = tile * TILE >= n && tile > 0;  // nothing but padding
-  if (!dead) {
-    for (int i = 0; i < V; ++i) part[wave][lane * V + i] = make_float2(A[i], e[i]);
-    __syncthreads();
-    // The pair of the waves before this one; of the whole tile in the last.
-    float pa[V], pe[V];
-    for (int i = 0; i < V; ++i) pa[i] = 1.f, pe[i] = 0.f;
-    for (int w = 0; w < wave; ++w)
-      for (int i = 0; i < V; ++i) {
-        const float2 p = part[w][lane * V + i];
-        pa[i] *= p.x, pe[i] = fmaf(p.x, pe[i], p.y);
-      }
-    float ta[V], te[V];
-    const long long word0 = ((long long)b * tiles) * (columns * CH) + column * CH + lane * V;
-    if (wave == W - 1) {
-      for (int i = 0; i < V; ++i) ta[i] = pa[i] * A[i], te[i] = fmaf(A[i], pe[i], e[i]);
-      if (tile < tiles - 1)
-        for (int i = 0; i < V; ++i) tell(board.pairs + word0 + (long long)tile * (columns * CH) + i, ta[i], te[i]);
+  for (int i = 0; i < V; ++i) desk.part[wave][lane * V + i] = make_float2(A[i], e[i]);
+  __syncthreads();
+  float pa[V], pe[V];  // the pair of the waves before this one; with the last's own, the tile's
+  for (int i = 0; i < V; ++i) pa[i] = 1.f, pe[i] = 0.f;
+  for (int w = 0; w < wave; ++w)
+    for (int i = 0; i < V; ++i) {
+      const float2 p = desk.part[w][lane * V + i];
+      pa[i] *= p.x, pe[i] = fmaf(p.x, pe[i], p.y);
     }
-    const int first = tile / kGroup * kGroup, count = tile - first;
-    for (int j = wave; j < count; j += W) {
-      const unsigned long long* p = board.pairs + word0 + (long long)(first + j) * (columns * CH);
-      unsigned long long v[V];
-      for (int polls = 0; polls < kMostPolls; ++polls) {
-        bool there = true;
-        for (int i = 0; i < V; ++i) v[i] = ask(p + i), there = there && v[i] != kNotYet;
-        if (__all(there)) break;
-        __builtin_amdgcn_s_sleep(1);
-      }
-      for (int i = 0; i < V; ++i)
-        back[j][lane * V + i] = make_float2(__uint_as_float((uint32_t)v[i]), __uint_as_float((uint32_t)(v[i] >> 32)));
+  const int group = k.tile / kGroup, count = k.tile - group * kGroup;  // tiles of its group before this one
+  if (count > 0 || wave == W - 1) {
+    float ta[V], te[V], h[V];
+    for (int i = 0; i < V; ++i) ta[i] = pa[i] * A[i], te[i] = fmaf(A[i], pe[i], e[i]);
+    unsigned long long* pairs = board.pairs + ((long long)k.b * tiles + group * kGroup) * wide + k.column * CH + lane * V;
+    unsigned long long* states =
+        board.states + ((long long)k.b * ((tiles + kGroup - 1) / kGroup) + group) * wide + k.column * CH + lane * V;
+    if (wave == W - 1 && k.tile < tiles - 1)
+      for (int i = 0; i < V; ++i) tell(pairs + (long long)count * wide + i, ta[i], te[i]);
+    // A wave asks for the pairs of an equal run of the group's tiles, and the last wave, whose run ends with the group, for the state
+    // before it.
+    constexpr int EACH = kGroup / W;
+    static_assert(kGroup % W == 0, "");
+    const int from = wave * EACH;
+    if (from < count) {
+      unsigned long long v[EACH][V];
+      ask_all(v, pairs + (long long)from * wide, wide, count - from);
+#pragma unroll
+      for (int q = 0; q < EACH; ++q)
+        for (int i = 0; i < V; ++i) desk.back[from + q][lane * V + i] = pair_of(v[q][i]);
+    }
+    if (wave == W - 1) {
+      unsigned long long v[1][V];
+      if (group > 0) ask_all(v, states - wide, wide, 1);
+      for (int i = 0; i < V; ++i) h[i] = group > 0 ? pair_of(v[0][i]).x : a.h0 ? a.h0[(long long)k.b * C + c + i] : 0.f;
     }
     if (count > 0) __syncthreads();
     if (wave == W - 1) {
-      float h[V];
-      const long long group0 = ((long long)b * ((tiles + kGroup - 1) / kGroup)) * (columns * CH) + column * CH + lane * V;
-      if (first > 0) {
-        const unsigned long long* p = board.states + group0 + (long long)(first / kGroup - 1) * (columns * CH);
-        unsigned long long v[V];
-        for (int polls = 0; polls < kMostPolls; ++polls) {
-          bool there = true;
-          for (int i = 0; i < V; ++i) v[i] = ask(p + i), there = there && v[i] != kNotYet;
-          if (__all(there)) break;
-          __builtin_amdgcn_s_sleep(1);
-        }
-        for (int i = 0; i < V; ++i) h[i] = __uint_as_float((uint32_t)v[i]);
-      } else {
-        for (int i = 0; i < V; ++i) h[i] = a.h0 ? a.h0[(long long)b * C + c + i] : 0.f;
-      }
       for (int j = 0; j < count; ++j)
         for (int i = 0; i < V; ++i) {
-          const float2 p = back[j][lane * V + i];
+          const float2 p = desk.back[j][lane * V + i];
           h[i] = fmaf(p.x, h[i], p.y);
         }
       for (int i = 0; i < V; ++i) {
-        begin[lane * V + i] = h[i];
-        const float end = fmaf(ta[i], h[i], te[i]);
-        if (tile % kGroup == kGroup - 1 && tile < tiles - 1)
-          tell(board.states + group0 + (long long)(tile / kGroup) * (columns * CH) + i, end, 0.f);
-        if (a.h_out && mine && (tile + 1) * TILE >= n) a.h_out[(long long)b * C + c + i] = end;
+        desk.begin[lane * V + i] = h[i];
+        h[i] = fmaf(ta[i], h[i], te[i]);
+        if (count == kGroup - 1 && k.tile < tiles - 1) tell(states + i, h[i], 0.f);
       }
+      if (mine && (k.tile + 1) * TILE >= n)
+        for (int i = 0; i < V; ++i) {
+          if (a.h_out) a.h_out[(long long)k.b * C + c + i] = h[i];
+          if (a.states)  // before padding's tokens in later tiles: the last
+            for (int j = ((k.tile + 1) * TILE + kKept - 1) / kKept; j < rows; ++j)
+              a.states[((long long)k.b * rows + j) * C + c + i] = h[i];
+        }
     }
-    __syncthreads();
-    float h[V];
-    for (int i = 0; i < V; ++i) h[i] = fmaf(pa[i], begin[lane * V + i], pe[i]);
-    const int rows = (N + kKept - 1) / kKept;
-    float* states = a.states ? a.states + (long long)b * rows * C + c : nullptr;
-    if (states && mine && t0 % kKept == 0 && t0 < N)
-      for (int i = 0; i < V; ++i) states[(long long)(t0 / kKept) * C + i] = h[i];
-    if (t0 < n) {
-#pragma unroll
-      for (int t = 0; t < TW; ++t) {
-        float o[V];
-        for (int i = 0; i < V; ++i) h[i] = fmaf(av[t][i], h[i], bv[t][i]), o[i] = t0 + t < n ? h[i] : 0.f;
-        if (y && mine && t0 + t < N) Pair<T, V>::store(y + (row0 + t0 + t) * C + c, o);
-      }
-    } else if (y) {
-      const float o[V] = {};
-      for (int t = 0; t < TW; ++t)
-        if (mine && t0 + t < N) Pair<T, V>::store(y + (row0 + t0 + t) * C + c, o);
-    }
-    // The states before padding's tokens in later tiles are the last.
-    if (states && wave == W - 1 && mine && (tile + 1) * TILE >= n)
-      for (int j = (tile + 1) * TILE / kKept; j < rows; ++j)
-        for (int i = 0; i < V; ++i) states[(long long)j * C + i] = h[i];
-  } else if (y) {
-    const float o[V] = {};
-    for (int t = 0; t < TW; ++t)
-      if (mine && t0 + t < N) Pair<T, V>::store(y + (row0 + t0 + t) * C + c, o);
   }
+  __syncthreads();
+  if (!mine || t0 >= N) return;
+  float h[V];
+  for (int i = 0; i < V; ++i) h[i] = fmaf(pa[i], desk.begin[lane * V + i], pe[i]);
+  if (a.states && t0 % kKept == 0)
+    for (int i = 0; i < V; ++i) a.states[((long long)k.b * rows + t0 / kKept) * C + c + i] = h[i];
+  if (!a.y) return;
+  T* py = (T*)a.y + row * C;
+#pragma unroll
+  for (int t = 0; t < TW; ++t) {
+    float o[V];
+    for (int i = 0; i < V; ++i) {
+      if (RUN != Run::kPadding) h[i] = fmaf(av[t][i], h[i], bv[t][i]);
+      o[i] = RUN == Run::kPlain || (RUN == Run::kAny && t0 + t < n) ? h[i] : 0.f;
+    }
+    if (RUN == Run::kPlain || t0 + t < N) Pair<T, V>::store(py, off, o);
+    py += C;
+  }
+}
+
+template <class T, int V, int TW>
+__global__ __launch_bounds__(64 * kWaves) void recurrence_fwd(RecurrenceArgs a, int tiles, int columns, unsigned total, Board board) {
+  constexpr int TILE = TW * kWaves, CH = 64 * V;
+  __shared__ Desk<CH> desk;
+  const unsigned id = draw(board, tiles);
+  if (id >= total) return;
+  const Tile k(id, columns, a.B);
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+  const int c0 = k.column * CH + lane * V, c = min(c0, a.C - V);  // (past the last channel: the last ones again)
+  const int n = length_of(a.lengths, k.b, a.N), t0 = k.tile * TILE + wave * TW;
+  if (k.tile * TILE >= n && k.tile > 0) {  // nothing but padding
+    const float o[V] = {};
+    if (a.y && c0 < a.C)
+      for (int t = t0; t < min(t0 + TW, a.N); ++t)
+        Pair<T, V>::store((T*)a.y + ((long long)k.b * a.N + t) * a.C, lane_part(c, sizeof(T)), o);
+    return;
+  }
+  float kk[V];
+  bool small = true;
+  for (int i = 0; i < V; ++i) kk[i] = a.scale * softplus(a.lam[c + i]), small = small && kk[i] <= kSmall;
+  if (t0 >= n) forward_run<T, V, TW, Run::kPadding>(a, k, tiles, columns, board, wave, lane, n, desk, kk);
+  else if (t0 + TW <= n && __all(small)) forward_run<T, V, TW, Run::kPlain>(a, k, tiles, columns, board, wave, lane, n, desk, kk);
+  else forward_run<T, V, TW, Run::kAny>(a, k, tiles, columns, board, wave, lane, n, desk, kk);
 }
 
 template <class T>
@@ -248,46 +349,210 @@ __global__ __launch_bounds__(kThreads) void recurrence_step(RecurrenceArgs a) {
   if (c >= C) return;
   const Gates g((float)((const T*)a.r)[b * a.rs + c], (float)((const T*)a.i)[b * a.is + c], a.scale * softplus(a.lam[c]));
   const long long at = (long long)b * C + c;
-  const float h = fmaf(g.a, a.h0[at], sqrtf(g.w) * g.gi * (float)((const T*)a.x)[b * a.xs + c]);
+  const float h = fmaf(g.a, a.h0[at], root(g.w) * g.gi * (float)((const T*)a.x)[b * a.xs + c]);
   ((T*)a.y)[at] = (T)h;
   a.h_out[at] = h;
 }
 
-template <class T>
-__global__ __launch_bounds__(kThreads) void recurrence_bwd(RecurrenceArgs a, float* before, float* part) {
-  const int c = blockIdx.x * kThreads + threadIdx.x, b = blockIdx.y, C = a.C;
-  if (c >= C) return;
-  const int n = length_of(a.lengths, b, a.N);
-  const float k = a.scale * softplus(a.lam[c]);
-  float h = a.h0 ? a.h0[(long long)b * C + c] : 0.f;
-  for (int t = 0; t < n; ++t) {
-    const long long at = (long long)b * a.N + t;
-    before[at * C + c] = h;
-    const Gates g((float)((const T*)a.r)[at * a.rs + c], (float)((const T*)a.i)[at * a.is + c], k);
-    h = fmaf(g.a, h, sqrtf(g.w) * g.gi * (float)((const T*)a.x)[at * a.xs + c]);
-  }
-  float z = 0.f, sum = 0.f;  // a_{n+1} q_{n+1}; the sum of t
-  for (int t = a.N - 1; t >= 0; --t) {
-    const long long at = (long long)b * a.N + t;
-    float dx = 0.f, dr = 0.f, di = 0.f;
-    if (t < n) {
-      const float x = (float)((const T*)a.x)[at * a.xs + c];
-      const Gates g((float)((const T*)a.r)[at * a.rs + c], (float)((const T*)a.i)[at * a.is + c], k);
-      const float q = (float)((const T*)a.dy)[at * C + c] + z, m = sqrtf(g.w);
-      const float per = g.w == 0.f ? 0.f : g.la / m;
-      const float l = q * (g.a * g.la * before[at * C + c] - g.a * g.a * per * g.gi * x);
-      dx = q * m * g.gi;
-      di = dx * x * (1.f - g.gi);
-      dr = l * (1.f - g.gr);
-      sum += l;
-      z = g.a * q;
+// ---- backward ----------------------------------------------------------------------------------
+template <int CH>
+struct DeskBack {
+  float2 part[kWaves][CH], back[kGroup][CH];
+  float z[kWaves][CH];  // what flows out of a wave's front where nothing flows in at its end; later, its sum of t
+  float begin[CH];
+};
+
+template <class T, int V, int TW, Run RUN>
+__device__ __forceinline__ void backward_run(const RecurrenceArgs& a, const Tile& k, int tiles, int columns, const Board& board,
+                                             float* sums, int wave, int lane, int n, DeskBack<64 * V>& desk, const float (&kk)[V],
+                                             Pair<T, V> (&x)[TW], Pair<T, V> (&r)[TW], Pair<T, V> (&g)[TW],
+                                             Pair<T, V> (&dy)[TW]) {
+  constexpr int W = kWaves, TILE = TW * W, CH = 64 * V;
+  const int C = a.C, N = a.N, wide = columns * CH;
+  const int c0 = k.column * CH + lane * V, c = min(c0, C - V);
+  const bool mine = c0 < C;
+  const int t0 = k.tile * TILE + wave * TW;
+  const uint32_t off = lane_part(c, sizeof(T));
+  const long long end = ((long long)k.b * N + t0 + TW - 1) * C;  // the run's last token
+  T *ox = (T*)a.dx + end, *orr = (T*)a.dr + end, *oi = (T*)a.di + end;
+  // Of a token: a; m sigmoid(i); x (1 - sigmoid(i)); t / q, at first its second part; sigmoid(r).
+  float av[TW][V], cx[TW][V], ci[TW][V], ct[TW][V], gr[TW][V];
+  float A[V], e[V], z[V];
+  for (int i = 0; i < V; ++i) A[i] = 1.f, e[i] = z[i] = 0.f;
+  if constexpr (RUN != Run::kPadding) {
+#pragma unroll
+    for (int t = 0; t < TW; ++t) {
+      for (int i = 0; i < V; ++i) {
+        const Gates q(r[t].get(i), g[t].get(i), kk[i], RUN == Run::kPlain);
+        const float inv = q.w < 0x1p-126f ? 0.f : __builtin_amdgcn_rsqf(q.w), xv = x[t].get(i);  // 1 / m; (m = 0 below the root's range)
+        const bool live = RUN == Run::kPlain || t0 + t < n;
+        av[t][i] = live ? q.a : 1.f;
+        cx[t][i] = live ? q.w * inv * q.gi : 0.f;
+        ci[t][i] = xv * (1.f - q.gi);
+        ct[t][i] = q.a * q.a * (q.la * inv) * (q.gi * xv);
+        gr[t][i] = q.gr;
+        A[i] *= av[t][i];
+        e[i] = fmaf(av[t][i], e[i], live ? cx[t][i] * xv : 0.f);
+      }
+      // (Two tokens at a time: all at once would take more registers than there are.)
+      if (t + 2 < TW)
+        for (int i = 0; i < V; ++i) r[t + 2].behind(e[i]), r[t + 2].behind(ct[t][i]), r[t + 2].behind(ci[t][i]);
     }
-    ((T*)a.dx)[at * C + c] = (T)dx;
-    ((T*)a.dr)[at * C + c] = (T)dr;
-    ((T*)a.di)[at * C + c] = (T)di;
+#pragma unroll
+    for (int t = TW - 1; t >= 0; --t)
+      for (int i = 0; i < V; ++i) z[i] = av[t][i] * ((RUN == Run::kPlain || t0 + t < n ? dy[t].get(i) : 0.f) + z[i]);
+    // (x and dy stay as they were loaded.)
+#pragma unroll
+    for (int t = 0; t < TW; ++t) x[t].hide(), dy[t].hide();
   }
-  part[(long long)b * C + c] = sum;
-  if (a.dh0) a.dh0[(long long)b * C + c] = z;
+  for (int i = 0; i < V; ++i) desk.part[wave][lane * V + i] = make_float2(A[i], e[i]), desk.z[wave][lane * V + i] = z[i];
+  const int rows = (N + kKept - 1) / kKept;
+  float h[V];
+  for (int i = 0; i < V; ++i) h[i] = t0 < N ? a.kept[((long long)k.b * rows + k.tile * TILE / kKept) * C + c + i] : 0.f;
+  __syncthreads();
+  // The tile's pair, told by the last wave as soon as it is there; the state before this wave's tokens, the pair of the waves behind it.
+  const int group = k.tile / kGroup, last = (n - 1) / TILE;  // the sequence's last tile
+  const int count = n > 0 ? min(group * kGroup + kGroup - 1, last) - k.tile : 0;  // tiles of its group behind this one
+  const bool further = (group + 1) * kGroup <= last && n > 0;
+  unsigned long long* pairs = board.pairs + ((long long)k.b * tiles + k.tile) * wide + k.column * CH + lane * V;
+  unsigned long long* states =
+      board.states + ((long long)k.b * ((tiles + kGroup - 1) / kGroup) + group) * wide + k.column * CH + lane * V;
+  float ta[V], tz[V];
+  if (wave == W - 1) {
+    for (int i = 0; i < V; ++i) ta[i] = 1.f, tz[i] = 0.f;
+    for (int w = W - 1; w >= 0; --w)
+      for (int i = 0; i < V; ++i) {
+        const float p = desk.part[w][lane * V + i].x;
+        ta[i] *= p, tz[i] = fmaf(p, tz[i], desk.z[w][lane * V + i]);
+      }
+    if (k.tile % kGroup != 0)
+      for (int i = 0; i < V; ++i) tell(pairs + i, ta[i], tz[i]);
+  }
+  float pa[V], pz[V];
+  for (int i = 0; i < V; ++i) pa[i] = 1.f, pz[i] = 0.f;
+  if constexpr (RUN != Run::kPadding) {
+    for (int w = 0; w < wave; ++w)
+      for (int i = 0; i < V; ++i) {
+        const float2 p = desk.part[w][lane * V + i];
+        h[i] = fmaf(p.x, h[i], p.y);
+      }
+    for (int w = W - 1; w > wave; --w)
+      for (int i = 0; i < V; ++i) {
+        const float p = desk.part[w][lane * V + i].x;
+        pa[i] *= p, pz[i] = fmaf(p, pz[i], desk.z[w][lane * V + i]);
+      }
+#pragma unroll
+    for (int t = 0; t < TW; ++t)
+      for (int i = 0; i < V; ++i) {
+        ct[t][i] = av[t][i] * (-kk[i] * gr[t][i]) * h[i] - ct[t][i];
+        h[i] = fmaf(av[t][i], h[i], RUN == Run::kPlain || t0 + t < n ? cx[t][i] * x[t].get(i) : 0.f);
+      }
+  }
+  constexpr int EACH = kGroup / W;
+  static_assert(kGroup % W == 0, "");
+  const int from = wave * EACH;
+  if (from < count) {
+    unsigned long long v[EACH][V];
+    ask_all(v, pairs + (long long)(from + 1) * wide, wide, count - from);
+#pragma unroll
+    for (int q = 0; q < EACH; ++q)
+      for (int i = 0; i < V; ++i) desk.back[from + q][lane * V + i] = pair_of(v[q][i]);
+  }
+  float f[V];
+  if (wave == W - 1) {
+    unsigned long long v[1][V];
+    if (further) ask_all(v, states + wide, wide, 1);
+    for (int i = 0; i < V; ++i) f[i] = further ? pair_of(v[0][i]).x : 0.f;
+  }
+  if (count > 0) __syncthreads();
+  if (wave == W - 1) {
+    for (int j = count - 1; j >= 0; --j)
+      for (int i = 0; i < V; ++i) {
+        const float2 p = desk.back[j][lane * V + i];
+        f[i] = fmaf(p.x, f[i], p.y);
+      }
+    for (int i = 0; i < V; ++i) {
+      desk.begin[lane * V + i] = f[i];
+      f[i] = fmaf(ta[i], f[i], tz[i]);
+      if (k.tile % kGroup == 0 && k.tile > 0) tell(states + i, f[i], 0.f);
+      if (k.tile == 0 && a.dh0 && mine) a.dh0[(long long)k.b * C + c + i] = f[i];
+    }
+  }
+  __syncthreads();
+  float sum[V] = {};
+  if (mine && t0 < N) {
+    for (int i = 0; i < V; ++i) z[i] = fmaf(pa[i], desk.begin[lane * V + i], pz[i]);
+#pragma unroll
+    for (int t = TW - 1; t >= 0; --t) {
+      float dx[V] = {}, dr[V] = {}, di[V] = {};
+      if (RUN == Run::kPlain || (RUN == Run::kAny && t0 + t < n)) {
+        for (int i = 0; i < V; ++i) {
+          const float q = dy[t].get(i) + z[i], l = q * ct[t][i];
+          dx[i] = q * cx[t][i];
+          di[i] = dx[i] * ci[t][i];
+          dr[i] = l * (1.f - gr[t][i]);
+          sum[i] += l;
+          z[i] = av[t][i] * q;
+        }
+      }
+      if (RUN == Run::kPlain || t0 + t < N) Pair<T, V>::store(ox, off, dx), Pair<T, V>::store(orr, off, dr), Pair<T, V>::store(oi, off, di);
+      ox -= C, orr -= C, oi -= C;
+    }
+  }
+  // (The z that flow out of the fronts have been read before the last barrier.)
+  for (int i = 0; i < V; ++i) desk.z[wave][lane * V + i] = sum[i];
+  __syncthreads();
+  if (wave == 0 && mine)
+    for (int i = 0; i < V; ++i) {
+      float s = 0.f;
+      for (int w = 0; w < W; ++w) s += desk.z[w][lane * V + i];
+      sums[((long long)k.b * tiles + k.tile) * C + c + i] = s;
+    }
+}
+
+// Tiles from the sequences' ends on.
+template <class T, int V, int TW>
+__global__ __launch_bounds__(64 * kWaves) void recurrence_bwd(RecurrenceArgs a, int tiles, int columns, unsigned total, Board board,
+                                                              float* sums) {
+  constexpr int TILE = TW * kWaves, CH = 64 * V;
+  __shared__ DeskBack<CH> desk;
+  const unsigned id = draw(board, tiles);
+  if (id >= total) return;
+  Tile k(id, columns, a.B);
+  k.tile = tiles - 1 - k.tile;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+  const int c0 = k.column * CH + lane * V, c = min(c0, a.C - V);  // (past the last channel: the last ones again)
+  const int n = length_of(a.lengths, k.b, a.N), t0 = k.tile * TILE + wave * TW;
+  const uint32_t off = lane_part(c, sizeof(T));
+  if (k.tile * TILE >= n && k.tile > 0) {  // nothing but padding
+    const float o[V] = {};
+    if (c0 >= a.C) return;
+    for (int t = t0; t < min(t0 + TW, a.N); ++t) {
+      const long long at = ((long long)k.b * a.N + t) * a.C;
+      Pair<T, V>::store((T*)a.dx + at, off, o), Pair<T, V>::store((T*)a.dr + at, off, o), Pair<T, V>::store((T*)a.di + at, off, o);
+    }
+    if (wave == 0)
+      for (int i = 0; i < V; ++i) sums[((long long)k.b * tiles + k.tile) * a.C + c + i] = 0.f;
+    return;
+  }
+  Pair<T, V> x[TW], r[TW], g[TW], dy[TW];
+  float kk[V];
+  if (t0 >= n)
+    return backward_run<T, V, TW, Run::kPadding>(a, k, tiles, columns, board, sums, wave, lane, n, desk, kk, x, r, g, dy);
+  const long long row = (long long)k.b * a.N + t0;
+  const T *px = (const T*)a.x + row * a.xs, *pr = (const T*)a.r + row * a.rs, *pi = (const T*)a.i + row * a.is;
+  const T* pd = (const T*)a.dy + row * a.C;
+#pragma unroll
+  for (int t = 0; t < TW; ++t) {
+    x[t].load(px, off), r[t].load(pr, off), g[t].load(pi, off), dy[t].load(pd, off);
+    if (t0 + t + 1 < a.N) px += a.xs, pr += a.rs, pi += a.is, pd += a.C;  // (past the last token: the last again)
+  }
+  bool small = true;
+  for (int i = 0; i < V; ++i) kk[i] = a.scale * softplus(a.lam[c + i]), small = small && kk[i] <= kSmall;
+  if (t0 + TW <= n && __all(small))
+    backward_run<T, V, TW, Run::kPlain>(a, k, tiles, columns, board, sums, wave, lane, n, desk, kk, x, r, g, dy);
+  else
+    backward_run<T, V, TW, Run::kAny>(a, k, tiles, columns, board, sums, wave, lane, n, desk, kk, x, r, g, dy);
 }
 
 // sigmoid(lam) / softplus(lam), 1 - exp(lam) / 2 and so on far below zero.
@@ -302,41 +567,31 @@ struct StoreDecayGrad {
 
 dim3 grid_of(const RecurrenceArgs& a) { return dim3((unsigned)((a.C + kThreads - 1) / kThreads), (unsigned)a.B); }
 
-// How a call is cut up: V channels a lane, tiles of a sequence, columns.
+// How a pass is cut up: V channels a lane and TW tokens, tiles of a sequence, columns; the board's words, a ticket's row of 16
+// first, none where a sequence is one tile.
 struct Plan {
-  int V, tiles, columns;
+  int V, TW, tiles, columns;
+  long long words;
 };
 template <class T>
-Plan plan_of(int N, int C, bool pairs) {
-  const int V = pairs ? 2 : 1, tile = kTokens<T> * kWaves;
-  return {V, (N + tile - 1) / tile, (C + 64 * V - 1) / (64 * V)};
-}
-// Words of the board: the ticket's (16), then pairs and states.
-long long board_words(const Plan& p, int B) {
-  if (p.tiles == 1) return 0;
-  const long long row = (long long)p.columns * 64 * p.V;
-  return 16 + (long long)B * row * (p.tiles + (p.tiles + kGroup - 1) / kGroup);
-}
-template <class T>
-size_t board_bytes(int B, int N, int C) {
-  const long long one = board_words(plan_of<T>(N, C, false), B), two = board_words(plan_of<T>(N, C, true), B);
-  return (size_t)(one > two ? one : two) * 8;
+Plan plan_of(int B, int N, int C, bool pairs, bool backward) {
+  Plan p;
+  p.V = pairs ? 2 : 1;
+  p.TW = (backward ? 8 : 16) / (sizeof(T) == 2 ? 1 : 2);
+  p.tiles = (N + p.TW * kWaves - 1) / (p.TW * kWaves), p.columns = (C + 64 * p.V - 1) / (64 * p.V);
+  const long long row = (long long)B * p.columns * 64 * p.V;
+  p.words = p.tiles == 1 ? 0 : 16 + row * (p.tiles + (p.tiles + kGroup - 1) / kGroup);
+  return p;
 }
 
-template <class T, int V>
-hipError_t launch_fwd(const RecurrenceArgs& a, void* ws, hipStream_t st) {
-  const Plan p = plan_of<T>(a.N, a.C, V == 2);
-  const long long words = board_words(p, a.B), row = (long long)p.columns * 64 * V;
-  unsigned long long* w = static_cast<unsigned long long*>(ws);
-  const Board board{reinterpret_cast<unsigned*>(w), w + 16, w + 16 + a.B * row * p.tiles};
-  if (p.tiles > 1) {
-    const long long blocks = (words + 1023) / 1024;
-    hipLaunchKernelGGL(clear_board, dim3((unsigned)(blocks < 1024 ? blocks : 1024)), dim3(256), 0, st, w, words);
-    const hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return e;
-  }
-  hipLaunchKernelGGL((recurrence_fwd<T, V>), wide_grid((long long)p.tiles * p.columns * a.B), dim3(64 * kWaves), 0, st, a,
-                     p.tiles, p.columns, board);
+Board board_of(const Plan& p, int B, unsigned long long* w) {
+  return Board{reinterpret_cast<unsigned*>(w), w + 16, w + 16 + (long long)B * p.columns * 64 * p.V * p.tiles};
+}
+
+hipError_t clear(unsigned long long* w, long long one, long long two, hipStream_t st) {
+  if (one + two == 0) return hipSuccess;
+  const long long blocks = (one + two + 1023) / 1024;
+  hipLaunchKernelGGL(clear_board, dim3((unsigned)(blocks < 1024 ? blocks : 1024)), dim3(256), 0, st, w, one, one + two);
   return hipGetLastError();
 }
 
@@ -349,15 +604,87 @@ bool paired(const RecurrenceArgs& a) {
   return ((a.C | a.xs | a.rs | a.is) & 1) == 0 && at % (2 * sizeof(T)) == 0;
 }
 
+template <class T, int V, int TW>
+hipError_t forward(const RecurrenceArgs& a, const Plan& p, unsigned long long* w, hipStream_t st) {
+  const unsigned total = (unsigned)p.tiles * p.columns * a.B;
+  hipLaunchKernelGGL((recurrence_fwd<T, V, TW>), wide_grid(total), dim3(64 * kWaves), 0, st, a, p.tiles, p.columns, total,
+                     board_of(p, a.B, w));
+  return hipGetLastError();
+}
+template <class T, int V, int TW>
+hipError_t backward(const RecurrenceArgs& a, const Plan& p, unsigned long long* w, float* sums, hipStream_t st) {
+  const unsigned total = (unsigned)p.tiles * p.columns * a.B;
+  hipLaunchKernelGGL((recurrence_bwd<T, V, TW>), wide_grid(total), dim3(64 * kWaves), 0, st, a, p.tiles, p.columns, total,
+                     board_of(p, a.B, w), sums);
+  return hipGetLastError();
+}
+
+template <class T>
+hipError_t run_forward(const RecurrenceArgs& a, const Plan& p, unsigned long long* w, hipStream_t st) {
+  constexpr int TW = sizeof(T) == 2 ? 16 : 8;
+  return p.V == 2 ? forward<T, 2, TW>(a, p, w, st) : forward<T, 1, TW>(a, p, w, st);
+}
+template <class T>
+hipError_t run_backward(const RecurrenceArgs& a, const Plan& p, unsigned long long* w, float* sums, hipStream_t st) {
+  constexpr int TW = sizeof(T) == 2 ? 8 : 4;
+  return p.V == 2 ? backward<T, 2, TW>(a, p, w, sums, st) : backward<T, 1, TW>(a, p, w, sums, st);
+}
+
+template <class T>
+size_t forward_bytes(int B, int N, int C) {
+  return (size_t)std::max(plan_of<T>(B, N, C, false, false).words, plan_of<T>(B, N, C, true, false).words) * 8;
+}
+
+// The backward pass's workspace: the boards of both passes, the tiles' sums, the states.
+struct BackLayout {
+  size_t sums, states, bytes;
+};
+template <class T>
+BackLayout back_layout(int B, int N, int C, bool kept) {
+  const long long board = std::max(plan_of<T>(B, N, C, false, true).words, plan_of<T>(B, N, C, true, true).words);
+  BackLayout l;
+  l.sums = round_up((size_t)board * 8 + (kept ? 0 : forward_bytes<T>(B, N, C)), 256);
+  l.states = l.sums + round_up((size_t)B * plan_of<T>(B, N, C, true, true).tiles * C * 4, 256);
+  l.bytes = l.states + (kept ? 0 : (size_t)B * ((N + kKept - 1) / kKept) * C * 4);
+  return l;
+}
+
+template <class T>
+hipError_t forward_call(const RecurrenceArgs& a, void* ws, hipStream_t st) {
+  const Plan p = plan_of<T>(a.B, a.N, a.C, paired<T>(a), false);
+  unsigned long long* w = static_cast<unsigned long long*>(ws);
+  const hipError_t e = clear(w, p.words, 0, st);
+  return e == hipSuccess ? run_forward<T>(a, p, w, st) : e;
+}
+
+template <class T>
+hipError_t backward_call(RecurrenceArgs a, void* ws, hipStream_t st) {
+  const bool kept = a.kept != nullptr, pairs = paired<T>(a);
+  const BackLayout l = back_layout<T>(a.B, a.N, a.C, kept);
+  const Plan p = plan_of<T>(a.B, a.N, a.C, pairs, true), q = plan_of<T>(a.B, a.N, a.C, pairs, false);
+  unsigned long long* w = static_cast<unsigned long long*>(ws);
+  float* sums = reinterpret_cast<float*>(static_cast<char*>(ws) + l.sums);
+  hipError_t e = clear(w, p.words, kept ? 0 : q.words, st);
+  if (e != hipSuccess) return e;
+  if (!kept) {  // the forward pass again, for its states alone
+    a.states = reinterpret_cast<float*>(static_cast<char*>(ws) + l.states);
+    a.kept = a.states;
+    e = run_forward<T>(a, q, w + p.words, st);
+    if (e != hipSuccess) return e;
+  }
+  e = run_backward<T>(a, p, w, sums, st);
+  if (e != hipSuccess) return e;
+  return column_sum_launch(sums, (long long)a.B * p.tiles, a.C, StoreDecayGrad{a.lam, a.dlam}, st);
+}
+
 }  // namespace
 
 size_t recurrence_workspace_bytes(bool bf16_io, int B, int N, int C) {
-  return bf16_io ? board_bytes<bf16>(B, N, C) : board_bytes<float>(B, N, C);
+  return bf16_io ? forward_bytes<bf16>(B, N, C) : forward_bytes<float>(B, N, C);
 }
 
 hipError_t recurrence_launch(bool bf16_io, const RecurrenceArgs& a, void* ws, hipStream_t st) {
-  if (bf16_io) return paired<bf16>(a) ? launch_fwd<bf16, 2>(a, ws, st) : launch_fwd<bf16, 1>(a, ws, st);
-  return paired<float>(a) ? launch_fwd<float, 2>(a, ws, st) : launch_fwd<float, 1>(a, ws, st);
+  return bf16_io ? forward_call<bf16>(a, ws, st) : forward_call<float>(a, ws, st);
 }
 
 hipError_t recurrence_step_launch(bool bf16_io, const RecurrenceArgs& a, hipStream_t st) {
@@ -366,16 +693,12 @@ hipError_t recurrence_step_launch(bool bf16_io, const RecurrenceArgs& a, hipStre
   return hipGetLastError();
 }
 
-size_t recurrence_bwd_workspace_bytes(bool, int B, int N, int C, bool) { return ((size_t)B * N * C + (size_t)B * C) * 4; }
+size_t recurrence_bwd_workspace_bytes(bool bf16_io, int B, int N, int C, bool kept) {
+  return bf16_io ? back_layout<bf16>(B, N, C, kept).bytes : back_layout<float>(B, N, C, kept).bytes;
+}
 
 hipError_t recurrence_bwd_launch(bool bf16_io, const RecurrenceArgs& a, void* ws, hipStream_t st) {
-  float* before = static_cast<float*>(ws);
-  float* part = before + (size_t)a.B * a.N * a.C;
-  if (bf16_io) hipLaunchKernelGGL(recurrence_bwd<bf16>, grid_of(a), dim3(kThreads), 0, st, a, before, part);
-  else hipLaunchKernelGGL(recurrence_bwd<float>, grid_of(a), dim3(kThreads), 0, st, a, before, part);
-  const hipError_t e = hipGetLastError();
-  if (e != hipSuccess) return e;
-  return column_sum_launch(part, a.B, a.C, StoreDecayGrad{a.lam, a.dlam}, st);
+  return bf16_io ? backward_call<bf16>(a, ws, st) : backward_call<float>(a, ws, st);
 }
 
 }  // namespace ttt

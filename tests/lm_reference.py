@@ -7,6 +7,8 @@ import torch
 
 from seq_reference import U, _d, _live, _sig
 
+ROOT = 2.0 ** -63
+
 
 # ----------------------------------------------------------------------------------- RMS norm
 def _sum(x, residual, factor):
@@ -80,7 +82,8 @@ def recurrence(x, r, i, lam, d_y=None, scale=8.0, h0=None, lengths=None, depth=0
     before each token.
 
     Tokens may be taken in runs from zero states, joined by products of decays: a product's rounding is u a token beside
-    the decay's own, and each entry goes through four more roundings of its size.
+    the decay's own, and each entry goes through four more roundings of its size. The hardware's root takes 1 - a^2 below
+    2^-126 as zero: m is off by up to 2^-63 there, and log(a) / m, about -m / 2, by half of that.
     """
     B, N, C = x.shape
     live = _live(lengths, B, N, x.device)[..., None]
@@ -96,7 +99,8 @@ def recurrence(x, r, i, lam, d_y=None, scale=8.0, h0=None, lengths=None, depth=0
     r_w = torch.where(2 * la > -0.5, r_la + 5 * U, 0.0) + torch.where(2 * la < -0.49, (2 * r_a + U) * a * a / w + U, 0.0)
     m, r_m = torch.sqrt(w), r_w / 2 + 2 * U
     b = torch.where(live, m * gi * x, 0.0)
-    off_b = b.abs() * (r_m + r_gi + 3 * U)
+    flush = torch.where(live, ROOT * gi * x.abs(), 0.0)
+    off_b = b.abs() * (r_m + r_gi + 3 * U) + flush
     a, r_a = torch.where(live, a, 1.0), torch.where(live, r_a, 0.0)
     h, H, E = (torch.empty(B, N + 1, C, dtype=torch.float64, device=x.device) for _ in range(3))
     h[:, 0] = 0.0 if h0 is None else _d(h0)
@@ -119,13 +123,13 @@ def recurrence(x, r, i, lam, d_y=None, scale=8.0, h0=None, lengths=None, depth=0
     F = F + 4 * U * Q
     before, before_size, before_off = h[:, :-1], H[:, :-1], E[:, :-1]
     dx = q * m * gi
-    off_dx = F * m * gi + Q * m * gi * (r_m + r_gi + 2 * U)
+    off_dx = F * m * gi + Q * gi * (m * (r_m + r_gi + 2 * U) + ROOT)
     one_gi, off_one_gi = 1 - gi, r_gi * gi + U
     xa = x.abs()
     out = {"d_x": (dx, off_dx), "d_i": (dx * x * one_gi, xa * (off_dx * one_gi + Q * m * gi * (off_one_gi + 2 * U * one_gi)))}
     one, two = a * la * before, a * a * (la / m) * gi * x
     size = a * la.abs() * before_size + two.abs()
-    off_in = a * la.abs() * (before_off + before_size * (r_a + r_la + 3 * U)) + two.abs() * (2 * r_a + r_la + r_m + r_gi + 8 * U)
+    off_in = a * la.abs() * (before_off + before_size * (r_a + r_la + 3 * U)) + two.abs() * (2 * r_a + r_la + r_m + r_gi + 8 * U) + flush
     t_, off_t = q * (one - two), Q * (off_in + 3 * U * size) + F * size
     t_, off_t = torch.where(live, t_, 0.0), torch.where(live, off_t, 0.0)
     size_t = torch.where(live, Q * size, 0.0)
