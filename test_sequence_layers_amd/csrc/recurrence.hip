@@ -48,17 +48,20 @@ __device__ __forceinline__ float softplus(float v) {
   return v == v ? fmaf(s, p, fmaxf(v, 0.f)) : v;
 }
 
-// The decay's largest exponent: k = scale softplus(lam). Where it is at most kSmall for a whole wave, as ordinary decays are (0.78 a
+// k = scale softplus(lam) is the decay's largest exponent. Where it is at most kSmall for a whole wave, as ordinary decays are (0.78 a
 // token and slower), E = a - 1 is la times a polynomial (within 3e-9), a = 1 + E and 1 - a^2 = -E (2 + E), without an
-// exponential or a choice.
+// exponential or a choice; `wide` says that it is not.
 constexpr float kSmall = 0.25f;
 
 struct Gates {
   float gr, gi, la, a, w;  // sigmoid(r), sigmoid(i), log a, a, 1 - a^2
-  __device__ __forceinline__ Gates(float r, float i, float k, bool small = false) {
+  __device__ __forceinline__ Gates(float r, float i, float k, bool wide) {
     gr = sigmoid(r), gi = sigmoid(i);
     la = -k * gr;
-    if (small) {
+    if (wide) {
+      a = exp2_hw(kLog2e * la);
+      w = one_minus(2.f * la, a * a);
+    } else {
       float p = 0.007514301221817732f;
       p = fmaf(p, la, 0.04149100184440613f);
       p = fmaf(p, la, 0.16665112972259521f);
@@ -66,12 +69,11 @@ struct Gates {
       const float E = la * fmaf(p, la, 1.f);
       a = 1.f + E;
       w = -E * (2.f + E);
-    } else {
-      a = exp2_hw(kLog2e * la);
-      w = one_minus(2.f * la, a * a);
     }
   }
 };
+// A condition that is the same for the whole wave, as the compiler cannot tell.
+__device__ __forceinline__ bool uniform(bool v) { return __builtin_amdgcn_readfirstlane(v ? 1 : 0) != 0; }
 
 __device__ __forceinline__ int length_of(const int* lengths, int b, int N) {
   return lengths ? min(max(lengths[b], 0), N) : N;
@@ -97,11 +99,6 @@ struct Pair {
   __device__ __forceinline__ void hide() {
     if constexpr (sizeof(Bits) == 8) asm volatile("" : "+v"(b.x), "+v"(b.y));
     else asm volatile("" : "+v"(b));
-  }
-  // Not to be looked at before v is there.
-  __device__ __forceinline__ void behind(float& v) {
-    if constexpr (sizeof(Bits) == 8) asm volatile("" : "+v"(b.x), "+v"(b.y), "+v"(v));
-    else asm volatile("" : "+v"(b), "+v"(v));
   }
   __device__ __forceinline__ float get(int i) const {
     if constexpr (sizeof(Bits) == 8) return __uint_as_float(i ? b.y : b.x);
@@ -150,8 +147,6 @@ __global__ void clear_board(unsigned long long* p, long long second, long long w
     p[k] = k == 0 || k == second ? 0ull : kNotYet;
 }
 
-constexpr int kWaves = 16;  // of a workgroup
-
 // Tile `tile` of column `column` of sequence b. Ids go through the columns first.
 struct Tile {
   int tile, b, column;
@@ -197,51 +192,66 @@ __device__ __forceinline__ float2 pair_of(unsigned long long w) {
 }
 
 // What the waves of a workgroup share.
-template <int CH>
+template <int W, int CH>
 struct Desk {
-  float2 part[kWaves][CH], back[kGroup][CH];
+  float2 part[W][CH], back[kGroup][CH];
   float begin[CH];
 };
 
-// A wave's run of TW tokens of a tile, from t0 on; n: the sequence's tokens.
-enum class Run {
-  kPadding,  // all of them behind the sequence's end
-  kPlain,    // none behind it, and decays slow enough for the polynomial
-  kAny,
-};
-// (Each kind is a whole path to the kernel's end: where they joined, the results of one would be held through the other, 64 registers of 128.
-// The barriers are met by whole waves, as often in each.)
-template <class T, int V, int TW, Run RUN>
-__device__ __forceinline__ void forward_run(const RecurrenceArgs& a, const Tile& k, int tiles, int columns, const Board& board, int wave,
-                                            int lane, int n, Desk<64 * V>& desk, const float (&kk)[V]) {
-  constexpr int W = kWaves, TILE = TW * W, CH = 64 * V;
-  const int C = a.C, N = a.N, wide = columns * CH, rows = (N + kKept - 1) / kKept;
-  const int c0 = k.column * CH + lane * V, c = min(c0, C - V);
+template <class T, int W, int V, int TW>
+__global__ __launch_bounds__(64 * W) void recurrence_fwd(RecurrenceArgs a, int tiles, int columns, unsigned total, Board board) {
+  constexpr int TILE = TW * W, CH = 64 * V;
+  __shared__ Desk<W, CH> desk;
+  const unsigned id = draw(board, tiles);
+  if (id >= total) return;
+  const Tile k(id, columns, a.B);
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, C = a.C, N = a.N;
+  const int wide = columns * CH, rows = (N + kKept - 1) / kKept;
+  const int c0 = k.column * CH + lane * V, c = min(c0, C - V);  // (past the last channel: the last ones again)
   const bool mine = c0 < C;
-  const int t0 = k.tile * TILE + wave * TW;
+  const int n = length_of(a.lengths, k.b, N), t0 = k.tile * TILE + wave * TW;
+  const int live = n - t0, inside = N - t0;  // tokens of this run and those behind it, of the sequence and of the padded one
   const long long row = (long long)k.b * N + t0;
   const uint32_t off = lane_part(c, sizeof(T));
+  T* py = a.y ? (T*)a.y + row * C : nullptr;
+  if (k.tile * TILE >= n && k.tile > 0) {  // nothing but padding
+    const float o[V] = {};
+    if (py && mine)
+      for (int t = 0; t < min(TW, inside); ++t) Pair<T, V>::store(py, off, o), py += C;
+    return;
+  }
+  Pair<T, V> x[TW], r[TW], g[TW];
+  const int from = min(t0, N - 1);  // (past the last token: the last again)
+  const T *px = (const T*)a.x + ((long long)k.b * N + from) * a.xs, *pr = (const T*)a.r + ((long long)k.b * N + from) * a.rs;
+  const T* pi = (const T*)a.i + ((long long)k.b * N + from) * a.is;
+#pragma unroll
+  for (int t = 0; t < TW; ++t) {
+    x[t].load(px, off), r[t].load(pr, off), g[t].load(pi, off);
+    if (t + 1 < inside) px += a.xs, pr += a.rs, pi += a.is;
+  }
+  float kk[V];
+  bool far = false;
+  for (int i = 0; i < V; ++i) kk[i] = a.scale * softplus(a.lam[c + i]), far = far || kk[i] > kSmall;
+  // (Of a run without padding and steep decays the tokens are one straight piece of code.)
+  const bool steep = uniform(__any(far)), plain = uniform(live >= TW && !steep);
   float A[V], e[V], av[TW][V], bv[TW][V];
   for (int i = 0; i < V; ++i) A[i] = 1.f, e[i] = 0.f;
-  if constexpr (RUN != Run::kPadding) {
-    Pair<T, V> x[TW], r[TW], g[TW];
-    const T *px = (const T*)a.x + row * a.xs, *pr = (const T*)a.r + row * a.rs, *pi = (const T*)a.i + row * a.is;
+  auto all = [&](auto plain) {
 #pragma unroll
     for (int t = 0; t < TW; ++t) {
-      x[t].load(px, off), r[t].load(pr, off), g[t].load(pi, off);
-      if (RUN == Run::kPlain || t0 + t + 1 < N) px += a.xs, pr += a.rs, pi += a.is;  // (past the last token: the last again)
+      for (int i = 0; i < V; ++i) av[t][i] = 1.f, bv[t][i] = 0.f;
+      if (plain.value || t < live)
+        for (int i = 0; i < V; ++i) {
+          const Gates q(r[t].get(i), g[t].get(i), kk[i], !plain.value && steep);
+          av[t][i] = q.a;
+          bv[t][i] = root(q.w) * q.gi * x[t].get(i);
+          A[i] *= av[t][i];
+          e[i] = fmaf(av[t][i], e[i], bv[t][i]);
+        }
     }
-#pragma unroll
-    for (int t = 0; t < TW; ++t)
-      for (int i = 0; i < V; ++i) {
-        const Gates q(r[t].get(i), g[t].get(i), kk[i], RUN == Run::kPlain);
-        const bool live = RUN == Run::kPlain || t0 + t < n;
-        av[t][i] = live ? q.a : 1.f;
-        bv[t][i] = live ? root(q.w) * q.gi * x[t].get(i) : 0.f;
-        A[i] *= av[t][i];
-        e[i] = fmaf(av[t][i], e[i], bv[t][i]);
-      }
-  }
+  };
+  if (plain) all(std::true_type{});
+  else all(std::false_type{});
   for (int i = 0; i < V; ++i) desk.part[wave][lane * V + i] = make_float2(A[i], e[i]);
   __syncthreads();
   float pa[V], pe[V];  // the pair of the waves before this one; with the last's own, the tile's
@@ -264,13 +274,13 @@ __device__ __forceinline__ void forward_run(const RecurrenceArgs& a, const Tile&
     // before it.
     constexpr int EACH = kGroup / W;
     static_assert(kGroup % W == 0, "");
-    const int from = wave * EACH;
-    if (from < count) {
+    const int first = wave * EACH;
+    if (first < count) {
       unsigned long long v[EACH][V];
-      ask_all(v, pairs + (long long)from * wide, wide, count - from);
+      ask_all(v, pairs + (long long)first * wide, wide, count - first);
 #pragma unroll
       for (int q = 0; q < EACH; ++q)
-        for (int i = 0; i < V; ++i) desk.back[from + q][lane * V + i] = pair_of(v[q][i]);
+        for (int i = 0; i < V; ++i) desk.back[first + q][lane * V + i] = pair_of(v[q][i]);
     }
     if (wave == W - 1) {
       unsigned long long v[1][V];
@@ -299,55 +309,30 @@ __device__ __forceinline__ void forward_run(const RecurrenceArgs& a, const Tile&
     }
   }
   __syncthreads();
-  if (!mine || t0 >= N) return;
+  if (!mine || inside <= 0) return;
   float h[V];
   for (int i = 0; i < V; ++i) h[i] = fmaf(pa[i], desk.begin[lane * V + i], pe[i]);
   if (a.states && t0 % kKept == 0)
     for (int i = 0; i < V; ++i) a.states[((long long)k.b * rows + t0 / kKept) * C + c + i] = h[i];
-  if (!a.y) return;
-  T* py = (T*)a.y + row * C;
+  if (!py) return;
+  auto put = [&](auto plain) {
 #pragma unroll
-  for (int t = 0; t < TW; ++t) {
-    float o[V];
-    for (int i = 0; i < V; ++i) {
-      if (RUN != Run::kPadding) h[i] = fmaf(av[t][i], h[i], bv[t][i]);
-      o[i] = RUN == Run::kPlain || (RUN == Run::kAny && t0 + t < n) ? h[i] : 0.f;
+    for (int t = 0; t < TW; ++t) {
+      float o[V];
+      for (int i = 0; i < V; ++i) h[i] = fmaf(av[t][i], h[i], bv[t][i]), o[i] = plain.value || t < live ? h[i] : 0.f;
+      if (plain.value || t < inside) Pair<T, V>::store(py, off, o);
+      py += C;
     }
-    if (RUN == Run::kPlain || t0 + t < N) Pair<T, V>::store(py, off, o);
-    py += C;
-  }
-}
-
-template <class T, int V, int TW>
-__global__ __launch_bounds__(64 * kWaves) void recurrence_fwd(RecurrenceArgs a, int tiles, int columns, unsigned total, Board board) {
-  constexpr int TILE = TW * kWaves, CH = 64 * V;
-  __shared__ Desk<CH> desk;
-  const unsigned id = draw(board, tiles);
-  if (id >= total) return;
-  const Tile k(id, columns, a.B);
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
-  const int c0 = k.column * CH + lane * V, c = min(c0, a.C - V);  // (past the last channel: the last ones again)
-  const int n = length_of(a.lengths, k.b, a.N), t0 = k.tile * TILE + wave * TW;
-  if (k.tile * TILE >= n && k.tile > 0) {  // nothing but padding
-    const float o[V] = {};
-    if (a.y && c0 < a.C)
-      for (int t = t0; t < min(t0 + TW, a.N); ++t)
-        Pair<T, V>::store((T*)a.y + ((long long)k.b * a.N + t) * a.C, lane_part(c, sizeof(T)), o);
-    return;
-  }
-  float kk[V];
-  bool small = true;
-  for (int i = 0; i < V; ++i) kk[i] = a.scale * softplus(a.lam[c + i]), small = small && kk[i] <= kSmall;
-  if (t0 >= n) forward_run<T, V, TW, Run::kPadding>(a, k, tiles, columns, board, wave, lane, n, desk, kk);
-  else if (t0 + TW <= n && __all(small)) forward_run<T, V, TW, Run::kPlain>(a, k, tiles, columns, board, wave, lane, n, desk, kk);
-  else forward_run<T, V, TW, Run::kAny>(a, k, tiles, columns, board, wave, lane, n, desk, kk);
+  };
+  if (plain) put(std::true_type{});
+  else put(std::false_type{});
 }
 
 template <class T>
 __global__ __launch_bounds__(kThreads) void recurrence_step(RecurrenceArgs a) {
   const int c = blockIdx.x * kThreads + threadIdx.x, b = blockIdx.y, C = a.C;
   if (c >= C) return;
-  const Gates g((float)((const T*)a.r)[b * a.rs + c], (float)((const T*)a.i)[b * a.is + c], a.scale * softplus(a.lam[c]));
+  const Gates g((float)((const T*)a.r)[b * a.rs + c], (float)((const T*)a.i)[b * a.is + c], a.scale * softplus(a.lam[c]), true);
   const long long at = (long long)b * C + c;
   const float h = fmaf(g.a, a.h0[at], root(g.w) * g.gi * (float)((const T*)a.x)[b * a.xs + c]);
   ((T*)a.y)[at] = (T)h;
@@ -355,65 +340,93 @@ __global__ __launch_bounds__(kThreads) void recurrence_step(RecurrenceArgs a) {
 }
 
 // ---- backward ----------------------------------------------------------------------------------
-template <int CH>
+template <int W, int CH>
 struct DeskBack {
-  float2 part[kWaves][CH], back[kGroup][CH];
-  float z[kWaves][CH];  // what flows out of a wave's front where nothing flows in at its end; later, its sum of t
+  float2 part[W][CH], back[kGroup][CH];
+  float z[W][CH];  // what flows out of a wave's front where nothing flows in at its end; later, its sum of t
   float begin[CH];
 };
 
-template <class T, int V, int TW, Run RUN>
-__device__ __forceinline__ void backward_run(const RecurrenceArgs& a, const Tile& k, int tiles, int columns, const Board& board,
-                                             float* sums, int wave, int lane, int n, DeskBack<64 * V>& desk, const float (&kk)[V],
-                                             Pair<T, V> (&x)[TW], Pair<T, V> (&r)[TW], Pair<T, V> (&g)[TW],
-                                             Pair<T, V> (&dy)[TW]) {
-  constexpr int W = kWaves, TILE = TW * W, CH = 64 * V;
-  const int C = a.C, N = a.N, wide = columns * CH;
-  const int c0 = k.column * CH + lane * V, c = min(c0, C - V);
+// Tiles from the sequences' ends on.
+template <class T, int W, int V, int TW>
+__global__ __launch_bounds__(64 * W) void recurrence_bwd(RecurrenceArgs a, int tiles, int columns, unsigned total, Board board,
+                                                              float* sums) {
+  constexpr int TILE = TW * W, CH = 64 * V;
+  __shared__ DeskBack<W, CH> desk;
+  static_assert(TILE % kKept == 0, "a tile starts at a kept state");
+  const unsigned id = draw(board, tiles);
+  if (id >= total) return;
+  Tile k(id, columns, a.B);
+  k.tile = tiles - 1 - k.tile;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, C = a.C, N = a.N;
+  const int wide = columns * CH, rows = (N + kKept - 1) / kKept;
+  const int c0 = k.column * CH + lane * V, c = min(c0, C - V);  // (past the last channel: the last ones again)
   const bool mine = c0 < C;
-  const int t0 = k.tile * TILE + wave * TW;
+  const int n = length_of(a.lengths, k.b, N), t0 = k.tile * TILE + wave * TW;
+  const int live = n - t0, inside = N - t0;  // tokens of this run and those behind it, of the sequence and of the padded one
   const uint32_t off = lane_part(c, sizeof(T));
   const long long end = ((long long)k.b * N + t0 + TW - 1) * C;  // the run's last token
   T *ox = (T*)a.dx + end, *orr = (T*)a.dr + end, *oi = (T*)a.di + end;
+  if (k.tile * TILE >= n && k.tile > 0) {  // nothing but padding
+    const float o[V] = {};
+    if (!mine) return;
+    for (int t = TW - 1; t >= 0; --t) {
+      if (t < inside) Pair<T, V>::store(ox, off, o), Pair<T, V>::store(orr, off, o), Pair<T, V>::store(oi, off, o);
+      ox -= C, orr -= C, oi -= C;
+    }
+    if (wave == 0)
+      for (int i = 0; i < V; ++i) sums[((long long)k.b * tiles + k.tile) * C + c + i] = 0.f;
+    return;
+  }
+  Pair<T, V> x[TW], r[TW], g[TW], dy[TW];
+  const long long from = (long long)k.b * N + min(t0, N - 1);  // (past the last token: the last again)
+  const T *px = (const T*)a.x + from * a.xs, *pr = (const T*)a.r + from * a.rs, *pi = (const T*)a.i + from * a.is;
+  const T* pd = (const T*)a.dy + from * C;
+#pragma unroll
+  for (int t = 0; t < TW; ++t) {
+    x[t].load(px, off), r[t].load(pr, off), g[t].load(pi, off), dy[t].load(pd, off);
+    if (t + 1 < inside) px += a.xs, pr += a.rs, pi += a.is, pd += C;
+  }
+  float h[V], kk[V];
+  bool far = false;
+  for (int i = 0; i < V; ++i) {
+    kk[i] = a.scale * softplus(a.lam[c + i]), far = far || kk[i] > kSmall;
+    h[i] = a.kept[((long long)k.b * rows + k.tile * TILE / kKept) * C + c + i];
+  }
+  const bool steep = uniform(__any(far));
   // Of a token: a; m sigmoid(i); x (1 - sigmoid(i)); t / q, at first its second part; sigmoid(r).
   float av[TW][V], cx[TW][V], ci[TW][V], ct[TW][V], gr[TW][V];
   float A[V], e[V], z[V];
   for (int i = 0; i < V; ++i) A[i] = 1.f, e[i] = z[i] = 0.f;
-  if constexpr (RUN != Run::kPadding) {
 #pragma unroll
-    for (int t = 0; t < TW; ++t) {
+  for (int t = 0; t < TW; ++t) {
+    for (int i = 0; i < V; ++i) av[t][i] = 1.f, cx[t][i] = ci[t][i] = ct[t][i] = gr[t][i] = 0.f;
+    if (t < live)
       for (int i = 0; i < V; ++i) {
-        const Gates q(r[t].get(i), g[t].get(i), kk[i], RUN == Run::kPlain);
-        const float inv = q.w < 0x1p-126f ? 0.f : __builtin_amdgcn_rsqf(q.w), xv = x[t].get(i);  // 1 / m; (m = 0 below the root's range)
-        const bool live = RUN == Run::kPlain || t0 + t < n;
-        av[t][i] = live ? q.a : 1.f;
-        cx[t][i] = live ? q.w * inv * q.gi : 0.f;
+        const Gates q(r[t].get(i), g[t].get(i), kk[i], steep);
+        const float inv = q.w < 0x1p-126f ? 0.f : __builtin_amdgcn_rsqf(q.w);  // 1 / m; (m = 0 below the root's range)
+        const float xv = x[t].get(i);
+        av[t][i] = q.a;
+        cx[t][i] = q.w * inv * q.gi;
         ci[t][i] = xv * (1.f - q.gi);
         ct[t][i] = q.a * q.a * (q.la * inv) * (q.gi * xv);
         gr[t][i] = q.gr;
-        A[i] *= av[t][i];
-        e[i] = fmaf(av[t][i], e[i], live ? cx[t][i] * xv : 0.f);
+        A[i] *= q.a;
+        e[i] = fmaf(q.a, e[i], cx[t][i] * xv);
       }
-      // (Two tokens at a time: all at once would take more registers than there are.)
-      if (t + 2 < TW)
-        for (int i = 0; i < V; ++i) r[t + 2].behind(e[i]), r[t + 2].behind(ct[t][i]), r[t + 2].behind(ci[t][i]);
-    }
-#pragma unroll
-    for (int t = TW - 1; t >= 0; --t)
-      for (int i = 0; i < V; ++i) z[i] = av[t][i] * ((RUN == Run::kPlain || t0 + t < n ? dy[t].get(i) : 0.f) + z[i]);
-    // (x and dy stay as they were loaded.)
-#pragma unroll
-    for (int t = 0; t < TW; ++t) x[t].hide(), dy[t].hide();
   }
+#pragma unroll
+  for (int t = TW - 1; t >= 0; --t)
+    for (int i = 0; i < V; ++i) z[i] = av[t][i] * ((t < live ? dy[t].get(i) : 0.f) + z[i]);
+  // (x and dy stay as they were loaded.)
+#pragma unroll
+  for (int t = 0; t < TW; ++t) x[t].hide(), dy[t].hide();
   for (int i = 0; i < V; ++i) desk.part[wave][lane * V + i] = make_float2(A[i], e[i]), desk.z[wave][lane * V + i] = z[i];
-  const int rows = (N + kKept - 1) / kKept;
-  float h[V];
-  for (int i = 0; i < V; ++i) h[i] = t0 < N ? a.kept[((long long)k.b * rows + k.tile * TILE / kKept) * C + c + i] : 0.f;
   __syncthreads();
   // The tile's pair, told by the last wave as soon as it is there; the state before this wave's tokens, the pair of the waves behind it.
-  const int group = k.tile / kGroup, last = (n - 1) / TILE;  // the sequence's last tile
-  const int count = n > 0 ? min(group * kGroup + kGroup - 1, last) - k.tile : 0;  // tiles of its group behind this one
-  const bool further = (group + 1) * kGroup <= last && n > 0;
+  const int group = k.tile / kGroup, last = n > 0 ? (n - 1) / TILE : 0;  // the sequence's last tile
+  const int count = min(group * kGroup + kGroup - 1, last) - k.tile;     // tiles of its group behind this one
+  const bool further = (group + 1) * kGroup <= last;
   unsigned long long* pairs = board.pairs + ((long long)k.b * tiles + k.tile) * wide + k.column * CH + lane * V;
   unsigned long long* states =
       board.states + ((long long)k.b * ((tiles + kGroup - 1) / kGroup) + group) * wide + k.column * CH + lane * V;
@@ -430,33 +443,31 @@ __device__ __forceinline__ void backward_run(const RecurrenceArgs& a, const Tile
   }
   float pa[V], pz[V];
   for (int i = 0; i < V; ++i) pa[i] = 1.f, pz[i] = 0.f;
-  if constexpr (RUN != Run::kPadding) {
-    for (int w = 0; w < wave; ++w)
-      for (int i = 0; i < V; ++i) {
-        const float2 p = desk.part[w][lane * V + i];
-        h[i] = fmaf(p.x, h[i], p.y);
-      }
-    for (int w = W - 1; w > wave; --w)
-      for (int i = 0; i < V; ++i) {
-        const float p = desk.part[w][lane * V + i].x;
-        pa[i] *= p, pz[i] = fmaf(p, pz[i], desk.z[w][lane * V + i]);
-      }
+  for (int w = 0; w < wave; ++w)
+    for (int i = 0; i < V; ++i) {
+      const float2 p = desk.part[w][lane * V + i];
+      h[i] = fmaf(p.x, h[i], p.y);
+    }
+  for (int w = W - 1; w > wave; --w)
+    for (int i = 0; i < V; ++i) {
+      const float p = desk.part[w][lane * V + i].x;
+      pa[i] *= p, pz[i] = fmaf(p, pz[i], desk.z[w][lane * V + i]);
+    }
 #pragma unroll
-    for (int t = 0; t < TW; ++t)
-      for (int i = 0; i < V; ++i) {
-        ct[t][i] = av[t][i] * (-kk[i] * gr[t][i]) * h[i] - ct[t][i];
-        h[i] = fmaf(av[t][i], h[i], RUN == Run::kPlain || t0 + t < n ? cx[t][i] * x[t].get(i) : 0.f);
-      }
-  }
+  for (int t = 0; t < TW; ++t)
+    for (int i = 0; i < V; ++i) {
+      ct[t][i] = av[t][i] * (-kk[i] * gr[t][i]) * h[i] - ct[t][i];
+      h[i] = fmaf(av[t][i], h[i], t < live ? cx[t][i] * x[t].get(i) : 0.f);
+    }
   constexpr int EACH = kGroup / W;
   static_assert(kGroup % W == 0, "");
-  const int from = wave * EACH;
-  if (from < count) {
+  const int first = wave * EACH;
+  if (first < count) {
     unsigned long long v[EACH][V];
-    ask_all(v, pairs + (long long)(from + 1) * wide, wide, count - from);
+    ask_all(v, pairs + (long long)(first + 1) * wide, wide, count - first);
 #pragma unroll
     for (int q = 0; q < EACH; ++q)
-      for (int i = 0; i < V; ++i) desk.back[from + q][lane * V + i] = pair_of(v[q][i]);
+      for (int i = 0; i < V; ++i) desk.back[first + q][lane * V + i] = pair_of(v[q][i]);
   }
   float f[V];
   if (wave == W - 1) {
@@ -480,24 +491,27 @@ __device__ __forceinline__ void backward_run(const RecurrenceArgs& a, const Tile
   }
   __syncthreads();
   float sum[V] = {};
-  if (mine && t0 < N) {
-    for (int i = 0; i < V; ++i) z[i] = fmaf(pa[i], desk.begin[lane * V + i], pz[i]);
+  for (int i = 0; i < V; ++i) z[i] = fmaf(pa[i], desk.begin[lane * V + i], pz[i]);
+  if (mine) {
+    auto put = [&](auto plain) {
 #pragma unroll
-    for (int t = TW - 1; t >= 0; --t) {
-      float dx[V] = {}, dr[V] = {}, di[V] = {};
-      if (RUN == Run::kPlain || (RUN == Run::kAny && t0 + t < n)) {
-        for (int i = 0; i < V; ++i) {
-          const float q = dy[t].get(i) + z[i], l = q * ct[t][i];
-          dx[i] = q * cx[t][i];
-          di[i] = dx[i] * ci[t][i];
-          dr[i] = l * (1.f - gr[t][i]);
-          sum[i] += l;
-          z[i] = av[t][i] * q;
-        }
+      for (int t = TW - 1; t >= 0; --t) {
+        float dx[V] = {}, dr[V] = {}, di[V] = {};
+        if (plain.value || t < live)
+          for (int i = 0; i < V; ++i) {
+            const float q = dy[t].get(i) + z[i], l = q * ct[t][i];
+            dx[i] = q * cx[t][i];
+            di[i] = dx[i] * ci[t][i];
+            dr[i] = l * (1.f - gr[t][i]);
+            sum[i] += l;
+            z[i] = av[t][i] * q;
+          }
+        if (plain.value || t < inside) Pair<T, V>::store(ox, off, dx), Pair<T, V>::store(orr, off, dr), Pair<T, V>::store(oi, off, di);
+        ox -= C, orr -= C, oi -= C;
       }
-      if (RUN == Run::kPlain || t0 + t < N) Pair<T, V>::store(ox, off, dx), Pair<T, V>::store(orr, off, dr), Pair<T, V>::store(oi, off, di);
-      ox -= C, orr -= C, oi -= C;
-    }
+    };
+    if (uniform(live >= TW)) put(std::true_type{});
+    else put(std::false_type{});
   }
   // (The z that flow out of the fronts have been read before the last barrier.)
   for (int i = 0; i < V; ++i) desk.z[wave][lane * V + i] = sum[i];
@@ -508,51 +522,6 @@ __device__ __forceinline__ void backward_run(const RecurrenceArgs& a, const Tile
       for (int w = 0; w < W; ++w) s += desk.z[w][lane * V + i];
       sums[((long long)k.b * tiles + k.tile) * C + c + i] = s;
     }
-}
-
-// Tiles from the sequences' ends on.
-template <class T, int V, int TW>
-__global__ __launch_bounds__(64 * kWaves) void recurrence_bwd(RecurrenceArgs a, int tiles, int columns, unsigned total, Board board,
-                                                              float* sums) {
-  constexpr int TILE = TW * kWaves, CH = 64 * V;
-  __shared__ DeskBack<CH> desk;
-  const unsigned id = draw(board, tiles);
-  if (id >= total) return;
-  Tile k(id, columns, a.B);
-  k.tile = tiles - 1 - k.tile;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
-  const int c0 = k.column * CH + lane * V, c = min(c0, a.C - V);  // (past the last channel: the last ones again)
-  const int n = length_of(a.lengths, k.b, a.N), t0 = k.tile * TILE + wave * TW;
-  const uint32_t off = lane_part(c, sizeof(T));
-  if (k.tile * TILE >= n && k.tile > 0) {  // nothing but padding
-    const float o[V] = {};
-    if (c0 >= a.C) return;
-    for (int t = t0; t < min(t0 + TW, a.N); ++t) {
-      const long long at = ((long long)k.b * a.N + t) * a.C;
-      Pair<T, V>::store((T*)a.dx + at, off, o), Pair<T, V>::store((T*)a.dr + at, off, o), Pair<T, V>::store((T*)a.di + at, off, o);
-    }
-    if (wave == 0)
-      for (int i = 0; i < V; ++i) sums[((long long)k.b * tiles + k.tile) * a.C + c + i] = 0.f;
-    return;
-  }
-  Pair<T, V> x[TW], r[TW], g[TW], dy[TW];
-  float kk[V];
-  if (t0 >= n)
-    return backward_run<T, V, TW, Run::kPadding>(a, k, tiles, columns, board, sums, wave, lane, n, desk, kk, x, r, g, dy);
-  const long long row = (long long)k.b * a.N + t0;
-  const T *px = (const T*)a.x + row * a.xs, *pr = (const T*)a.r + row * a.rs, *pi = (const T*)a.i + row * a.is;
-  const T* pd = (const T*)a.dy + row * a.C;
-#pragma unroll
-  for (int t = 0; t < TW; ++t) {
-    x[t].load(px, off), r[t].load(pr, off), g[t].load(pi, off), dy[t].load(pd, off);
-    if (t0 + t + 1 < a.N) px += a.xs, pr += a.rs, pi += a.is, pd += a.C;  // (past the last token: the last again)
-  }
-  bool small = true;
-  for (int i = 0; i < V; ++i) kk[i] = a.scale * softplus(a.lam[c + i]), small = small && kk[i] <= kSmall;
-  if (t0 + TW <= n && __all(small))
-    backward_run<T, V, TW, Run::kPlain>(a, k, tiles, columns, board, sums, wave, lane, n, desk, kk, x, r, g, dy);
-  else
-    backward_run<T, V, TW, Run::kAny>(a, k, tiles, columns, board, sums, wave, lane, n, desk, kk, x, r, g, dy);
 }
 
 // sigmoid(lam) / softplus(lam), 1 - exp(lam) / 2 and so on far below zero.
@@ -567,21 +536,29 @@ struct StoreDecayGrad {
 
 dim3 grid_of(const RecurrenceArgs& a) { return dim3((unsigned)((a.C + kThreads - 1) / kThreads), (unsigned)a.B); }
 
-// How a pass is cut up: V channels a lane and TW tokens, tiles of a sequence, columns; the board's words, a ticket's row of 16
-// first, none where a sequence is one tile.
+// How a pass is cut up: W waves a workgroup, V channels a lane and TW tokens, tiles of a sequence, columns; the board's words, a
+// ticket's row of 16 first, none where a sequence is one tile.
 struct Plan {
-  int V, TW, tiles, columns;
+  int W, V, TW, tiles, columns;
   long long words;
+  long long workgroups(int B) const { return (long long)B * tiles * columns; }
 };
-template <class T>
-Plan plan_of(int B, int N, int C, bool pairs, bool backward) {
-  Plan p;
-  p.V = pairs ? 2 : 1;
-  p.TW = (backward ? 8 : 16) / (sizeof(T) == 2 ? 1 : 2);
-  p.tiles = (N + p.TW * kWaves - 1) / (p.TW * kWaves), p.columns = (C + 64 * p.V - 1) / (64 * p.V);
-  const long long row = (long long)B * p.columns * 64 * p.V;
+Plan cut(int B, int N, int C, int W, int V, int TW) {
+  Plan p{W, V, TW, (N + TW * W - 1) / (TW * W), (C + 64 * V - 1) / (64 * V), 0};
+  const long long row = (long long)B * p.columns * 64 * V;
   p.words = p.tiles == 1 ? 0 : 16 + row * (p.tiles + (p.tiles + kGroup - 1) / kGroup);
   return p;
+}
+// Two channels a lane where that gives each CU a workgroup: a wave then moves 256 bytes (bf16) at a time and joins half as many pairs;
+// otherwise one, for twice as many workgroups. (Tiles of 32 tokens for small calls gain a tenth at most, 1 x 512 x 256 8.5 -> 7.7 us, and
+// lose where a sequence has many, 2 x 1024 x 768 11 -> 19.) As many tokens a lane as registers hold.
+constexpr int kCus = 256;
+template <class T>
+Plan plan_of(int B, int N, int C, bool pairs, bool backward) {
+  constexpr bool kHalf = sizeof(T) == 2;
+  const int W = backward && !kHalf ? 16 : 8, TW = backward ? (kHalf ? 8 : 4) : (kHalf ? 16 : 8);
+  const Plan two = cut(B, N, C, W, 2, TW);
+  return pairs && two.workgroups(B) >= kCus ? two : cut(B, N, C, W, 1, TW);
 }
 
 Board board_of(const Plan& p, int B, unsigned long long* w) {
@@ -604,30 +581,31 @@ bool paired(const RecurrenceArgs& a) {
   return ((a.C | a.xs | a.rs | a.is) & 1) == 0 && at % (2 * sizeof(T)) == 0;
 }
 
-template <class T, int V, int TW>
-hipError_t forward(const RecurrenceArgs& a, const Plan& p, unsigned long long* w, hipStream_t st) {
-  const unsigned total = (unsigned)p.tiles * p.columns * a.B;
-  hipLaunchKernelGGL((recurrence_fwd<T, V, TW>), wide_grid(total), dim3(64 * kWaves), 0, st, a, p.tiles, p.columns, total,
+template <class T, int W, int V, int TW>
+void forward(const RecurrenceArgs& a, const Plan& p, unsigned long long* w, hipStream_t st) {
+  const unsigned total = (unsigned)p.workgroups(a.B);
+  hipLaunchKernelGGL((recurrence_fwd<T, W, V, TW>), wide_grid(total), dim3(64 * W), 0, st, a, p.tiles, p.columns, total,
                      board_of(p, a.B, w));
-  return hipGetLastError();
 }
-template <class T, int V, int TW>
-hipError_t backward(const RecurrenceArgs& a, const Plan& p, unsigned long long* w, float* sums, hipStream_t st) {
-  const unsigned total = (unsigned)p.tiles * p.columns * a.B;
-  hipLaunchKernelGGL((recurrence_bwd<T, V, TW>), wide_grid(total), dim3(64 * kWaves), 0, st, a, p.tiles, p.columns, total,
+template <class T, int W, int V, int TW>
+void backward(const RecurrenceArgs& a, const Plan& p, unsigned long long* w, float* sums, hipStream_t st) {
+  const unsigned total = (unsigned)p.workgroups(a.B);
+  hipLaunchKernelGGL((recurrence_bwd<T, W, V, TW>), wide_grid(total), dim3(64 * W), 0, st, a, p.tiles, p.columns, total,
                      board_of(p, a.B, w), sums);
-  return hipGetLastError();
 }
 
+// (By plan_of's pieces.)
 template <class T>
 hipError_t run_forward(const RecurrenceArgs& a, const Plan& p, unsigned long long* w, hipStream_t st) {
   constexpr int TW = sizeof(T) == 2 ? 16 : 8;
-  return p.V == 2 ? forward<T, 2, TW>(a, p, w, st) : forward<T, 1, TW>(a, p, w, st);
+  p.V == 2 ? forward<T, 8, 2, TW>(a, p, w, st) : forward<T, 8, 1, TW>(a, p, w, st);
+  return hipGetLastError();
 }
 template <class T>
 hipError_t run_backward(const RecurrenceArgs& a, const Plan& p, unsigned long long* w, float* sums, hipStream_t st) {
-  constexpr int TW = sizeof(T) == 2 ? 8 : 4;
-  return p.V == 2 ? backward<T, 2, TW>(a, p, w, sums, st) : backward<T, 1, TW>(a, p, w, sums, st);
+  constexpr int W = sizeof(T) == 2 ? 8 : 16, TW = sizeof(T) == 2 ? 8 : 4;
+  p.V == 2 ? backward<T, W, 2, TW>(a, p, w, sums, st) : backward<T, W, 1, TW>(a, p, w, sums, st);
+  return hipGetLastError();
 }
 
 template <class T>
@@ -644,7 +622,7 @@ BackLayout back_layout(int B, int N, int C, bool kept) {
   const long long board = std::max(plan_of<T>(B, N, C, false, true).words, plan_of<T>(B, N, C, true, true).words);
   BackLayout l;
   l.sums = round_up((size_t)board * 8 + (kept ? 0 : forward_bytes<T>(B, N, C)), 256);
-  l.states = l.sums + round_up((size_t)B * plan_of<T>(B, N, C, true, true).tiles * C * 4, 256);
+  l.states = l.sums + round_up((size_t)B * plan_of<T>(B, N, C, true, true).tiles * C * 4, 256);  // (all backward tiles are as long)
   l.bytes = l.states + (kept ? 0 : (size_t)B * ((N + kKept - 1) / kKept) * C * 4);
   return l;
 }
