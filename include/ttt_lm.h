@@ -43,8 +43,7 @@ ttt_status ttt_forward_rmsnorm(ttt_dtype dt, int M, int H, int D, float eps, con
  * The same with an output in 8 bits: y: [M, H, D] of e4m3 (4 bits of exponent, 3 of fraction, largest 448, no
  * infinities), scales: fp32 [M, H, D / group]; y * scale is the norm's output,
  *   scale = max |.| of `group` channels / 448 (of 2^-100 where that is larger), y = the nearest to . / scale, ties to even.
- * group: D (one scale for a row) or 32, 64 or 128 that divide D; with a group other than D, x, residual, sum and weight and their rows
- * are 16-byte aligned and y 8-byte aligned. A group with a NaN is NaN, one with an infinity NaN there and zeros elsewhere.
+ * group: D (one scale for a row), or 32, 64 or 128 where that divides D. A group with a NaN is NaN, one with an infinity NaN there and zeros elsewhere.
  */
 ttt_status ttt_forward_rmsnorm_e4m3(ttt_dtype dt, int M, int H, int D, int group, float eps, const void* x,
                                     long long x_stride, const void* residual, const float* weight, void* sum, void* y,

@@ -60,7 +60,7 @@ ttt_status forward_rmsnorm(ttt_dtype dt, double p, const long long* rng, ttt::Rm
   bufs.out(a.y, e4m3 ? n : n * e, e4m3 ? 1 : e);
   if (e4m3) bufs.out(a.scales, n / a.group * 4, 4);
   add_rng(bufs, p, rng);
-  if (!bufs.ok() || (parts && !ttt::rmsnorm_vector(dt == TTT_BF16, a))) return TTT_ERR_INVALID;
+  if (!bufs.ok()) return TTT_ERR_INVALID;
   return from_hip(ttt::rmsnorm_launch(dt == TTT_BF16, a, static_cast<hipStream_t>(stream)));
 }
 

@@ -23,7 +23,6 @@ struct RmsNormArgs {
   void *ds, *dx;
   float *dw, *partial;
 };
-bool rmsnorm_vector(bool bf16_io, const RmsNormArgs& a);
 hipError_t rmsnorm_launch(bool bf16_io, const RmsNormArgs& a, hipStream_t st);
 size_t rmsnorm_bwd_workspace_bytes(bool bf16_io, int M, int H, int D);
 hipError_t rmsnorm_bwd_launch(bool bf16_io, const RmsNormArgs& a, hipStream_t st);

@@ -83,22 +83,30 @@ inline Shape shape_of(bool bf, bool vec, int D) {
   return {1024, n <= 2048 ? 2 : 4, V};
 }
 
-// Calls f.run<T, L, K, V>() for the shape; every shape shape_of returns is listed.
+// Calls f.run<T, L, K, V>() for the shape; every shape shape_of returns of 16-byte pieces is listed in with_pieces, with_shape has all.
 template <class F>
-hipError_t with_shape(bool bf, Shape s, const F& f) {
+hipError_t with_pieces(bool bf, Shape s, const F& f) {
 #define TTT_LN(T, l, k, v) \
   if (s.L == l && s.K == k && s.V == v) return f.template run<T, l, k, v>();
-#define TTT_LN_SCALAR(T) \
-  TTT_LN(T, 64, 1, 1) TTT_LN(T, 64, 4, 1) TTT_LN(T, 64, 16, 1) TTT_LN(T, 256, 16, 1) TTT_LN(T, 1024, 16, 1)
   if (bf) {
     TTT_LN(bf16, 8, 1, 8) TTT_LN(bf16, 16, 1, 8) TTT_LN(bf16, 32, 1, 8) TTT_LN(bf16, 64, 1, 8)
     TTT_LN(bf16, 64, 2, 8) TTT_LN(bf16, 64, 3, 8) TTT_LN(bf16, 256, 1, 8) TTT_LN(bf16, 256, 2, 8)
     TTT_LN(bf16, 1024, 1, 8) TTT_LN(bf16, 1024, 2, 8)
-    TTT_LN_SCALAR(bf16)
   } else {
     TTT_LN(float, 8, 1, 4) TTT_LN(float, 16, 1, 4) TTT_LN(float, 32, 1, 4) TTT_LN(float, 64, 1, 4)
     TTT_LN(float, 64, 2, 4) TTT_LN(float, 64, 4, 4) TTT_LN(float, 256, 2, 4) TTT_LN(float, 256, 4, 4)
     TTT_LN(float, 1024, 2, 4) TTT_LN(float, 1024, 4, 4)
+  }
+  return hipErrorInvalidValue;
+}
+template <class F>
+hipError_t with_shape(bool bf, Shape s, const F& f) {
+#define TTT_LN_SCALAR(T) \
+  TTT_LN(T, 64, 1, 1) TTT_LN(T, 64, 4, 1) TTT_LN(T, 64, 16, 1) TTT_LN(T, 256, 16, 1) TTT_LN(T, 1024, 16, 1)
+  if (s.V > 1) return with_pieces(bf, s, f);
+  if (bf) {
+    TTT_LN_SCALAR(bf16)
+  } else {
     TTT_LN_SCALAR(float)
   }
 #undef TTT_LN_SCALAR

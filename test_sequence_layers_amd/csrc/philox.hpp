@@ -47,29 +47,17 @@ __device__ __forceinline__ Random8 random8(unsigned long long seed, unsigned lon
 }
 
 // The masks of a row that L lanes hold in K accesses of V elements (element (k L + lane) V + i): bit i of bits[k]. `first` is
-// the counter of the row's first 8 elements. Of single elements, eight lanes have eight elements of one counter: lane j of
-// them evaluates access j's and hands it round.
+// the counter of the row's first 8 elements.
 template <int L, int K, int V>
 struct RowMask {
+  static_assert(V == 8 || (V == 4 && L % 2 == 0), "");
   uint32_t bits[K];
   __device__ __forceinline__ void make(unsigned long long seed, unsigned long long first, uint32_t least, int lane) {
-    if constexpr (V == 8) {
 #pragma unroll
-      for (int k = 0; k < K; ++k) bits[k] = random8(seed, first + (unsigned)(k * L + lane)).mask(least);
-    } else if constexpr (V == 4) {
-#pragma unroll
-      for (int k = 0; k < K; ++k)
-        bits[k] = random8(seed, first + ((unsigned)(k * L + lane) >> 1)).mask(least) >> (4 * (lane & 1));
-    } else {
-      static_assert(V == 1 && L % 8 == 0, "");
-      const int base = (threadIdx.x & 63) & ~7;
-#pragma unroll
-      for (int q = 0; q < K; q += 8) {
-        const uint32_t mine = random8(seed, first + (unsigned)(((q + (lane & 7)) * L + (lane & ~7)) >> 3)).mask(least);
-#pragma unroll
-        for (int k = q; k < K && k < q + 8; ++k)
-          bits[k] = (uint32_t)__builtin_amdgcn_ds_bpermute(4 * (base + (k & 7)), (int)mine) >> (lane & 7);
-      }
+    for (int k = 0; k < K; ++k) {
+      const unsigned piece = (unsigned)(k * L + lane);
+      if constexpr (V == 8) bits[k] = random8(seed, first + piece).mask(least);
+      else bits[k] = random8(seed, first + (piece >> 1)).mask(least) >> (4 * (lane & 1));
     }
   }
   __device__ __forceinline__ bool kept(int k, int i) const { return (bits[k] >> i) & 1u; }

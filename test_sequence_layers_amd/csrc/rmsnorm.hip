@@ -11,9 +11,81 @@
 #include "lm.hpp"
 #include "normrows.hpp"
 #include "philox.hpp"
+#include "pieces.hpp"
 
 namespace ttt {
 namespace {
+
+// Where a row's D elements are over L lanes: piece k L + lane of access k. With TAIL the last is a part of one: it is read as the
+// last whole piece of the row, over the one before it, in the same access as the others, and moved to the front when it is used (where
+// a row is less than a piece, element by element). Without, D is a multiple of V.
+template <int L, int V, bool TAIL>
+struct Spread {
+  int lane, D, whole, rest;  // whole pieces; elements behind them
+  __device__ __forceinline__ Spread(int lane, int D) : lane(lane), D(D), whole(D / V), rest(D % V) {}
+  __device__ __forceinline__ bool full(int k) const { return k * L + lane < whole; }
+  __device__ __forceinline__ bool any(int k) const { return TAIL ? (k * L + lane) * V < D : full(k); }
+  __device__ __forceinline__ bool has_part(int k) const { return TAIL && whole / L == k; }  // (the same for all lanes)
+  __device__ __forceinline__ bool part() const { return lane == whole % L; }
+  // Where to read access k's piece; past the row its first.
+  __device__ __forceinline__ int from(int k) const {
+    const int at = (k * L + lane) * V;
+    return full(k) ? at : TAIL && any(k) ? D - V : 0;
+  }
+};
+
+template <class T, int L, int K, bool TAIL>
+struct AnyRow {
+  static constexpr int V = kPiece<T>;
+  typedef Spread<L, V, TAIL> S;
+  Piece<T> r[K];
+  __device__ __forceinline__ void load(const T* p, const S& s) {
+    if (TAIL && s.whole == 0) {
+      if (s.lane == 0) r[0].load_some(p, s.rest);
+      return;
+    }
+#pragma unroll
+    for (int k = 0; k < K; ++k) r[k].load(p + s.from(k));
+  }
+  __device__ __forceinline__ void widen(float* v, const S& s, bool in = true) const {
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      Piece<T> q = r[k];
+      if (s.has_part(k) && s.whole > 0) {
+        q.keep_last(s.rest);
+        if (!s.part()) q = r[k];
+      }
+      q.widen(v + k * V);
+      const bool ok = in && s.any(k);
+      for (int i = 0; i < V; ++i) v[k * V + i] = ok ? v[k * V + i] : 0.f;
+    }
+  }
+  static __device__ __forceinline__ void store(T* p, const float* v, const S& s) {
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      if (s.full(k)) Piece<T>::store(p + (k * L + s.lane) * V, v + k * V);
+      if (s.has_part(k) && s.part()) Piece<T>::store_some(p + s.whole * V, v + k * V, s.rest);
+    }
+  }
+};
+
+// The fp32 weights of a row's elements; past the row's end the last.
+template <int L, int K, int V, bool TAIL>
+__device__ __forceinline__ void load_weights(const float* w, float* out, const Spread<L, V, TAIL>& s) {
+#pragma unroll
+  for (int k = 0; k < K; ++k) {
+    if (s.has_part(k)) {
+      for (int i = 0; i < V; ++i) out[k * V + i] = w[min((k * L + s.lane) * V + i, s.D - 1)];
+    } else {
+#pragma unroll
+      for (int i = 0; i < V; i += 4) {
+        Piece<float> q;
+        q.load(w + (s.full(k) ? (k * L + s.lane) * V : 0) + i);
+        q.widen(out + k * V + i);
+      }
+    }
+  }
+}
 
 // rstd of a row, times *back; v is scaled by 1 / *back where its squares overflow (from 2^60 or so on: the largest squares
 // are 2^96 then, and eps is nothing beside them), so that such rows are normed like others. An infinite or NaN entry makes its row
@@ -41,11 +113,11 @@ __device__ __forceinline__ float inverse_rms(float* v, int D, float eps, float (
   return rcp_hw(sqrtf(fmaf(q, rcp_hw((float)D), eps)));
 }
 
-// v -> residual + v keep scale (v's own values where there is no residual), the values before they are rounded.
-template <int L, int K, int V>
-__device__ __forceinline__ void drop_row(float* v, const Drop& d, long long row, int D, int lane) {
+// v -> v keep scale.
+template <int L, int K, int V, bool TAIL>
+__device__ __forceinline__ void drop_row(float* v, const Drop& d, long long row, const Spread<L, V, TAIL>& s) {
   RowMask<L, K, V> m;
-  m.make(d.rng[0], d.rng[1] + (unsigned long long)row * (unsigned)((D + 7) / 8), d.least, lane);
+  m.make(d.rng[0], d.rng[1] + (unsigned long long)row * (unsigned)((s.D + 7) / 8), d.least, s.lane);
 #pragma unroll
   for (int k = 0; k < K; ++k)
     for (int i = 0; i < V; ++i) v[k * V + i] = m.kept(k, i) ? v[k * V + i] * d.scale : 0.f;
@@ -76,73 +148,80 @@ __device__ __forceinline__ uint32_t lanes_max(uint32_t v, int L) {
 }
 
 // Four e4m3 of four fp32, rounded to nearest even; values are within +-448 (1 + 2^-22) or NaN.
-__device__ __forceinline__ uint32_t to_e4m3(float a, float b, float c, float d) {
-  int r = __builtin_amdgcn_cvt_pk_fp8_f32(a, b, 0, false);
-  return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(c, d, r, true);
+__device__ __forceinline__ uint32_t to_e4m3(const float* v) {
+  const int r = __builtin_amdgcn_cvt_pk_fp8_f32(v[0], v[1], 0, false);
+  return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(v[2], v[3], r, true);
 }
-template <int V>
-__device__ __forceinline__ void store_e4m3(uint8_t* p, const float* v) {
-  if constexpr (V == 8) {
-    *reinterpret_cast<uint2*>(p) = make_uint2(to_e4m3(v[0], v[1], v[2], v[3]), to_e4m3(v[4], v[5], v[6], v[7]));
-  } else if constexpr (V == 4) {
-    *reinterpret_cast<uint32_t*>(p) = to_e4m3(v[0], v[1], v[2], v[3]);
-  } else {
-    p[0] = (uint8_t)to_e4m3(v[0], 0.f, 0.f, 0.f);
+template <int K, int L, int V, bool TAIL>
+__device__ __forceinline__ void store_e4m3(uint8_t* p, const float* v, const Spread<L, V, TAIL>& s) {
+  typedef uint32_t Any __attribute__((aligned(1)));
+#pragma unroll
+  for (int k = 0; k < K; ++k) {
+    uint32_t q[V / 4];
+#pragma unroll
+    for (int i = 0; i < V / 4; ++i) q[i] = to_e4m3(v + k * V + 4 * i);
+    if (s.full(k)) {
+#pragma unroll
+      for (int i = 0; i < V / 4; ++i) reinterpret_cast<Any*>(p + (k * L + s.lane) * V)[i] = q[i];
+    }
+    if (s.has_part(k) && s.part()) {
+#pragma unroll
+      for (int i = 0; i < V - 1; ++i)
+        if (i < s.rest) p[s.whole * V + i] = (uint8_t)(q[i / 4] >> (8 * (i & 3)));
+    }
   }
 }
 
 constexpr float kE4m3Most = 448.f;
 constexpr float kLeastMax = 0x1p-100f;  // a smaller maximum's inverse could be infinite; such values are zeros in 8 bits
 
-template <class T, int L, int K, int V, bool ADD, bool E4M3>
+template <class T, int L, int K, bool TAIL, bool ADD, bool E4M3>
 __global__ __launch_bounds__(threads_of<L>) void rmsnorm_fwd(const T* __restrict__ x, long long xs, const T* res,
                                                              const float* __restrict__ w, T* sum, void* __restrict__ y,
                                                              float* __restrict__ scales, int rows, int H, int D,
                                                              int group, float eps, Drop drop) {
+  constexpr int V = kPiece<T>;
   __shared__ float red[2][16];
-  const int lane = threadIdx.x % L;
+  const Spread<L, V, TAIL> s(threadIdx.x % L, D);
   const long long row = wide_block() * (threads_of<L> / L) + threadIdx.x / L;
   if (row >= rows) return;  // (whole groups; for L > 64 the whole workgroup)
   const int m = (int)(row / H), h = (int)(row - (long long)m * H);
-  Row<T, L, K, V> rx, rr;
-  rx.load(x + (long long)m * xs + (long long)h * D, lane, D);
-  if (ADD) rr.load(res + row * D, lane, D);
-  float v[K * V];
-  rx.widen(v, lane, D);
+  AnyRow<T, L, K, TAIL> rx, rr;
+  rx.load(x + (long long)m * xs + (long long)h * D, s);
+  if (ADD) rr.load(res + row * D, s);
+  float v[K * V], wv[K * V];
+  rx.widen(v, s);
   if (ADD) {
-    if (drop.least) drop_row<L, K, V>(v, drop, row, D, lane);
+    if (drop.least) drop_row<L, K>(v, drop, row, s);
     float r[K * V];
-    rr.widen(r, lane, D);
+    rr.widen(r, s);
 #pragma unroll
-    for (int k = 0; k < K; ++k) {
-      const int at = (k * L + lane) * V;
-      for (int i = 0; i < V; ++i) v[k * V + i] += r[k * V + i];
-      if (at < D) store_row<T, V>(sum + row * D + at, v + k * V);
-    }
+    for (int j = 0; j < K * V; ++j) v[j] += r[j];
+    AnyRow<T, L, K, TAIL>::store(sum + row * D, v, s);
   }
+  load_weights<L, K>(w + (long long)h * D, wv, s);
   float back;
   const float rstd = inverse_rms<L, K, V>(v, D, eps, red, &back);
-#pragma unroll
-  for (int k = 0; k < K; ++k) {
-    const int at = (k * L + lane) * V;
-    float wv[V];
-    load_params<V>(w + (long long)h * D + (at < D ? at : 0), wv);
-    for (int i = 0; i < V; ++i) v[k * V + i] *= rstd * wv[i];
-  }
   if constexpr (!E4M3) {
 #pragma unroll
-    for (int k = 0; k < K; ++k) {
-      const int at = (k * L + lane) * V;
-      if (at < D) store_row<T, V>((T*)y + row * D + at, v + k * V);
-    }
+    for (int j = 0; j < K * V; ++j) v[j] *= rstd * wv[j];
+    AnyRow<T, L, K, TAIL>::store((T*)y + row * D, v, s);
   } else {
-    // Maxima of the absolute values' bits: as numbers they are in the same order, and a NaN is above all.
+    // rstd is not in y / scale: of v w, its maximum M over the group and 448 / M, the first and the last as two numbers
+    // each, so that the rounding to 8 bits has but one other before it. Maxima of the absolute values' bits: as numbers they are in the
+    // same order, and a NaN is above all.
+    float low[K * V];
     uint32_t most[K], all = 0;
 #pragma unroll
     for (int k = 0; k < K; ++k) {
       most[k] = 0;
-      if ((k * L + lane) * V < D)
-        for (int i = 0; i < V; ++i) most[k] = max(most[k], __float_as_uint(v[k * V + i]) & 0x7fffffffu);
+      for (int i = 0; i < V; ++i) {
+        const int j = k * V + i;
+        const float t = v[j] * wv[j];
+        low[j] = fmaf(v[j], wv[j], -t);
+        v[j] = (TAIL ? (k * L + s.lane) * V + i < D : s.full(k)) ? t : 0.f;
+        most[k] = max(most[k], __float_as_uint(v[j]) & 0x7fffffffu);
+      }
       all = max(all, most[k]);
     }
     if (group == D) {
@@ -158,49 +237,52 @@ __global__ __launch_bounds__(threads_of<L>) void rmsnorm_fwd(const T* __restrict
     const int share = group / V;  // lanes of a group, where it is less than the row
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-      const int at = (k * L + lane) * V;
-      float top = __uint_as_float(group == D ? all : lanes_max(most[k], share));
-      top = top < kLeastMax ? kLeastMax : top;
-      const float inv = kE4m3Most / top;
-      if (at < D) {
-        for (int i = 0; i < V; ++i) v[k * V + i] *= inv;
-        store_e4m3<V>((uint8_t*)y + row * D + at, v + k * V);
-        if (group == D ? at == 0 : (lane & (share - 1)) == 0) scales[(row * D + at) / group] = top / kE4m3Most;
+      const float top = __uint_as_float(group == D ? all : lanes_max(most[k], share));
+      float scaled = top * rstd;  // the largest of the norm's output
+      const bool odd = !(scaled >= kLeastMax && scaled < __builtin_inff());
+      const float r = rcp_hw(top), inv = kE4m3Most * r, inv_low = fmaf(-inv, top, kE4m3Most) * r;
+      if (__ballot(odd) == 0) {
+        for (int i = 0; i < V; ++i) v[k * V + i] = fmaf(v[k * V + i], inv, fmaf(v[k * V + i], inv_low, low[k * V + i] * inv));
+      } else {  // zeros, next to nothing, infinities, NaN
+        scaled = scaled < kLeastMax ? kLeastMax : scaled;
+        const float plain = rstd * (kE4m3Most / scaled);
+        for (int i = 0; i < V; ++i) {
+          const int j = k * V + i;
+          v[j] = odd ? v[j] * plain : fmaf(v[j], inv, fmaf(v[j], inv_low, low[j] * inv));
+        }
       }
+      const int at = (k * L + s.lane) * V;
+      if (at < D && (group == D ? at == 0 : (s.lane & (share - 1)) == 0)) scales[(row * D + at) / group] = scaled / kE4m3Most;
     }
+    store_e4m3<K>((uint8_t*)y + row * D, v, s);
   }
 }
 
 // Workgroup (bx, by): as in layer norm's backward pass, R tokens at a time of the HB heads from by HB on. Partial row bx: dw (H D).
-template <class T, int L, int K, int V, bool ADD>
-__global__ __launch_bounds__(bwd_threads(L, K* V)) void rmsnorm_bwd(const T* __restrict__ s, long long ss,
-                                                                    const float* __restrict__ w,
-                                                                    const T* __restrict__ dy, const T* dsum, T* ds,
-                                                                    T* __restrict__ dx, float* __restrict__ part, int M,
-                                                                    int H, int D, int HB, int R, float eps, Drop drop) {
-  constexpr int LKV = L * K * V;
+template <class T, int L, int K, bool TAIL, bool ADD>
+__global__ __launch_bounds__(bwd_threads(L, K* kPiece<T>)) void rmsnorm_bwd(const T* __restrict__ sum, long long ss,
+                                                                            const float* __restrict__ w,
+                                                                            const T* __restrict__ dy, const T* dsum, T* ds,
+                                                                            T* __restrict__ dx, float* __restrict__ part,
+                                                                            int M, int H, int D, int HB, int R, float eps,
+                                                                            Drop drop) {
+  constexpr int V = kPiece<T>, LKV = L * K * V;
   constexpr bool kRoom = L <= 256;  // (as in layer norm's backward pass)
   __shared__ float red[4][16];
   __shared__ float join[L <= 64 ? bwd_threads(L, K * V) * K * V : 1];
-  const int lane = threadIdx.x % L, g = threadIdx.x / L;
+  const int g = threadIdx.x / L;
+  const Spread<L, V, TAIL> s(threadIdx.x % L, D);
   const int r = g / HB, hg = blockIdx.y * HB + g % HB, h = min(hg, H - 1);
   const bool live = r < R && hg < H;
   const float inv_d = rcp_hw((float)D);
   float wv[K * V], aw[K * V] = {};
-  auto weights = [&]() {
-#pragma unroll
-    for (int k = 0; k < K; ++k) {
-      const int at = (k * L + lane) * V;
-      load_params<V>(w + (long long)h * D + (at < D ? at : 0), wv + k * V);
-    }
-  };
-  if (kRoom) weights();
-  Row<T, L, K, V> rx, rd, rr;
+  if (kRoom) load_weights<L, K>(w + (long long)h * D, wv, s);
+  AnyRow<T, L, K, TAIL> rx, rd, rr;
   auto fetch = [&](long long m) {  // (past the last token: the last again)
     const long long t = m < M ? m : M - 1;
-    rx.load(s + t * ss + (long long)h * D, lane, D);
-    rd.load(dy + (t * H + h) * D, lane, D);
-    if (ADD) rr.load(dsum + (t * H + h) * D, lane, D);
+    rx.load(sum + t * ss + (long long)h * D, s);
+    rd.load(dy + (t * H + h) * D, s);
+    if (ADD) rr.load(dsum + (t * H + h) * D, s);
   };
   const long long step = (long long)gridDim.x * R;
   if (kRoom) fetch((long long)blockIdx.x * R + r);
@@ -209,13 +291,13 @@ __global__ __launch_bounds__(bwd_threads(L, K* V)) void rmsnorm_bwd(const T* __r
     const bool in = live && m < M;
     float v[K * V], d[K * V], e[K * V];
     if (!kRoom) fetch(m);
-    rx.widen(v, lane, D);
-    rd.widen(d, lane, D, in);
-    if (ADD) rr.widen(e, lane, D, in);
+    rx.widen(v, s);
+    rd.widen(d, s, in);
+    if (ADD) rr.widen(e, s, in);
     if (kRoom) fetch(m + step);
     float back;
     const float rstd = inverse_rms<L, K, V>(v, D, eps, red, &back);
-    if (!kRoom) weights();
+    if (!kRoom) load_weights<L, K>(w + (long long)h * D, wv, s);
     float s2 = 0.f;
 #pragma unroll
     for (int j = 0; j < K * V; ++j) {
@@ -229,18 +311,10 @@ __global__ __launch_bounds__(bwd_threads(L, K* V)) void rmsnorm_bwd(const T* __r
 #pragma unroll
     for (int j = 0; j < K * V; ++j) d[j] = outer * (d[j] - v[j] * s2) + (ADD ? e[j] : 0.f);
     const long long o = (m * H + h) * D;
-#pragma unroll
-    for (int k = 0; k < K; ++k) {
-      const int at = (k * L + lane) * V;
-      if (in && at < D) store_row<T, V>(ds + o + at, d + k * V);
-    }
+    if (in) AnyRow<T, L, K, TAIL>::store(ds + o, d, s);
     if (dx) {
-      if (drop.least) drop_row<L, K, V>(d, drop, m, D, lane);
-#pragma unroll
-      for (int k = 0; k < K; ++k) {
-        const int at = (k * L + lane) * V;
-        if (in && at < D) store_row<T, V>(dx + o + at, d + k * V);
-      }
+      if (drop.least) drop_row<L, K>(d, drop, m, s);
+      if (in) AnyRow<T, L, K, TAIL>::store(dx + o, d, s);
     }
   }
   const long long W = (long long)H * D;
@@ -249,21 +323,21 @@ __global__ __launch_bounds__(bwd_threads(L, K* V)) void rmsnorm_bwd(const T* __r
 #pragma unroll
     for (int k = 0; k < K; ++k)
       for (int i = 0; i < V; ++i) {
-        const int at = (k * L + lane) * V + i;
+        const int at = (k * L + s.lane) * V + i;
         if (at < D) row[(long long)h * D + at] = aw[k * V + i];
       }
   } else {
     __syncthreads();
 #pragma unroll
     for (int k = 0; k < K; ++k)
-      for (int i = 0; i < V; ++i) join[g * LKV + (k * L + lane) * V + i] = aw[k * V + i];
+      for (int i = 0; i < V; ++i) join[g * LKV + (k * L + s.lane) * V + i] = aw[k * V + i];
     __syncthreads();
     for (int t = threadIdx.x; t < HB * D; t += blockDim.x) {
       const int hh = t / D, at = t - hh * D;
       if (blockIdx.y * HB + hh >= H) break;
-      float sum = 0.f;
-      for (int q = 0; q < R; ++q) sum += join[(q * HB + hh) * LKV + at];
-      row[(long long)(blockIdx.y * HB + hh) * D + at] = sum;
+      float total = 0.f;
+      for (int q = 0; q < R; ++q) total += join[(q * HB + hh) * LKV + at];
+      row[(long long)(blockIdx.y * HB + hh) * D + at] = total;
     }
   }
 }
@@ -278,14 +352,18 @@ struct FwdCall {
   hipStream_t st;
   template <class T, int L, int K, int V>
   hipError_t run() const {
-    return a.scales ? (a.residual ? go<T, L, K, V, true, true>() : go<T, L, K, V, false, true>())
-                    : (a.residual ? go<T, L, K, V, true, false>() : go<T, L, K, V, false, false>());
+    return a.D % V ? some<T, L, K, true>() : some<T, L, K, false>();
   }
-  template <class T, int L, int K, int V, bool ADD, bool E4M3>
+  template <class T, int L, int K, bool TAIL>
+  hipError_t some() const {
+    return a.scales ? (a.residual ? go<T, L, K, TAIL, true, true>() : go<T, L, K, TAIL, false, true>())
+                    : (a.residual ? go<T, L, K, TAIL, true, false>() : go<T, L, K, TAIL, false, false>());
+  }
+  template <class T, int L, int K, bool TAIL, bool ADD, bool E4M3>
   hipError_t go() const {
     constexpr int G = threads_of<L> / L;
     const int rows = a.M * a.H;
-    hipLaunchKernelGGL((rmsnorm_fwd<T, L, K, V, ADD, E4M3>), wide_grid(((long long)rows + G - 1) / G), dim3(threads_of<L>), 0,
+    hipLaunchKernelGGL((rmsnorm_fwd<T, L, K, TAIL, ADD, E4M3>), wide_grid(((long long)rows + G - 1) / G), dim3(threads_of<L>), 0,
                        st, (const T*)a.x, a.xs, (const T*)a.residual, a.w, (T*)a.sum, a.y, a.scales, rows, a.H, a.D,
                        a.group, a.eps, a.drop);
     return hipGetLastError();
@@ -298,12 +376,13 @@ struct BwdCall {
   hipStream_t st;
   template <class T, int L, int K, int V>
   hipError_t run() const {
-    return a.dsum ? go<T, L, K, V, true>() : go<T, L, K, V, false>();
+    return a.D % V ? (a.dsum ? go<T, L, K, true, true>() : go<T, L, K, true, false>())
+                   : (a.dsum ? go<T, L, K, false, true>() : go<T, L, K, false, false>());
   }
-  template <class T, int L, int K, int V, bool ADD>
+  template <class T, int L, int K, bool TAIL, bool ADD>
   hipError_t go() const {
     const int threads = L <= 64 ? (p.HB * p.R * L + 63) / 64 * 64 : L;
-    hipLaunchKernelGGL((rmsnorm_bwd<T, L, K, V, ADD>), dim3((unsigned)p.P, (unsigned)p.gy), dim3(threads), 0, st,
+    hipLaunchKernelGGL((rmsnorm_bwd<T, L, K, TAIL, ADD>), dim3((unsigned)p.P, (unsigned)p.gy), dim3(threads), 0, st,
                        (const T*)a.x, a.xs, a.w, (const T*)a.dy, (const T*)a.dsum, (T*)a.ds, (T*)a.dx, a.partial, a.M,
                        a.H, a.D, p.HB, p.R, a.eps, a.drop);
     return hipGetLastError();
@@ -312,29 +391,18 @@ struct BwdCall {
 
 }  // namespace
 
-bool rmsnorm_vector(bool bf16_io, const RmsNormArgs& a) {
-  const void* all[] = {a.x, a.residual, a.w, a.sum, a.dy, a.dsum, a.ds, a.dx};
-  if (!vector_rows(bf16_io, a.D, a.xs)) return false;
-  for (const void* p : all)
-    if (!aligned16(p)) return false;
-  const uintptr_t y = reinterpret_cast<uintptr_t>(a.y);  // in 8 bits an access is a byte for each element
-  return (y & (a.scales ? (bf16_io ? 7u : 3u) : 15u)) == 0;
-}
-
 hipError_t rmsnorm_launch(bool bf16_io, const RmsNormArgs& a, hipStream_t st) {
-  return with_shape(bf16_io, shape_of(bf16_io, rmsnorm_vector(bf16_io, a), a.D), FwdCall{a, st});
+  return with_pieces(bf16_io, shape_of(bf16_io, true, a.D), FwdCall{a, st});
 }
 
 size_t rmsnorm_bwd_workspace_bytes(bool bf16_io, int M, int H, int D) {
-  long long P = bwd_plan(shape_of(bf16_io, false, D), M, H).P;
-  if (vector_rows(bf16_io, D, 0)) P = std::max(P, bwd_plan(shape_of(bf16_io, true, D), M, H).P);
-  return (size_t)P * H * D * sizeof(float);
+  return (size_t)bwd_plan(shape_of(bf16_io, true, D), M, H).P * H * D * sizeof(float);
 }
 
 hipError_t rmsnorm_bwd_launch(bool bf16_io, const RmsNormArgs& a, hipStream_t st) {
-  const Shape s = shape_of(bf16_io, rmsnorm_vector(bf16_io, a), a.D);
+  const Shape s = shape_of(bf16_io, true, a.D);
   const BwdPlan p = bwd_plan(s, a.M, a.H);
-  const hipError_t e = with_shape(bf16_io, s, BwdCall{a, p, st});
+  const hipError_t e = with_pieces(bf16_io, s, BwdCall{a, p, st});
   if (e != hipSuccess) return e;
   return column_sum_launch(a.partial, p.P, a.H * a.D, StoreWeightGrad{a.dw}, st);
 }

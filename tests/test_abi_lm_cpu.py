@@ -54,8 +54,8 @@ def _e4m3(dt=BF16, M=8, H=1, D=256, group=128, eps=1e-5, x=P[0], xs=256, res=P[1
 
 @pytest.mark.parametrize("kw,want", [
     (dict(group=0), INVALID), (dict(group=96), INVALID), (dict(group=16), UNSUPPORTED), (dict(sc=None), INVALID), (dict(sc=P[5]), INVALID),
-    (dict(sc=P[6] + 2), INVALID), (dict(x=P[0] + 2), INVALID), (dict(xs=257), INVALID), (dict(y=P[5] + 4), INVALID),
-    (dict(w=P[3] + 4), INVALID), (dict(res=P[1] + 8), INVALID), (dict(s=P[4] + 8), INVALID), (dict(y=P[4]), INVALID),
+    (dict(sc=P[6] + 2), INVALID), (dict(x=P[0] + 1), INVALID), (dict(xs=255), INVALID), (dict(res=P[1] + 1), INVALID),
+    (dict(w=P[3] + 2), INVALID), (dict(s=P[1] + 8), INVALID), (dict(y=P[4]), INVALID),
     (dict(s=None), INVALID), (dict(H=2, D=128), UNSUPPORTED)])
 def test_rmsnorm_e4m3_refusals(kw, want):
     assert _e4m3(**kw) == want

@@ -46,6 +46,19 @@ def test_dropout(case, add):
     assert torch.equal(d_x != 0, (f > 0) & (d_y != 0))
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_every_narrow_width_at_every_alignment(dtype):
+    for C in [*range(1, 26), 511, 513]:
+        i = Inputs(C, dtype)
+        e = C % 8
+        x, res, f = sliced(i.normal(9, C), 1, e), i.normal(9, C), factors(SEED, OFFSET, 0.5, 9, C)
+        around = torch.full((9 * C + 32,), 7.0, dtype=i.io, device="cuda")
+        y = around[8 + e:8 + e + 9 * C].view(9, C)
+        T.ttt_forward_dropout(x, 0.5, rng_of(SEED, OFFSET), residual=res, y=y)
+        held(f"y of {C}", y, R.dropout(x, f, res))
+        assert bool((around[:8 + e] == 7).all()) and bool((around[8 + e + 9 * C:] == 7).all())
+
+
 def test_the_mask_is_the_norms():
     """A call of its own, of rows or one of many, drops what the fused one does."""
     i = Inputs(1, "fp32")

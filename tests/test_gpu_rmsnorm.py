@@ -80,6 +80,35 @@ def test_residual_and_dropout(case, p):
         assert d_x is None
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_every_narrow_width_at_every_alignment(dtype):
+    """Widths of 1 .. 40 and around whole accesses, rows starting at every element of 16 bytes: the sums of a row to the bounds, and
+    what is around the outputs as it was."""
+    for D in [*range(1, 41), 63, 65, 127, 129, 511, 513, 1023, 1025, 2047, 2049]:
+        i = Inputs(D, dtype)
+        e = D % 8
+        w, x, res, d_y = i.param(D, mean=1.0, scale=0.2), sliced(i.normal(5, D), 1, e), i.normal(5, D), i.normal(5, D)
+
+        def inside():
+            around = torch.full((5 * D + 32,), 7.0, dtype=i.io, device="cuda")
+            return around, around[8 + e:8 + e + 5 * D].view(5, D)
+
+        (by, y), (bs, s), (bd, d_s) = inside(), inside(), inside()
+        T.ttt_forward_rmsnorm(x, w, EPS, residual=res, y=y, sum_out=s)
+        ref = R.rmsnorm(x, w, EPS, DEPTH, res)
+        held(f"y of {D}", y, ref["y"])
+        held(f"sum of {D}", s, ref["sum"])
+        d_w = T.ttt_backward_rmsnorm(s, w, d_y, EPS, d_s=d_s)[2]
+        ref = R.rmsnorm_backward(s, w, d_y, EPS, DEPTH, 140)
+        held(f"d_s of {D}", d_s, ref["d_s"])
+        held(f"d_weight of {D}", d_w, ref["d_weight"])
+        for around in (by, bs, bd):
+            assert bool((around[:8 + e] == 7).all()) and bool((around[8 + e + 5 * D:] == 7).all())
+        q, scales = T.ttt_forward_rmsnorm_e4m3(x, w, EPS)
+        ref = R.rmsnorm_e4m3(x, w, EPS, DEPTH, D)
+        within(f"y * scales of {D}", q.double() * scales.double(), ref["deq"])
+
+
 @pytest.mark.parametrize("add", [False, True])
 @pytest.mark.parametrize("M,H,D,dtype,group,cut", [
     (1, 1, 1, "fp32", 0, False), (3, 1, 7, "bf16", 0, False), (16, 1, 768, "bf16", 0, False), (5, 1, 33, "fp32", 0, True),
@@ -233,8 +262,6 @@ def test_refusals():
             T.ttt_forward_rmsnorm_e4m3(**(dict(x=x, weight=w) | bad))
     with pytest.raises(T.TTTError):
         T.ttt_forward_rmsnorm_e4m3(x, w, group=16)
-    with pytest.raises(T.TTTError):  # groups need 16-byte rows
-        T.ttt_forward_rmsnorm_e4m3(sliced(x, 1, 3), w, group=32)
     d_y = torch.zeros_like(x)
     for bad in (dict(d_x=torch.zeros_like(x)), dict(p=0.5), dict(d_sum=res[:2]), dict(d_y=d_y[:2])):
         with pytest.raises((ValueError, TypeError)):
