@@ -141,10 +141,11 @@ struct Board {
   unsigned* ticket;
   unsigned long long *pairs, *states;
 };
-// Two boards, one behind the other; `second`: where that starts (and its ticket counter is), or the end.
-__global__ void clear_board(unsigned long long* p, long long second, long long words) {
-  for (long long k = (long long)blockIdx.x * blockDim.x + threadIdx.x; k < words; k += (long long)gridDim.x * blockDim.x)
-    p[k] = k == 0 || k == second ? 0ull : kNotYet;
+// Two boards, one behind the other; `second`: where that starts (and its ticket counter is), or the end. Words in twos.
+constexpr int kClearThreads = 256;
+__global__ __launch_bounds__(kClearThreads) void clear_board(ulonglong2* p, long long second, long long words) {
+  const long long k = wide_block() * kClearThreads + threadIdx.x;
+  if (2 * k < words) p[k] = make_ulonglong2(k == 0 || 2 * k == second ? 0ull : kNotYet, kNotYet);
 }
 
 // Tile `tile` of column `column` of sequence b. Ids go through the columns first.
@@ -567,8 +568,8 @@ Board board_of(const Plan& p, int B, unsigned long long* w) {
 
 hipError_t clear(unsigned long long* w, long long one, long long two, hipStream_t st) {
   if (one + two == 0) return hipSuccess;
-  const long long blocks = (one + two + 1023) / 1024;
-  hipLaunchKernelGGL(clear_board, dim3((unsigned)(blocks < 1024 ? blocks : 1024)), dim3(256), 0, st, w, one, one + two);
+  hipLaunchKernelGGL(clear_board, wide_grid((one + two + 2 * kClearThreads - 1) / (2 * kClearThreads)), dim3(kClearThreads), 0, st,
+                     reinterpret_cast<ulonglong2*>(w), one, one + two);
   return hipGetLastError();
 }
 

@@ -22,6 +22,9 @@ CASES = [  # B, N, C, dtype, h0, lengths, sliced
     (2, 333, 193, "bf16", True, None, True), (1, 511, 2050, "bf16", False, None, False), (1, 1023, 70, "fp32", True, None, False),
     (3, 1999, 1000, "fp32", True, [1999, 777, 1500], False), (2, 2048, 768, "bf16", False, None, True),
     (1, 4097, 300, "bf16", True, None, False), (8, 700, 96, "bf16", True, [700, 0, 1, 64, 65, 256, 257, 699], True),
+    # two channels a lane, several groups of tiles, ends in each
+    (4, 5000, 386, "bf16", True, [5000, 0, 2049, 4100], True), (4, 5000, 384, "bf16", False, None, False),
+    (5, 2500, 258, "fp32", True, [2500, 1024, 1025, 63, 2049], False), (2, 9000, 129, "bf16", True, [9000, 8193], False),
     (1, 16500, 64, "fp32", True, None, False), (1, 10000, 130, "bf16", False, [9001], False), (65, 40, 1, "fp32", True, None, False),
 ]
 ids = lambda c: "-".join(str(v) for v in c[:5]) + ("-lengths" if c[5] else "") + ("-sliced" if c[6] else "")  # noqa: E731
