@@ -136,36 +136,43 @@ __device__ __forceinline__ unsigned long long ask(const unsigned long long* p) {
   return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
 
-// Words: a ticket counter, then [tiles][channels] pairs and [groups][channels] states of every sequence.
+// Words: the columns' ticket counters, then [tiles][channels] pairs and [groups][channels] states of every sequence.
 struct Board {
-  unsigned* ticket;
+  unsigned* tickets;
   unsigned long long *pairs, *states;
 };
-// Two boards, one behind the other; `second`: where that starts (and its ticket counter is), or the end. Words in twos.
+// Two boards, one behind the other, each with its tickets' words first; words in twos.
 constexpr int kClearThreads = 256;
-__global__ __launch_bounds__(kClearThreads) void clear_board(ulonglong2* p, long long second, long long words) {
-  const long long k = wide_block() * kClearThreads + threadIdx.x;
-  if (2 * k < words) p[k] = make_ulonglong2(k == 0 || 2 * k == second ? 0ull : kNotYet, kNotYet);
+__global__ __launch_bounds__(kClearThreads) void clear_board(ulonglong2* p, long long tickets, long long second, long long tickets2,
+                                                             long long words) {
+  const long long k = wide_block() * kClearThreads + threadIdx.x, at = 2 * k;
+  const bool ticket = at < tickets || (at >= second && at < second + tickets2);
+  const unsigned long long v = ticket ? 0ull : kNotYet;
+  if (at < words) p[k] = make_ulonglong2(v, v);
 }
 
-// Tile `tile` of column `column` of sequence b. Ids go through the columns first.
+// A workgroup's tile: its column goes by its number, its place there by a ticket of the column's, drawn in the order in which workgroups
+// start. A tile waits for tiles of smaller tickets alone: they have started and wait for still smaller ones, so that every wait
+// ends. (A counter for each column, in a line of its own: from one for all, hundreds of workgroups at once take 4 us.)
+constexpr int kTicketWords = 16;
 struct Tile {
   int tile, b, column;
-  __device__ __forceinline__ Tile(unsigned id, int columns, int B) {
-    tile = (int)(id / (unsigned)(columns * B));
-    const int rest = (int)(id - (unsigned)tile * (unsigned)(columns * B));
-    b = rest / columns, column = rest - b * columns;
-  }
 };
-
-// A workgroup's tile. Tickets are drawn in the order in which workgroups start, and a tile waits for tiles of smaller tickets alone: they
-// have started and wait for still smaller ones, so that every wait ends.
-__device__ __forceinline__ unsigned draw(const Board& board, int tiles) {
-  if (tiles == 1) return (unsigned)wide_block();
-  __shared__ unsigned drawn;
-  if (threadIdx.x == 0) drawn = atomicAdd(board.ticket, 1u);
-  __syncthreads();
-  return __builtin_amdgcn_readfirstlane(drawn);
+// False where there is no tile for this workgroup.
+__device__ __forceinline__ bool draw(const Board& board, int tiles, int columns, unsigned total, Tile& k) {
+  const unsigned id = (unsigned)wide_block();
+  if (id >= total) return false;
+  const unsigned all = total / (unsigned)tiles;  // columns of all sequences
+  const unsigned of = id % all;
+  k.b = (int)(of / (unsigned)columns), k.column = (int)(of - (unsigned)k.b * (unsigned)columns);
+  k.tile = 0;
+  if (tiles > 1) {
+    __shared__ unsigned drawn;
+    if (threadIdx.x == 0) drawn = atomicAdd(board.tickets + (long long)of * (2 * kTicketWords), 1u);
+    __syncthreads();
+    k.tile = __builtin_amdgcn_readfirstlane(drawn);
+  }
+  return true;
 }
 
 // K times V neighbouring words, `step` apart, the first `count` of them asked for until they have come: all at once, and again only
@@ -203,9 +210,8 @@ template <class T, int W, int V, int TW>
 __global__ __launch_bounds__(64 * W) void recurrence_fwd(RecurrenceArgs a, int tiles, int columns, unsigned total, Board board) {
   constexpr int TILE = TW * W, CH = 64 * V;
   __shared__ Desk<W, CH> desk;
-  const unsigned id = draw(board, tiles);
-  if (id >= total) return;
-  const Tile k(id, columns, a.B);
+  Tile k;
+  if (!draw(board, tiles, columns, total, k)) return;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, C = a.C, N = a.N;
   const int wide = columns * CH, rows = (N + kKept - 1) / kKept;
   const int c0 = k.column * CH + lane * V, c = min(c0, C - V);  // (past the last channel: the last ones again)
@@ -221,6 +227,8 @@ __global__ __launch_bounds__(64 * W) void recurrence_fwd(RecurrenceArgs a, int t
       for (int t = 0; t < min(TW, inside); ++t) Pair<T, V>::store(py, off, o), py += C;
     return;
   }
+  float kk[V];  // (first: loads come back in order)
+  for (int i = 0; i < V; ++i) kk[i] = a.lam[c + i];
   Pair<T, V> x[TW], r[TW], g[TW];
   const int from = min(t0, N - 1);  // (past the last token: the last again)
   const T *px = (const T*)a.x + ((long long)k.b * N + from) * a.xs, *pr = (const T*)a.r + ((long long)k.b * N + from) * a.rs;
@@ -230,9 +238,8 @@ __global__ __launch_bounds__(64 * W) void recurrence_fwd(RecurrenceArgs a, int t
     x[t].load(px, off), r[t].load(pr, off), g[t].load(pi, off);
     if (t + 1 < inside) px += a.xs, pr += a.rs, pi += a.is;
   }
-  float kk[V];
   bool far = false;
-  for (int i = 0; i < V; ++i) kk[i] = a.scale * softplus(a.lam[c + i]), far = far || kk[i] > kSmall;
+  for (int i = 0; i < V; ++i) kk[i] = a.scale * softplus(kk[i]), far = far || kk[i] > kSmall;
   // (Of a run without padding and steep decays the tokens are one straight piece of code.)
   const bool steep = uniform(__any(far)), plain = uniform(live >= TW && !steep);
   float A[V], e[V], av[TW][V], bv[TW][V];
@@ -355,9 +362,8 @@ __global__ __launch_bounds__(64 * W) void recurrence_bwd(RecurrenceArgs a, int t
   constexpr int TILE = TW * W, CH = 64 * V;
   __shared__ DeskBack<W, CH> desk;
   static_assert(TILE % kKept == 0, "a tile starts at a kept state");
-  const unsigned id = draw(board, tiles);
-  if (id >= total) return;
-  Tile k(id, columns, a.B);
+  Tile k;
+  if (!draw(board, tiles, columns, total, k)) return;
   k.tile = tiles - 1 - k.tile;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, C = a.C, N = a.N;
   const int wide = columns * CH, rows = (N + kKept - 1) / kKept;
@@ -379,6 +385,11 @@ __global__ __launch_bounds__(64 * W) void recurrence_bwd(RecurrenceArgs a, int t
       for (int i = 0; i < V; ++i) sums[((long long)k.b * tiles + k.tile) * C + c + i] = 0.f;
     return;
   }
+  float h[V], kk[V];  // (first: loads come back in order)
+  for (int i = 0; i < V; ++i) {
+    kk[i] = a.lam[c + i];
+    h[i] = a.kept[((long long)k.b * rows + k.tile * TILE / kKept) * C + c + i];
+  }
   Pair<T, V> x[TW], r[TW], g[TW], dy[TW];
   const long long from = (long long)k.b * N + min(t0, N - 1);  // (past the last token: the last again)
   const T *px = (const T*)a.x + from * a.xs, *pr = (const T*)a.r + from * a.rs, *pi = (const T*)a.i + from * a.is;
@@ -388,12 +399,8 @@ __global__ __launch_bounds__(64 * W) void recurrence_bwd(RecurrenceArgs a, int t
     x[t].load(px, off), r[t].load(pr, off), g[t].load(pi, off), dy[t].load(pd, off);
     if (t + 1 < inside) px += a.xs, pr += a.rs, pi += a.is, pd += C;
   }
-  float h[V], kk[V];
   bool far = false;
-  for (int i = 0; i < V; ++i) {
-    kk[i] = a.scale * softplus(a.lam[c + i]), far = far || kk[i] > kSmall;
-    h[i] = a.kept[((long long)k.b * rows + k.tile * TILE / kKept) * C + c + i];
-  }
+  for (int i = 0; i < V; ++i) kk[i] = a.scale * softplus(kk[i]), far = far || kk[i] > kSmall;
   const bool steep = uniform(__any(far));
   // Of a token: a; m sigmoid(i); x (1 - sigmoid(i)); t / q, at first its second part; sigmoid(r).
   float av[TW][V], cx[TW][V], ci[TW][V], ct[TW][V], gr[TW][V];
@@ -537,17 +544,19 @@ struct StoreDecayGrad {
 
 dim3 grid_of(const RecurrenceArgs& a) { return dim3((unsigned)((a.C + kThreads - 1) / kThreads), (unsigned)a.B); }
 
-// How a pass is cut up: W waves a workgroup, V channels a lane and TW tokens, tiles of a sequence, columns; the board's words, a
-// ticket's row of 16 first, none where a sequence is one tile.
+// How a pass is cut up: W waves a workgroup, V channels a lane and TW tokens, tiles of a sequence, columns; the board's words, the
+// tickets' among them, none where a sequence is one tile.
 struct Plan {
   int W, V, TW, tiles, columns;
-  long long words;
+  long long words, tickets;
   long long workgroups(int B) const { return (long long)B * tiles * columns; }
 };
 Plan cut(int B, int N, int C, int W, int V, int TW) {
-  Plan p{W, V, TW, (N + TW * W - 1) / (TW * W), (C + 64 * V - 1) / (64 * V), 0};
-  const long long row = (long long)B * p.columns * 64 * V;
-  p.words = p.tiles == 1 ? 0 : 16 + row * (p.tiles + (p.tiles + kGroup - 1) / kGroup);
+  Plan p{W, V, TW, (N + TW * W - 1) / (TW * W), (C + 64 * V - 1) / (64 * V), 0, 0};
+  if (p.tiles == 1) return p;
+  const long long columns = (long long)B * p.columns;
+  p.tickets = columns * kTicketWords;
+  p.words = p.tickets + columns * 64 * V * (p.tiles + (p.tiles + kGroup - 1) / kGroup);
   return p;
 }
 // Two channels a lane where that gives each CU a workgroup: a wave then moves 256 bytes (bf16) at a time and joins half as many pairs;
@@ -563,13 +572,15 @@ Plan plan_of(int B, int N, int C, bool pairs, bool backward) {
 }
 
 Board board_of(const Plan& p, int B, unsigned long long* w) {
-  return Board{reinterpret_cast<unsigned*>(w), w + 16, w + 16 + (long long)B * p.columns * 64 * p.V * p.tiles};
+  unsigned long long* pairs = w + p.tickets;
+  return Board{reinterpret_cast<unsigned*>(w), pairs, pairs + (long long)B * p.columns * 64 * p.V * p.tiles};
 }
 
-hipError_t clear(unsigned long long* w, long long one, long long two, hipStream_t st) {
-  if (one + two == 0) return hipSuccess;
-  hipLaunchKernelGGL(clear_board, wide_grid((one + two + 2 * kClearThreads - 1) / (2 * kClearThreads)), dim3(kClearThreads), 0, st,
-                     reinterpret_cast<ulonglong2*>(w), one, one + two);
+hipError_t clear(unsigned long long* w, const Plan& one, const Plan* two, hipStream_t st) {
+  const long long words = one.words + (two ? two->words : 0);
+  if (words == 0) return hipSuccess;
+  hipLaunchKernelGGL(clear_board, wide_grid((words + 2 * kClearThreads - 1) / (2 * kClearThreads)), dim3(kClearThreads), 0, st,
+                     reinterpret_cast<ulonglong2*>(w), one.tickets, one.words, two ? two->tickets : 0, words);
   return hipGetLastError();
 }
 
@@ -632,7 +643,7 @@ template <class T>
 hipError_t forward_call(const RecurrenceArgs& a, void* ws, hipStream_t st) {
   const Plan p = plan_of<T>(a.B, a.N, a.C, paired<T>(a), false);
   unsigned long long* w = static_cast<unsigned long long*>(ws);
-  const hipError_t e = clear(w, p.words, 0, st);
+  const hipError_t e = clear(w, p, nullptr, st);
   return e == hipSuccess ? run_forward<T>(a, p, w, st) : e;
 }
 
@@ -643,7 +654,7 @@ hipError_t backward_call(RecurrenceArgs a, void* ws, hipStream_t st) {
   const Plan p = plan_of<T>(a.B, a.N, a.C, pairs, true), q = plan_of<T>(a.B, a.N, a.C, pairs, false);
   unsigned long long* w = static_cast<unsigned long long*>(ws);
   float* sums = reinterpret_cast<float*>(static_cast<char*>(ws) + l.sums);
-  hipError_t e = clear(w, p.words, kept ? 0 : q.words, st);
+  hipError_t e = clear(w, p, kept ? nullptr : &q, st);
   if (e != hipSuccess) return e;
   if (!kept) {  // the forward pass again, for its states alone
     a.states = reinterpret_cast<float*>(static_cast<char*>(ws) + l.states);
