@@ -247,8 +247,7 @@ __global__ __launch_bounds__(64 * W) void recurrence_fwd(RecurrenceArgs a, int t
   auto all = [&](auto plain) {
 #pragma unroll
     for (int t = 0; t < TW; ++t) {
-      for (int i = 0; i < V; ++i) av[t][i] = 1.f, bv[t][i] = 0.f;
-      if (plain.value || t < live)
+      if (plain.value || t < live) {
         for (int i = 0; i < V; ++i) {
           const Gates q(r[t].get(i), g[t].get(i), kk[i], !plain.value && steep);
           av[t][i] = q.a;
@@ -256,6 +255,9 @@ __global__ __launch_bounds__(64 * W) void recurrence_fwd(RecurrenceArgs a, int t
           A[i] *= av[t][i];
           e[i] = fmaf(av[t][i], e[i], bv[t][i]);
         }
+      } else {
+        for (int i = 0; i < V; ++i) av[t][i] = 1.f, bv[t][i] = 0.f;
+      }
     }
   };
   if (plain) all(std::true_type{});
@@ -402,26 +404,28 @@ __global__ __launch_bounds__(64 * W) void recurrence_bwd(RecurrenceArgs a, int t
   bool far = false;
   for (int i = 0; i < V; ++i) kk[i] = a.scale * softplus(kk[i]), far = far || kk[i] > kSmall;
   const bool steep = uniform(__any(far));
-  // Of a token: a; m sigmoid(i); x (1 - sigmoid(i)); t / q, at first its second part; sigmoid(r).
+  // Of a token: a; m sigmoid(i); x (1 - sigmoid(i)); t / q = a la (h - (a / m) sigmoid(i) x), at first what is taken from h; sigmoid(r).
   float av[TW][V], cx[TW][V], ci[TW][V], ct[TW][V], gr[TW][V];
   float A[V], e[V], z[V];
   for (int i = 0; i < V; ++i) A[i] = 1.f, e[i] = z[i] = 0.f;
 #pragma unroll
   for (int t = 0; t < TW; ++t) {
-    for (int i = 0; i < V; ++i) av[t][i] = 1.f, cx[t][i] = ci[t][i] = ct[t][i] = gr[t][i] = 0.f;
-    if (t < live)
+    if (t < live) {
       for (int i = 0; i < V; ++i) {
         const Gates q(r[t].get(i), g[t].get(i), kk[i], steep);
         const float inv = q.w < 0x1p-126f ? 0.f : __builtin_amdgcn_rsqf(q.w);  // 1 / m; (m = 0 below the root's range)
-        const float xv = x[t].get(i);
+        const float xv = x[t].get(i), m = q.w * inv, drive = q.gi * xv;
         av[t][i] = q.a;
-        cx[t][i] = q.w * inv * q.gi;
+        cx[t][i] = m * q.gi;
         ci[t][i] = xv * (1.f - q.gi);
-        ct[t][i] = q.a * q.a * (q.la * inv) * (q.gi * xv);
+        ct[t][i] = q.a * inv * drive;
         gr[t][i] = q.gr;
         A[i] *= q.a;
-        e[i] = fmaf(q.a, e[i], cx[t][i] * xv);
+        e[i] = fmaf(q.a, e[i], m * drive);
       }
+    } else {
+      for (int i = 0; i < V; ++i) av[t][i] = 1.f, cx[t][i] = ci[t][i] = ct[t][i] = gr[t][i] = 0.f;
+    }
   }
 #pragma unroll
   for (int t = TW - 1; t >= 0; --t)
@@ -464,7 +468,7 @@ __global__ __launch_bounds__(64 * W) void recurrence_bwd(RecurrenceArgs a, int t
 #pragma unroll
   for (int t = 0; t < TW; ++t)
     for (int i = 0; i < V; ++i) {
-      ct[t][i] = av[t][i] * (-kk[i] * gr[t][i]) * h[i] - ct[t][i];
+      ct[t][i] = av[t][i] * (-kk[i] * gr[t][i]) * (h[i] - ct[t][i]);
       h[i] = fmaf(av[t][i], h[i], t < live ? cx[t][i] * x[t].get(i) : 0.f);
     }
   constexpr int EACH = kGroup / W;
