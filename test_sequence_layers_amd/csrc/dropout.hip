@@ -29,6 +29,16 @@ struct Eight {
 #pragma unroll
     for (int i = 0; i < N; ++i) Piece<T>::store(p + i * kPiece<T>, v + i * kPiece<T>);
   }
+  // The last `count`, of 1 .. 7, to p.
+  static __device__ __forceinline__ void store_last(T* p, const float* v, int count) {
+    if constexpr (N == 1) {
+      Piece<T>::store_last(p, v, count);
+    } else {
+#pragma unroll
+      for (int j = 1; j < 8; ++j)
+        if (j >= 8 - count) p[count - 8 + j] = v[j];
+    }
+  }
 };
 
 // `per`: counters of a row.
@@ -45,36 +55,33 @@ __global__ __launch_bounds__(kThreads) void dropout(const T* x, long long xs, co
     piece = (unsigned)(id - row * per);
     from = row * xs + (long long)piece * 8, at = row * C + (long long)piece * 8;
   }
+  // The end of a row of another width is taken with its last 8 elements, where it has as many: the first `skip` are the counter's before.
   const int rest = C % 8;
   const bool whole = rest == 0 || piece < per - 1;
+  const int skip = whole ? 0 : 8 - rest;
   float v[8] = {}, r[8] = {};
   Eight<T> px, pr;
-  if (whole) {
-    px.load(x + from);
-    if (ADD) pr.load(res + at);
+  if (C >= 8) {
+    px.load(x + from - skip);
+    if (ADD) pr.load(res + at - skip);
   } else {
 #pragma unroll
-    for (int j = 0; j < 7; ++j)
-      if (j < rest) {
-        v[j] = (float)x[from + j];
-        if (ADD) r[j] = (float)res[at + j];
+    for (int j = 1; j < 8; ++j)
+      if (j >= skip) {
+        v[j] = (float)x[from - skip + j];
+        if (ADD) r[j] = (float)res[at - skip + j];
       }
   }
-  Random8 u{};
-  if (d.least) u = random8(d.rng[0], d.rng[1] + (unsigned long long)id);
-  if (whole) {
+  uint32_t kept = 0xff;
+  if (d.least) kept = random8(d.rng[0], d.rng[1] + (unsigned long long)id).mask(d.least) << skip;
+  if (C >= 8) {
     px.widen(v);
     if (ADD) pr.widen(r);
   }
 #pragma unroll
-  for (int j = 0; j < 8; ++j) v[j] = (u.kept(j, d.least) ? v[j] * d.scale : 0.f) + r[j];
-  if (whole) {
-    Eight<T>::store(y + at, v);
-  } else {
-#pragma unroll
-    for (int j = 0; j < 7; ++j)
-      if (j < rest) y[at + j] = (T)v[j];
-  }
+  for (int j = 0; j < 8; ++j) v[j] = ((kept >> j) & 1 ? v[j] * d.scale : 0.f) + r[j];
+  if (whole) Eight<T>::store(y + at, v);
+  else Eight<T>::store_last(y + at, v, rest);
 }
 
 template <class T, bool ADD>

@@ -16,32 +16,32 @@
 namespace ttt {
 namespace {
 
-// Where a row's D elements are over L lanes: piece k L + lane of access k. With TAIL the last is a part of one: it is read as the
-// last whole piece of the row, over the one before it, in the same access as the others, and moved to the front when it is used (where
-// a row is less than a piece, element by element). Without, D is a multiple of V.
-template <int L, int V, bool TAIL>
+// Where a row's D elements are over L lanes: piece k L + lane of access k. Where D is no multiple of V, the last piece, in access PART,
+// is a part of one: its lane has the row's last V elements, in an access like the others, of which the first `skip` are the piece's
+// before it and count as none here (where a row is less than a piece, there are none). PART is -1 where there is no such piece.
+template <int L, int V, int PART>
 struct Spread {
-  int lane, D, whole, rest;  // whole pieces; elements behind them
-  __device__ __forceinline__ Spread(int lane, int D) : lane(lane), D(D), whole(D / V), rest(D % V) {}
-  __device__ __forceinline__ bool full(int k) const { return k * L + lane < whole; }
-  __device__ __forceinline__ bool any(int k) const { return TAIL ? (k * L + lane) * V < D : full(k); }
-  __device__ __forceinline__ bool has_part(int k) const { return TAIL && whole / L == k; }  // (the same for all lanes)
-  __device__ __forceinline__ bool part() const { return lane == whole % L; }
-  // Where to read access k's piece; past the row its first.
-  __device__ __forceinline__ int from(int k) const {
-    const int at = (k * L + lane) * V;
-    return full(k) ? at : TAIL && any(k) ? D - V : 0;
-  }
+  static constexpr bool kTail = PART >= 0;
+  int lane, D, whole, rest, skip;  // whole pieces; elements behind them
+  __device__ __forceinline__ Spread(int lane, int D)
+      : lane(lane), D(D), whole(D / V), rest(D % V), skip(kTail && lane == whole % L ? V - rest : 0) {}
+  static constexpr __device__ bool has_part(int k) { return k == PART; }
+  __device__ __forceinline__ bool full(int k) const { return kTail && k != PART ? k < PART : k * L + lane < whole; }
+  __device__ __forceinline__ bool any(int k) const { return has_part(k) ? (k * L + lane) * V < D : full(k); }
+  __device__ __forceinline__ bool part(int k) const { return has_part(k) && skip > 0; }
+  __device__ __forceinline__ bool holds(int k, int i) const { return any(k) && (!has_part(k) || i >= skip); }
+  // The channel of access k's first element; past the row its first.
+  __device__ __forceinline__ int from(int k) const { return full(k) ? (k * L + lane) * V : any(k) ? D - V : 0; }
 };
 
-template <class T, int L, int K, bool TAIL>
+template <class T, int L, int K, int PART>
 struct AnyRow {
   static constexpr int V = kPiece<T>;
-  typedef Spread<L, V, TAIL> S;
+  typedef Spread<L, V, PART> S;
   Piece<T> r[K];
   __device__ __forceinline__ void load(const T* p, const S& s) {
-    if (TAIL && s.whole == 0) {
-      if (s.lane == 0) r[0].load_some(p, s.rest);
+    if (PART == 0 && s.whole == 0) {
+      if (s.lane == 0) r[0].load_last(p, s.rest);
       return;
     }
 #pragma unroll
@@ -50,41 +50,34 @@ struct AnyRow {
   __device__ __forceinline__ void widen(float* v, const S& s, bool in = true) const {
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-      Piece<T> q = r[k];
-      if (s.has_part(k) && s.whole > 0) {
-        q.keep_last(s.rest);
-        if (!s.part()) q = r[k];
-      }
-      q.widen(v + k * V);
-      const bool ok = in && s.any(k);
-      for (int i = 0; i < V; ++i) v[k * V + i] = ok ? v[k * V + i] : 0.f;
+      r[k].widen(v + k * V);
+      for (int i = 0; i < V; ++i) v[k * V + i] = in && s.holds(k, i) ? v[k * V + i] : 0.f;
     }
   }
   static __device__ __forceinline__ void store(T* p, const float* v, const S& s) {
 #pragma unroll
     for (int k = 0; k < K; ++k) {
       if (s.full(k)) Piece<T>::store(p + (k * L + s.lane) * V, v + k * V);
-      if (s.has_part(k) && s.part()) Piece<T>::store_some(p + s.whole * V, v + k * V, s.rest);
+      if (s.part(k)) Piece<T>::store_last(p + s.whole * V, v + k * V, s.rest);
     }
   }
 };
 
-// The fp32 weights of a row's elements; past the row's end the last.
-template <int L, int K, int V, bool TAIL>
-__device__ __forceinline__ void load_weights(const float* w, float* out, const Spread<L, V, TAIL>& s) {
+// The fp32 weights of a row's elements.
+template <int L, int K, int V, int PART>
+__device__ __forceinline__ void load_weights(const float* w, float* out, const Spread<L, V, PART>& s) {
+  if (PART == 0 && s.whole == 0) {
 #pragma unroll
-  for (int k = 0; k < K; ++k) {
-    if (s.has_part(k)) {
-      for (int i = 0; i < V; ++i) out[k * V + i] = w[min((k * L + s.lane) * V + i, s.D - 1)];
-    } else {
-#pragma unroll
-      for (int i = 0; i < V; i += 4) {
-        Piece<float> q;
-        q.load(w + (s.full(k) ? (k * L + s.lane) * V : 0) + i);
-        q.widen(out + k * V + i);
-      }
-    }
+    for (int i = 0; i < V; ++i) out[i] = s.holds(0, i) ? w[s.from(0) + i] : 0.f;
+    return;
   }
+#pragma unroll
+  for (int k = 0; k < K; ++k)
+    for (int i = 0; i < V; i += 4) {
+      Piece<float> q;
+      q.load(w + s.from(k) + i);
+      q.widen(out + k * V + i);
+    }
 }
 
 // rstd of a row, times *back; v is scaled by 1 / *back where its squares overflow (from 2^60 or so on: the largest squares
@@ -114,10 +107,13 @@ __device__ __forceinline__ float inverse_rms(float* v, int D, float eps, float (
 }
 
 // v -> v keep scale.
-template <int L, int K, int V, bool TAIL>
-__device__ __forceinline__ void drop_row(float* v, const Drop& d, long long row, const Spread<L, V, TAIL>& s) {
+template <int L, int K, int V, int PART>
+__device__ __forceinline__ void drop_row(float* v, const Drop& d, long long row, const Spread<L, V, PART>& s) {
   RowMask<L, K, V> m;
   m.make(d.rng[0], d.rng[1] + (unsigned long long)row * (unsigned)((s.D + 7) / 8), d.least, s.lane);
+#pragma unroll
+  for (int k = 0; k < K; ++k)
+    if (s.has_part(k)) m.bits[k] <<= s.skip;
 #pragma unroll
   for (int k = 0; k < K; ++k)
     for (int i = 0; i < V; ++i) v[k * V + i] = m.kept(k, i) ? v[k * V + i] * d.scale : 0.f;
@@ -152,9 +148,10 @@ __device__ __forceinline__ uint32_t to_e4m3(const float* v) {
   const int r = __builtin_amdgcn_cvt_pk_fp8_f32(v[0], v[1], 0, false);
   return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(v[2], v[3], r, true);
 }
-template <int K, int L, int V, bool TAIL>
-__device__ __forceinline__ void store_e4m3(uint8_t* p, const float* v, const Spread<L, V, TAIL>& s) {
+template <int K, int L, int V, int PART>
+__device__ __forceinline__ void store_e4m3(uint8_t* p, const float* v, const Spread<L, V, PART>& s) {
   typedef uint32_t Any __attribute__((aligned(1)));
+  typedef uint16_t HalfWord __attribute__((aligned(1)));
 #pragma unroll
   for (int k = 0; k < K; ++k) {
     uint32_t q[V / 4];
@@ -164,10 +161,13 @@ __device__ __forceinline__ void store_e4m3(uint8_t* p, const float* v, const Spr
 #pragma unroll
       for (int i = 0; i < V / 4; ++i) reinterpret_cast<Any*>(p + (k * L + s.lane) * V)[i] = q[i];
     }
-    if (s.has_part(k) && s.part()) {
-#pragma unroll
-      for (int i = 0; i < V - 1; ++i)
-        if (i < s.rest) p[s.whole * V + i] = (uint8_t)(q[i / 4] >> (8 * (i & 3)));
+    if (s.part(k)) {
+      uint8_t* to = p + s.whole * V;
+      uint64_t last = (V == 8 ? (uint64_t)q[V / 4 - 1] << 32 : 0) | q[0];
+      last >>= 8 * s.skip;
+      if (s.rest & 4) *reinterpret_cast<Any*>(to) = (uint32_t)last, to += 4, last >>= 32;
+      if (s.rest & 2) *reinterpret_cast<HalfWord*>(to) = (uint16_t)last, to += 2, last >>= 16;
+      if (s.rest & 1) *to = (uint8_t)last;
     }
   }
 }
@@ -175,18 +175,18 @@ __device__ __forceinline__ void store_e4m3(uint8_t* p, const float* v, const Spr
 constexpr float kE4m3Most = 448.f;
 constexpr float kLeastMax = 0x1p-100f;  // a smaller maximum's inverse could be infinite; such values are zeros in 8 bits
 
-template <class T, int L, int K, bool TAIL, bool ADD, bool E4M3>
+template <class T, int L, int K, int PART, bool ADD, bool E4M3>
 __global__ __launch_bounds__(threads_of<L>) void rmsnorm_fwd(const T* __restrict__ x, long long xs, const T* res,
                                                              const float* __restrict__ w, T* sum, void* __restrict__ y,
                                                              float* __restrict__ scales, int rows, int H, int D,
                                                              int group, float eps, Drop drop) {
   constexpr int V = kPiece<T>;
   __shared__ float red[2][16];
-  const Spread<L, V, TAIL> s(threadIdx.x % L, D);
+  const Spread<L, V, PART> s(threadIdx.x % L, D);
   const long long row = wide_block() * (threads_of<L> / L) + threadIdx.x / L;
   if (row >= rows) return;  // (whole groups; for L > 64 the whole workgroup)
   const int m = (int)(row / H), h = (int)(row - (long long)m * H);
-  AnyRow<T, L, K, TAIL> rx, rr;
+  AnyRow<T, L, K, PART> rx, rr;
   rx.load(x + (long long)m * xs + (long long)h * D, s);
   if (ADD) rr.load(res + row * D, s);
   float v[K * V], wv[K * V];
@@ -197,7 +197,7 @@ __global__ __launch_bounds__(threads_of<L>) void rmsnorm_fwd(const T* __restrict
     rr.widen(r, s);
 #pragma unroll
     for (int j = 0; j < K * V; ++j) v[j] += r[j];
-    AnyRow<T, L, K, TAIL>::store(sum + row * D, v, s);
+    AnyRow<T, L, K, PART>::store(sum + row * D, v, s);
   }
   load_weights<L, K>(w + (long long)h * D, wv, s);
   float back;
@@ -205,7 +205,7 @@ __global__ __launch_bounds__(threads_of<L>) void rmsnorm_fwd(const T* __restrict
   if constexpr (!E4M3) {
 #pragma unroll
     for (int j = 0; j < K * V; ++j) v[j] *= rstd * wv[j];
-    AnyRow<T, L, K, TAIL>::store((T*)y + row * D, v, s);
+    AnyRow<T, L, K, PART>::store((T*)y + row * D, v, s);
   } else {
     // rstd is not in y / scale: of v w, its maximum M over the group and 448 / M, the first and the last as two numbers
     // each, so that the rounding to 8 bits has but one other before it. Maxima of the absolute values' bits: as numbers they are in the
@@ -219,7 +219,7 @@ __global__ __launch_bounds__(threads_of<L>) void rmsnorm_fwd(const T* __restrict
         const int j = k * V + i;
         const float t = v[j] * wv[j];
         low[j] = fmaf(v[j], wv[j], -t);
-        v[j] = (TAIL ? (k * L + s.lane) * V + i < D : s.full(k)) ? t : 0.f;
+        v[j] = s.holds(k, i) ? t : 0.f;
         most[k] = max(most[k], __float_as_uint(v[j]) & 0x7fffffffu);
       }
       all = max(all, most[k]);
@@ -259,7 +259,7 @@ __global__ __launch_bounds__(threads_of<L>) void rmsnorm_fwd(const T* __restrict
 }
 
 // Workgroup (bx, by): as in layer norm's backward pass, R tokens at a time of the HB heads from by HB on. Partial row bx: dw (H D).
-template <class T, int L, int K, bool TAIL, bool ADD>
+template <class T, int L, int K, int PART, bool ADD>
 __global__ __launch_bounds__(bwd_threads(L, K* kPiece<T>)) void rmsnorm_bwd(const T* __restrict__ sum, long long ss,
                                                                             const float* __restrict__ w,
                                                                             const T* __restrict__ dy, const T* dsum, T* ds,
@@ -271,13 +271,13 @@ __global__ __launch_bounds__(bwd_threads(L, K* kPiece<T>)) void rmsnorm_bwd(cons
   __shared__ float red[4][16];
   __shared__ float join[L <= 64 ? bwd_threads(L, K * V) * K * V : 1];
   const int g = threadIdx.x / L;
-  const Spread<L, V, TAIL> s(threadIdx.x % L, D);
+  const Spread<L, V, PART> s(threadIdx.x % L, D);
   const int r = g / HB, hg = blockIdx.y * HB + g % HB, h = min(hg, H - 1);
   const bool live = r < R && hg < H;
   const float inv_d = rcp_hw((float)D);
   float wv[K * V], aw[K * V] = {};
   if (kRoom) load_weights<L, K>(w + (long long)h * D, wv, s);
-  AnyRow<T, L, K, TAIL> rx, rd, rr;
+  AnyRow<T, L, K, PART> rx, rd, rr;
   auto fetch = [&](long long m) {  // (past the last token: the last again)
     const long long t = m < M ? m : M - 1;
     rx.load(sum + t * ss + (long long)h * D, s);
@@ -311,10 +311,10 @@ __global__ __launch_bounds__(bwd_threads(L, K* kPiece<T>)) void rmsnorm_bwd(cons
 #pragma unroll
     for (int j = 0; j < K * V; ++j) d[j] = outer * (d[j] - v[j] * s2) + (ADD ? e[j] : 0.f);
     const long long o = (m * H + h) * D;
-    if (in) AnyRow<T, L, K, TAIL>::store(ds + o, d, s);
+    if (in) AnyRow<T, L, K, PART>::store(ds + o, d, s);
     if (dx) {
       if (drop.least) drop_row<L, K>(d, drop, m, s);
-      if (in) AnyRow<T, L, K, TAIL>::store(dx + o, d, s);
+      if (in) AnyRow<T, L, K, PART>::store(dx + o, d, s);
     }
   }
   const long long W = (long long)H * D;
@@ -323,14 +323,14 @@ __global__ __launch_bounds__(bwd_threads(L, K* kPiece<T>)) void rmsnorm_bwd(cons
 #pragma unroll
     for (int k = 0; k < K; ++k)
       for (int i = 0; i < V; ++i) {
-        const int at = (k * L + s.lane) * V + i;
-        if (at < D) row[(long long)h * D + at] = aw[k * V + i];
+        if (s.holds(k, i)) row[(long long)h * D + s.from(k) + i] = aw[k * V + i];
       }
   } else {
     __syncthreads();
 #pragma unroll
     for (int k = 0; k < K; ++k)
-      for (int i = 0; i < V; ++i) join[g * LKV + (k * L + s.lane) * V + i] = aw[k * V + i];
+      for (int i = 0; i < V; ++i)
+        if (s.holds(k, i)) join[g * LKV + s.from(k) + i] = aw[k * V + i];
     __syncthreads();
     for (int t = threadIdx.x; t < HB * D; t += blockDim.x) {
       const int hh = t / D, at = t - hh * D;
@@ -347,23 +347,33 @@ struct StoreWeightGrad {
   __device__ void operator()(int col, float s) const { dw[col] = s; }
 };
 
+// Calls f with the access that has a part of a piece; of as many lanes' accesses as shape_of takes it is the last, of four one of two.
+template <int L, int K, int V, class F>
+hipError_t by_part(int D, const F& f) {
+  if (D % V == 0) return f(std::integral_constant<int, -1>{});
+  if constexpr (K == 4) {
+    if (D / V / L == 2) return f(std::integral_constant<int, 2>{});
+  }
+  return D / V / L == K - 1 ? f(std::integral_constant<int, K - 1>{}) : hipErrorInvalidValue;
+}
+
 struct FwdCall {
   const RmsNormArgs& a;
   hipStream_t st;
   template <class T, int L, int K, int V>
   hipError_t run() const {
-    return a.D % V ? some<T, L, K, true>() : some<T, L, K, false>();
+    return by_part<L, K, V>(a.D, [&](auto part) { return some<T, L, K, part.value>(); });
   }
-  template <class T, int L, int K, bool TAIL>
+  template <class T, int L, int K, int PART>
   hipError_t some() const {
-    return a.scales ? (a.residual ? go<T, L, K, TAIL, true, true>() : go<T, L, K, TAIL, false, true>())
-                    : (a.residual ? go<T, L, K, TAIL, true, false>() : go<T, L, K, TAIL, false, false>());
+    return a.scales ? (a.residual ? go<T, L, K, PART, true, true>() : go<T, L, K, PART, false, true>())
+                    : (a.residual ? go<T, L, K, PART, true, false>() : go<T, L, K, PART, false, false>());
   }
-  template <class T, int L, int K, bool TAIL, bool ADD, bool E4M3>
+  template <class T, int L, int K, int PART, bool ADD, bool E4M3>
   hipError_t go() const {
     constexpr int G = threads_of<L> / L;
     const int rows = a.M * a.H;
-    hipLaunchKernelGGL((rmsnorm_fwd<T, L, K, TAIL, ADD, E4M3>), wide_grid(((long long)rows + G - 1) / G), dim3(threads_of<L>), 0,
+    hipLaunchKernelGGL((rmsnorm_fwd<T, L, K, PART, ADD, E4M3>), wide_grid(((long long)rows + G - 1) / G), dim3(threads_of<L>), 0,
                        st, (const T*)a.x, a.xs, (const T*)a.residual, a.w, (T*)a.sum, a.y, a.scales, rows, a.H, a.D,
                        a.group, a.eps, a.drop);
     return hipGetLastError();
@@ -376,13 +386,14 @@ struct BwdCall {
   hipStream_t st;
   template <class T, int L, int K, int V>
   hipError_t run() const {
-    return a.D % V ? (a.dsum ? go<T, L, K, true, true>() : go<T, L, K, true, false>())
-                   : (a.dsum ? go<T, L, K, false, true>() : go<T, L, K, false, false>());
+    return by_part<L, K, V>(a.D, [&](auto part) {
+      return a.dsum ? go<T, L, K, part.value, true>() : go<T, L, K, part.value, false>();
+    });
   }
-  template <class T, int L, int K, bool TAIL, bool ADD>
+  template <class T, int L, int K, int PART, bool ADD>
   hipError_t go() const {
     const int threads = L <= 64 ? (p.HB * p.R * L + 63) / 64 * 64 : L;
-    hipLaunchKernelGGL((rmsnorm_bwd<T, L, K, TAIL, ADD>), dim3((unsigned)p.P, (unsigned)p.gy), dim3(threads), 0, st,
+    hipLaunchKernelGGL((rmsnorm_bwd<T, L, K, PART, ADD>), dim3((unsigned)p.P, (unsigned)p.gy), dim3(threads), 0, st,
                        (const T*)a.x, a.xs, a.w, (const T*)a.dy, (const T*)a.dsum, (T*)a.ds, (T*)a.dx, a.partial, a.M,
                        a.H, a.D, p.HB, p.R, a.eps, a.drop);
     return hipGetLastError();
