@@ -7,7 +7,6 @@
 // with the root of la.
 //
 // A thread walks a channel of a sequence from end to end.
-#include <algorithm>
 #include <type_traits>
 
 #include "internal.hpp"
@@ -87,13 +86,14 @@ __device__ __forceinline__ uint32_t lane_part(int c, int size) {
   return off;
 }
 
-// V neighbouring channels of one token as they are loaded (V = 2: 4 or 8 bytes), and stores of them.
+// V neighbouring channels of one token as they are loaded (V = 2: 4 or 8 bytes, at any alignment of the elements), and stores of them.
 template <class T, int V>
 struct Pair {
   typedef typename std::conditional<sizeof(T) * V == 8, uint2, typename std::conditional<sizeof(T) * V == 4, uint32_t, uint16_t>::type>::type Bits;
   Bits b;
   __device__ __forceinline__ void load(const T* row, uint32_t off) {
-    b = *reinterpret_cast<const Bits*>(reinterpret_cast<const char*>(row) + off);
+    typedef Bits Any __attribute__((aligned(sizeof(T))));
+    b = *reinterpret_cast<const Any*>(reinterpret_cast<const char*>(row) + off);
   }
   // To be looked at anew.
   __device__ __forceinline__ void hide() {
@@ -111,11 +111,13 @@ struct Pair {
     if constexpr (V == 1) {
       *reinterpret_cast<T*>(p) = (T)v[0];
     } else if constexpr (sizeof(T) == 4) {
-      *reinterpret_cast<float2*>(p) = make_float2(v[0], v[1]);
+      typedef uint2 Any __attribute__((aligned(4)));
+      *reinterpret_cast<Any*>(p) = make_uint2(__float_as_uint(v[0]), __float_as_uint(v[1]));
     } else {
+      typedef uint32_t Any __attribute__((aligned(2)));
       typedef __bf16 two __attribute__((ext_vector_type(2)));
       typedef float ftwo __attribute__((ext_vector_type(2)));
-      *reinterpret_cast<two*>(p) = __builtin_convertvector(ftwo{v[0], v[1]}, two);
+      *reinterpret_cast<Any*>(p) = __builtin_bit_cast(uint32_t, __builtin_convertvector(ftwo{v[0], v[1]}, two));
     }
   }
 };
@@ -214,7 +216,7 @@ __global__ __launch_bounds__(64 * W) void recurrence_fwd(RecurrenceArgs a, int t
   if (!draw(board, tiles, columns, total, k)) return;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, C = a.C, N = a.N;
   const int wide = columns * CH, rows = (N + kKept - 1) / kKept;
-  const int c0 = k.column * CH + lane * V, c = min(c0, C - V);  // (past the last channel: the last ones again)
+  const int c0 = k.column * CH + lane * V, c = min(c0, C - V);  // (past the last channel the last ones again: an odd last channel's lane has the one before it too, with the same results)
   const bool mine = c0 < C;
   const int n = length_of(a.lengths, k.b, N), t0 = k.tile * TILE + wave * TW;
   const int live = n - t0, inside = N - t0;  // tokens of this run and those behind it, of the sequence and of the padded one
@@ -369,7 +371,7 @@ __global__ __launch_bounds__(64 * W) void recurrence_bwd(RecurrenceArgs a, int t
   k.tile = tiles - 1 - k.tile;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, C = a.C, N = a.N;
   const int wide = columns * CH, rows = (N + kKept - 1) / kKept;
-  const int c0 = k.column * CH + lane * V, c = min(c0, C - V);  // (past the last channel: the last ones again)
+  const int c0 = k.column * CH + lane * V, c = min(c0, C - V);  // (past the last channel the last ones again: an odd last channel's lane has the one before it too, with the same results)
   const bool mine = c0 < C;
   const int n = length_of(a.lengths, k.b, N), t0 = k.tile * TILE + wave * TW;
   const int live = n - t0, inside = N - t0;  // tokens of this run and those behind it, of the sequence and of the padded one
@@ -568,11 +570,11 @@ Plan cut(int B, int N, int C, int W, int V, int TW) {
 // lose where a sequence has many, 2 x 1024 x 768 11 -> 19.) As many tokens a lane as registers hold.
 constexpr int kCus = 256;
 template <class T>
-Plan plan_of(int B, int N, int C, bool pairs, bool backward) {
+Plan plan_of(int B, int N, int C, bool backward) {
   constexpr bool kHalf = sizeof(T) == 2;
   const int W = backward && !kHalf ? 16 : 8, TW = backward ? (kHalf ? 8 : 4) : (kHalf ? 16 : 8);
   const Plan two = cut(B, N, C, W, 2, TW);
-  return pairs && two.workgroups(B) >= kCus ? two : cut(B, N, C, W, 1, TW);
+  return C > 1 && two.workgroups(B) >= kCus ? two : cut(B, N, C, W, 1, TW);
 }
 
 Board board_of(const Plan& p, int B, unsigned long long* w) {
@@ -586,15 +588,6 @@ hipError_t clear(unsigned long long* w, const Plan& one, const Plan* two, hipStr
   hipLaunchKernelGGL(clear_board, wide_grid((words + 2 * kClearThreads - 1) / (2 * kClearThreads)), dim3(kClearThreads), 0, st,
                      reinterpret_cast<ulonglong2*>(w), one.tickets, one.words, two ? two->tickets : 0, words);
   return hipGetLastError();
-}
-
-// Two channels an access need rows of pairs.
-template <class T>
-bool paired(const RecurrenceArgs& a) {
-  const uintptr_t at = reinterpret_cast<uintptr_t>(a.x) | reinterpret_cast<uintptr_t>(a.r) | reinterpret_cast<uintptr_t>(a.i) |
-                       reinterpret_cast<uintptr_t>(a.y) | reinterpret_cast<uintptr_t>(a.dy) | reinterpret_cast<uintptr_t>(a.dx) |
-                       reinterpret_cast<uintptr_t>(a.dr) | reinterpret_cast<uintptr_t>(a.di);
-  return ((a.C | a.xs | a.rs | a.is) & 1) == 0 && at % (2 * sizeof(T)) == 0;
 }
 
 template <class T, int W, int V, int TW>
@@ -626,7 +619,7 @@ hipError_t run_backward(const RecurrenceArgs& a, const Plan& p, unsigned long lo
 
 template <class T>
 size_t forward_bytes(int B, int N, int C) {
-  return (size_t)std::max(plan_of<T>(B, N, C, false, false).words, plan_of<T>(B, N, C, true, false).words) * 8;
+  return (size_t)plan_of<T>(B, N, C, false).words * 8;
 }
 
 // The backward pass's workspace: the boards of both passes, the tiles' sums, the states.
@@ -635,17 +628,17 @@ struct BackLayout {
 };
 template <class T>
 BackLayout back_layout(int B, int N, int C, bool kept) {
-  const long long board = std::max(plan_of<T>(B, N, C, false, true).words, plan_of<T>(B, N, C, true, true).words);
+  const Plan p = plan_of<T>(B, N, C, true);
   BackLayout l;
-  l.sums = round_up((size_t)board * 8 + (kept ? 0 : forward_bytes<T>(B, N, C)), 256);
-  l.states = l.sums + round_up((size_t)B * plan_of<T>(B, N, C, true, true).tiles * C * 4, 256);  // (all backward tiles are as long)
+  l.sums = round_up((size_t)p.words * 8 + (kept ? 0 : forward_bytes<T>(B, N, C)), 256);
+  l.states = l.sums + round_up((size_t)B * p.tiles * C * 4, 256);
   l.bytes = l.states + (kept ? 0 : (size_t)B * ((N + kKept - 1) / kKept) * C * 4);
   return l;
 }
 
 template <class T>
 hipError_t forward_call(const RecurrenceArgs& a, void* ws, hipStream_t st) {
-  const Plan p = plan_of<T>(a.B, a.N, a.C, paired<T>(a), false);
+  const Plan p = plan_of<T>(a.B, a.N, a.C, false);
   unsigned long long* w = static_cast<unsigned long long*>(ws);
   const hipError_t e = clear(w, p, nullptr, st);
   return e == hipSuccess ? run_forward<T>(a, p, w, st) : e;
@@ -653,9 +646,9 @@ hipError_t forward_call(const RecurrenceArgs& a, void* ws, hipStream_t st) {
 
 template <class T>
 hipError_t backward_call(RecurrenceArgs a, void* ws, hipStream_t st) {
-  const bool kept = a.kept != nullptr, pairs = paired<T>(a);
+  const bool kept = a.kept != nullptr;
   const BackLayout l = back_layout<T>(a.B, a.N, a.C, kept);
-  const Plan p = plan_of<T>(a.B, a.N, a.C, pairs, true), q = plan_of<T>(a.B, a.N, a.C, pairs, false);
+  const Plan p = plan_of<T>(a.B, a.N, a.C, true), q = plan_of<T>(a.B, a.N, a.C, false);
   unsigned long long* w = static_cast<unsigned long long*>(ws);
   float* sums = reinterpret_cast<float*>(static_cast<char*>(ws) + l.sums);
   hipError_t e = clear(w, p, kept ? nullptr : &q, st);

@@ -26,6 +26,8 @@ CASES = [  # B, N, C, dtype, h0, lengths, sliced
     (4, 5000, 386, "bf16", True, [5000, 0, 2049, 4100], True), (4, 5000, 384, "bf16", False, None, False),
     (5, 2500, 258, "fp32", True, [2500, 1024, 1025, 63, 2049], False), (2, 9000, 129, "bf16", True, [9000, 8193], False),
     (1, 16500, 64, "fp32", True, None, False), (1, 10000, 130, "bf16", False, [9001], False), (65, 40, 1, "fp32", True, None, False),
+    # the same of odd widths, rows at odd elements
+    (4, 1030, 517, "fp32", True, [1030, 64, 0, 1001], True), (6, 700, 771, "bf16", True, None, True),
 ]
 ids = lambda c: "-".join(str(v) for v in c[:5]) + ("-lengths" if c[5] else "") + ("-sliced" if c[6] else "")  # noqa: E731
 
@@ -183,6 +185,29 @@ def test_lengths_outside_are_the_nearer_end():
         assert torch.equal(a, b)
     assert torch.equal(T.ttt_forward_gated_recurrence(*mats, h0=s["h0"], lengths=near),
                        T.ttt_forward_gated_recurrence(*mats, h0=s["h0"], lengths=far))
+
+
+@pytest.mark.parametrize("B,N,C,dtype", [(2, 9000, 129, "bf16"), (4, 1030, 517, "fp32"), (2, 65, 33, "bf16"), (2, 70, 128, "fp32")])
+def test_rows_at_any_element_and_what_is_around_them(B, N, C, dtype):
+    """Outputs that start one element behind an aligned place: the bits of other calls, and what is before and behind as it was."""
+    print(f"recurrence around B={B} N={N} C={C} {dtype}", flush=True)
+    mats, s, d_y = _inputs(B, N, C, dtype, True, None, False)
+    arounds = []
+
+    def inside(t):
+        around = torch.full((t.numel() + 32,), 7.0, dtype=t.dtype, device="cuda")
+        arounds.append((around, t.numel()))
+        return around[9:9 + t.numel()].view(t.shape)
+
+    want = T.ttt_forward_gated_recurrence(*mats, **s)
+    end, kept = inside(s["h0"]), inside(torch.empty(B, (N + 63) // 64, C, device="cuda"))
+    assert torch.equal(T.ttt_forward_gated_recurrence(*mats, y=inside(want), h_out=end, states=kept, **s), want)
+    want = T.ttt_backward_gated_recurrence(*mats, d_y, **s)
+    got = T.ttt_backward_gated_recurrence(*mats, d_y, states=kept, **s,
+                                          **{k: inside(t) for k, t in zip(("d_x", "d_r", "d_i", "d_lam", "d_h0"), want)})
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    for around, n in arounds:
+        assert bool((around[:9] == 7).all()) and bool((around[9 + n:] == 7).all())
 
 
 @pytest.mark.parametrize("B,N,C,dtype", [(2, 700, 130, "bf16"), (1, 5000, 64, "fp32"), (3, 257, 101, "bf16"), (2, 64, 33, "fp32"),
