@@ -148,6 +148,13 @@ __device__ __forceinline__ uint32_t to_e4m3(const float* v) {
   const int r = __builtin_amdgcn_cvt_pk_fp8_f32(v[0], v[1], 0, false);
   return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(v[2], v[3], r, true);
 }
+// Halfway between two (normal) numbers of e4m3; the neighbour of such a number on the side of `rest`, what it lacks to the value that it was
+// rounded from. (Rounding to fp32 comes to a halfway point, but not past it, so that the value's own nearest is kept.)
+__device__ __forceinline__ bool is_tie(float v) { return (__float_as_uint(v) & 0xfffffu) == 0x80000u; }
+__device__ __forceinline__ float towards(float v, float rest) {
+  const int u = __float_as_int(v), up = (__float_as_int(rest) ^ u) >= 0 ? 1 : -1;
+  return __int_as_float(rest == 0.f ? u : u + up);
+}
 template <int K, int L, int V, int PART>
 __device__ __forceinline__ void store_e4m3(uint8_t* p, const float* v, const Spread<L, V, PART>& s) {
   typedef uint32_t Any __attribute__((aligned(1)));
@@ -242,7 +249,18 @@ __global__ __launch_bounds__(threads_of<L>) void rmsnorm_fwd(const T* __restrict
       const bool odd = !(scaled >= kLeastMax && scaled < __builtin_inff());
       const float r = rcp_hw(top), inv = kE4m3Most * r, inv_low = fmaf(-inv, top, kE4m3Most) * r;
       if (__ballot(odd) == 0) {
-        for (int i = 0; i < V; ++i) v[k * V + i] = fmaf(v[k * V + i], inv, fmaf(v[k * V + i], inv_low, low[k * V + i] * inv));
+        bool tie = false;
+        float h[V];
+        for (int i = 0; i < V; ++i) {
+          h[i] = fmaf(v[k * V + i], inv, fmaf(v[k * V + i], inv_low, low[k * V + i] * inv));
+          tie = tie || is_tie(h[i]);
+        }
+        if (__ballot(tie) != 0)
+          for (int i = 0; i < V; ++i) {
+            const float rest = fmaf(v[k * V + i], inv, -h[i]) + fmaf(v[k * V + i], inv_low, low[k * V + i] * inv);
+            if (is_tie(h[i])) h[i] = towards(h[i], rest);
+          }
+        for (int i = 0; i < V; ++i) v[k * V + i] = h[i];
       } else {  // zeros, next to nothing, infinities, NaN
         scaled = scaled < kLeastMax ? kLeastMax : scaled;
         const float plain = rstd * (kE4m3Most / scaled);
