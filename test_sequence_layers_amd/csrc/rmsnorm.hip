@@ -246,6 +246,7 @@ __global__ __launch_bounds__(threads_of<L>) void rmsnorm_fwd(const T* __restrict
     for (int k = 0; k < K; ++k) {
       const float top = __uint_as_float(group == D ? all : lanes_max(most[k], share));
       float scaled = top * rstd;  // the largest of the norm's output
+      float scale;
       const bool odd = !(scaled >= kLeastMax && scaled < __builtin_inff());
       const float r = rcp_hw(top), inv = kE4m3Most * r, inv_low = fmaf(-inv, top, kE4m3Most) * r;
       if (__ballot(odd) == 0) {
@@ -261,6 +262,8 @@ __global__ __launch_bounds__(threads_of<L>) void rmsnorm_fwd(const T* __restrict
             if (is_tie(h[i])) h[i] = towards(h[i], rest);
           }
         for (int i = 0; i < V; ++i) v[k * V + i] = h[i];
+        scale = scaled * (1.f / kE4m3Most);  // (divided: the remainder is exact)
+        scale = fmaf(fmaf(-scale, kE4m3Most, scaled), 1.f / kE4m3Most, scale);
       } else {  // zeros, next to nothing, infinities, NaN
         scaled = scaled < kLeastMax ? kLeastMax : scaled;
         const float plain = rstd * (kE4m3Most / scaled);
@@ -268,9 +271,10 @@ __global__ __launch_bounds__(threads_of<L>) void rmsnorm_fwd(const T* __restrict
           const int j = k * V + i;
           v[j] = odd ? v[j] * plain : fmaf(v[j], inv, fmaf(v[j], inv_low, low[j] * inv));
         }
+        scale = scaled / kE4m3Most;
       }
       const int at = (k * L + s.lane) * V;
-      if (at < D && (group == D ? at == 0 : (s.lane & (share - 1)) == 0)) scales[(row * D + at) / group] = scaled / kE4m3Most;
+      if (at < D && (group == D ? at == 0 : (s.lane & (share - 1)) == 0)) scales[(row * D + at) / group] = scale;
     }
     store_e4m3<K>((uint8_t*)y + row * D, v, s);
   }
