@@ -149,11 +149,12 @@ __device__ __forceinline__ uint32_t to_e4m3(const float* v) {
   return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(v[2], v[3], r, true);
 }
 // Halfway between two (normal) numbers of e4m3; the neighbour of such a number on the side of `rest`, what it lacks to the value that it was
-// rounded from. (Rounding to fp32 comes to a halfway point, but not past it, so that the value's own nearest is kept.)
+// rounded from (less than 2^-40 of it is none: products are known to 2^-46). Rounding to fp32 comes to a halfway point, but not past it, so
+// that the value's own nearest is kept.
 __device__ __forceinline__ bool is_tie(float v) { return (__float_as_uint(v) & 0xfffffu) == 0x80000u; }
 __device__ __forceinline__ float towards(float v, float rest) {
   const int u = __float_as_int(v), up = (__float_as_int(rest) ^ u) >= 0 ? 1 : -1;
-  return __int_as_float(rest == 0.f ? u : u + up);
+  return __int_as_float(fabsf(rest) < 0x1p-40f * fabsf(v) ? u : u + up);
 }
 template <int K, int L, int V, int PART>
 __device__ __forceinline__ void store_e4m3(uint8_t* p, const float* v, const Spread<L, V, PART>& s) {

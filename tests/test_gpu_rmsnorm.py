@@ -10,6 +10,7 @@ from lm_helpers import EPS, factors, rng_of, within  # noqa: E402
 from seq_helpers import Inputs, replays, sliced  # noqa: E402
 from seq_reference import held  # noqa: E402
 
+from oracle import lm_oracle as O  # noqa: E402
 import test_sequence_layers_amd as T  # noqa: E402
 
 DEPTH = 24 + 6 + 16
@@ -152,6 +153,30 @@ def test_e4m3_rounds_to_the_nearest():
     below, above = table[:-1].double(), table[1:].double()
     mid = got[n:2 * n - 1]
     assert bool(((mid == below) | (mid == above)).all())
+
+
+@pytest.mark.parametrize("D,group", [(128, 0), (256, 128), (4096, 0)])
+def test_e4m3_takes_values_beside_a_tie_to_their_own_side(D, group):
+    """Numbers of fp32 next to halfway points of their group's scale, off by at most 2^-24 of themselves: with weights of one the
+    quotient by the group's largest is exact before it is rounded to 8 bits, and the nearest is the quotient's in 64 bits."""
+    ties = torch.tensor([(8.5 + m) * 2.0 ** (e - 3) for e in range(-6, 9) for m in range(8)], dtype=torch.float64)
+    ties = ties[ties < 448]
+    i = Inputs(D, "fp32")
+    top = (i.normal(64, 1).abs().clamp(min=0.01) * 2.0 ** torch.arange(-20, 44, device="cuda")[:, None].float()).cpu()
+    v = torch.zeros(64, D, dtype=torch.float64)
+    v[:, 0] = 448
+    v[:, 1:1 + len(ties)] = ties
+    if group:
+        v[:, group:] = -v[:, :-group]
+    if D > 512:
+        v = v.roll(1000, 1)
+    x = (v * top.double() / 448).float()
+    q = x.double() * 448 / top.double()
+    y, scales = T.ttt_forward_rmsnorm_e4m3(x.cuda(), torch.ones(D, device="cuda"), EPS, group=group)
+    assert torch.equal(y.double().cpu(), torch.from_numpy(O.e4m3(q.numpy())))
+    # a scale: half of what the squares' sum loses, two steps each of the mean, the root and its inverse, two products
+    norm = x.double() / (x.double().square().mean(-1, keepdim=True) + EPS).sqrt()
+    assert float((scales.double().cpu() * 448 / norm.abs().amax(-1, keepdim=True) - 1).abs().max()) < (DEPTH / 2 + 10) * 2.0 ** -24
 
 
 def test_in_place():
