@@ -7,8 +7,8 @@
 
 namespace ttt {
 
-// 16 bytes of a row, at any alignment of its elements: the hardware takes them so, and rows of odd widths are read as fast as others
-// (1537 x 1001 fp32 backward TIME).
+// 16 bytes of a row, at any alignment of its elements: the hardware takes them so, and rows of odd widths cost little more than others
+// (norm of 32768 rows in bf16: 36.8 us of 768 channels, 37.6 of 766, 38.8 of 767, 46 with the end of a row, and its weights, element by element).
 template <class T>
 constexpr int kPiece = 16 / (int)sizeof(T);
 typedef uint32_t Words __attribute__((ext_vector_type(4)));
