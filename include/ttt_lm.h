@@ -82,7 +82,9 @@ long long ttt_dropout_counters(int M, int C);
  * x, r, i, y: [B, N, C]; lam: fp32 [C]; h0 (nullable, zeros without it), h_out (nullable): fp32 [B, C], the states before
  * token 0 and after each sequence's last. states (nullable): fp32 [B, ceil(N / 64), C] receives the states before tokens 0, 64,
  * 128, ... (of padding: the sequence's last), which the backward pass can take. scale finite and positive. B at most 65535, N at
- * most 2^22, C at most 2^20, B * (N + 128) * (C + 64) at most 2^38.
+ * most 2^22, C at most 2^20, B * (N + 128) * (C + 64) at most 2^38. A NaN, or an infinite x or h0, stays in its channel of its sequence:
+ * what is before it is as without it, what is behind it infinite or NaN. Of a state the decays of many tokens may leave nothing (their product is
+ * fp32's): what is below 2^-126 of it is lost.
  */
 ttt_status ttt_forward_gated_recurrence(ttt_dtype dt, int B, int N, int C, float scale, const void* x,
                                         long long x_stride, const void* r, long long r_stride, const void* i,

@@ -164,6 +164,27 @@ def test_what_is_not_finite_stays_in_its_channel_and_sequence():
         assert torch.equal(a[clean], b[clean])
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_an_infinite_input_is_behind_it_alone(dtype):
+    """Within a run of tokens, at a tile's first and last, and so far back that the decays' product is nothing: rows before are the bits of
+    the call without it, rows from it on are not finite; infinite gates are gates of 0 and 1."""
+    mats, _, d_y = _inputs(1, 3000, 6, dtype, False, None, False)
+    want, grads = T.ttt_forward_gated_recurrence(*mats), T.ttt_backward_gated_recurrence(*mats, d_y)
+    x, r, g, lam = (t.clone() for t in mats)
+    at = (5, 127, 128, 640, 2999, 0)
+    for c, n in enumerate(at):
+        x[0, n, c] = float("inf") if c % 2 else -float("inf")
+    y, got = T.ttt_forward_gated_recurrence(x, r, g, lam), T.ttt_backward_gated_recurrence(x, r, g, lam, d_y)
+    for c, n in enumerate(at):
+        assert torch.equal(y[0, :n, c], want[0, :n, c]) and not torch.isfinite(y[0, n:, c]).any()
+        assert torch.equal(got[0][..., c], grads[0][..., c])  # (x is not in its own gradient)
+        assert torch.equal(got[1][0, :n, c], grads[1][0, :n, c]) and torch.equal(got[2][0, :n, c], grads[2][0, :n, c])
+    ends = torch.tensor([float("inf"), -float("inf")], device="cuda", dtype=x.dtype).repeat(3)
+    r, g = ends.expand(1, 3000, 6).contiguous(), ends.flip(0).expand(1, 3000, 6).contiguous()
+    assert torch.isfinite(T.ttt_forward_gated_recurrence(mats[0], r, g, lam)).all()
+    assert all(torch.isfinite(t).all() for t in T.ttt_backward_gated_recurrence(mats[0], r, g, lam, d_y)[:4])
+
+
 def test_an_empty_slots_state_reaches_nothing():
     """A sequence of no tokens with a start state of NaN: its state is handed on, its rows and gradients are zeros, d_lam is clean."""
     mats, s, d_y = _inputs(3, 100, 70, "bf16", True, [100, 0, 50], False)
