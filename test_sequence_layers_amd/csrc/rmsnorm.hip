@@ -7,7 +7,7 @@
 // A stream of rows, bound by HBM, laid out as layer norm's (normrows.hpp): a row is read once into the registers of L
 // lanes, and the sum, the statistics, the maxima and every output come from there. Apart, the addition, the norm and
 // the conversion would read and write the row two more times each. At the card's copying rate (5.2 TB/s) or near it: 32768 x 768 in bf16
-// with dropout forward 36.7 us (5.5 TB/s), backward 52 (4.9); 16384 x 1536 into 8 bits 36.3 in groups of 128 and 33 by rows (4.9 and
+// with dropout forward 36.7 us (5.5 TB/s), backward 52 (4.9); 16384 x 1536 into 8 bits 34 in groups of 128 and 33 by rows (5.2 and
 // 5.3). Small calls are a launch: 16 x 768 into 8 bits 3.7 us, backward 1537 x 1001 in fp32 12.2 (one row a wave, then 3 us for the sum
 // of partial rows).
 #include "internal.hpp"
@@ -122,7 +122,7 @@ __device__ __forceinline__ void drop_row(float* v, const Drop& d, long long row,
     for (int i = 0; i < V; ++i) v[k * V + i] = m.kept(k, i) ? v[k * V + i] * d.scale : 0.f;
 }
 
-// Largest value over aligned groups of L lanes (runtime L, a power of two).
+// Largest value over aligned groups of L lanes (runtime L, a power of two, 4 at least: 32 channels of bf16).
 __device__ __forceinline__ uint32_t lanes_max(uint32_t v, int L) {
   auto other = [](uint32_t a, int which) {
     const int x = (int)a;
@@ -131,8 +131,8 @@ __device__ __forceinline__ uint32_t lanes_max(uint32_t v, int L) {
                       : which == 4 ? __builtin_amdgcn_update_dpp(0, x, kDppMirror8, 0xf, 0xf, true)
                                    : __builtin_amdgcn_update_dpp(0, x, kDppMirror16, 0xf, 0xf, true));
   };
-  if (L >= 2) v = max(v, other(v, 1));
-  if (L >= 4) v = max(v, other(v, 2));
+  v = max(v, other(v, 1));
+  v = max(v, other(v, 2));
   if (L >= 8) v = max(v, other(v, 4));
   if (L >= 16) v = max(v, other(v, 8));
   if (L >= 32) {

@@ -264,6 +264,18 @@ def test_a_probability_of_less_than_half_a_step_drops_nothing():
     assert torch.equal(d_s, d_x)
 
 
+def test_rows_past_32_bits():
+    """Rows whose stride takes them past 2^32 elements: the last row's results are those of a call on it alone."""
+    D, stride = 777, 2_400_000_001
+    rows = torch.zeros(2 * stride + D, device="cuda", dtype=torch.bfloat16)  # 9.6 GB
+    x, i = rows.as_strided((3, D), (stride, 1)), Inputs(1, "bf16")
+    x.copy_(i.normal(3, D))
+    w, d_y = i.param(D, mean=1.0, scale=0.2), i.normal(3, D)
+    y, d_s = T.ttt_forward_rmsnorm(x, w, EPS), T.ttt_backward_rmsnorm(x, w, d_y, EPS)[0]
+    assert torch.equal(y[2:], T.ttt_forward_rmsnorm(x[2:].contiguous(), w, EPS))
+    assert torch.equal(d_s[2:], T.ttt_backward_rmsnorm(x[2:].contiguous(), w, d_y[2:].contiguous(), EPS)[0])
+
+
 def test_refusals():
     x, w, res = torch.zeros(4, 64, device="cuda"), torch.zeros(64, device="cuda"), torch.zeros(4, 64, device="cuda")
     rng = rng_of(0, 0)
