@@ -10,9 +10,8 @@
 
 namespace {
 
+using ttt::kKept;
 using ttt::round_up;
-
-constexpr int kKept = 64;  // tokens between the recurrence's kept states
 
 ttt_status check_rmsnorm_sizes(ttt_dtype dt, int M, int H, int D) {
   if (!known(dt) || M <= 0 || H <= 0 || D <= 0) return TTT_ERR_INVALID;

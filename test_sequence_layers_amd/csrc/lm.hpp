@@ -39,6 +39,7 @@ struct DropoutArgs {
 hipError_t dropout_launch(bool bf16_io, const DropoutArgs& a, hipStream_t st);
 
 // ---- gated recurrence -------------------------------------------------------------------------
+constexpr int kKept = 64;  // tokens between the recurrence's kept states
 struct RecurrenceArgs {
   int B, N, C;
   float scale;

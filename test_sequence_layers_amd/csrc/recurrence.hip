@@ -28,7 +28,6 @@ namespace ttt {
 namespace {
 
 constexpr int kThreads = 64;  // of a step's workgroup
-constexpr int kKept = 64;     // tokens between kept states
 
 // (exp(u) - 1) / u for -1/2 <= u <= 0, within 1.1 * 2^-24 of it (a polynomial through Chebyshev's nodes), and 1 - exp(u) for
 // u <= 0: by that where the difference would lose bits; e is exp(u).
