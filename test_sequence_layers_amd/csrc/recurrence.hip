@@ -231,7 +231,7 @@ __global__ __launch_bounds__(64 * W) void recurrence_fwd(RecurrenceArgs a, int t
   if (!draw(board, tiles, columns, total, k)) return;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, C = a.C, N = a.N;
   const int wide = columns * CH, rows = (N + kKept - 1) / kKept;
-  const int c0 = k.column * CH + lane * V, c = min(c0, C - V);  // (past the last channel the last ones again: an odd last channel's lane has the one before it too, with the same results)
+  const int c0 = k.column * CH + lane * V, c = min(c0, C - V);  // (past the last channel the last ones again: an odd last channel's lane has the one before it too, of the same wave, with the same results)
   const bool mine = c0 < C;
   const int n = length_of(a.lengths, k.b, N), t0 = k.tile * TILE + wave * TW;
   const int live = n - t0, inside = N - t0;  // tokens of this run and those behind it, of the sequence and of the padded one
@@ -389,7 +389,7 @@ __global__ __launch_bounds__(64 * W) void recurrence_bwd(RecurrenceArgs a, int t
   k.tile = tiles - 1 - k.tile;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, C = a.C, N = a.N;
   const int wide = columns * CH, rows = (N + kKept - 1) / kKept;
-  const int c0 = k.column * CH + lane * V, c = min(c0, C - V);  // (past the last channel the last ones again: an odd last channel's lane has the one before it too, with the same results)
+  const int c0 = k.column * CH + lane * V, c = min(c0, C - V);  // (past the last channel the last ones again: an odd last channel's lane has the one before it too, of the same wave, with the same results)
   const bool mine = c0 < C;
   const int n = length_of(a.lengths, k.b, N), t0 = k.tile * TILE + wave * TW;
   const int live = n - t0, inside = N - t0;  // tokens of this run and those behind it, of the sequence and of the padded one
@@ -584,15 +584,18 @@ Plan cut(int B, int N, int C, int W, int V, int TW) {
   return p;
 }
 // Two channels a lane where that gives each CU a workgroup: a wave then moves 256 bytes (bf16) at a time and joins half as many pairs;
-// otherwise one, for twice as many workgroups. (Tiles of 32 tokens for small calls gain a tenth at most, 1 x 512 x 256 8.5 -> 7.7 us, and
-// lose where a sequence has many, 2 x 1024 x 768 11 -> 19.) As many tokens a lane as registers hold.
+// otherwise one, for twice as many workgroups. One too where the last column would be a single channel: its lane would compute the channel
+// before it, which another workgroup has, and the two may form their decays differently (Gates: by all of a
+// column's channels): 4 x 8192 x 769 in bf16 70 us forward and 151 backward, x 770 62 and 123. (Tiles of 32 tokens
+// for small calls gain a tenth at most, 1 x 512 x 256 8.5 -> 7.7 us, and lose where a sequence has many, 2 x 1024 x 768 11 -> 19.) As many
+// tokens a lane as registers hold.
 constexpr int kCus = 256;
 template <class T>
 Plan plan_of(int B, int N, int C, bool backward) {
   constexpr bool kHalf = sizeof(T) == 2;
   const int W = backward && !kHalf ? 16 : 8, TW = backward ? (kHalf ? 8 : 4) : (kHalf ? 16 : 8);
   const Plan two = cut(B, N, C, W, 2, TW);
-  return C > 1 && two.workgroups(B) >= kCus ? two : cut(B, N, C, W, 1, TW);
+  return C % 128 != 1 && two.workgroups(B) >= kCus ? two : cut(B, N, C, W, 1, TW);
 }
 
 Board board_of(const Plan& p, int B, unsigned long long* w) {

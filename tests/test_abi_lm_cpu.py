@@ -153,6 +153,28 @@ def test_workspace_sizes():
         assert bwd(BF16, 4, 8192, 768, kept) > 0 and bwd(BF16, 4, 8192, 768, kept) % 256 == 0 and bwd(BF16, 4, 8192, 0, kept) == 0
 
 
+def _channels_a_lane(B, N, C, dt):
+    """Of the forward recurrence, from its workspace: 16 words for each column of 64 or 128 channels of a sequence, one for each channel
+    of its tiles (of 128 tokens in bf16, 64 in fp32) and groups of 16 tiles, 8 bytes each."""
+    need = T.load_library().ttt_forward_gated_recurrence_workspace(dt, B, N, C)
+    tiles = -(-N // (128 if dt == BF16 else 64))
+    fits = [V for V in (1, 2) if (8 * B * -(-C // (64 * V)) * (16 + 64 * V * (tiles + -(-tiles // 16))) + 255) // 256 * 256 == need]
+    assert len(fits) == 1, (B, N, C, need)
+    return fits[0]
+
+
+@pytest.mark.parametrize("dt", [BF16, F32])
+def test_a_channel_of_the_recurrence_has_one_workgroup(dt):
+    """With two channels a lane the last of an odd width is computed with the one before it, which has to be of the same column: a
+    column forms its decays by all its channels, so two of them need not give the same bits for it."""
+    seen = set()
+    for C in [*range(1, 400), 511, 512, 513, 514, 769, 1023, 1024, 1025, 2049, 65537]:
+        V = _channels_a_lane(300, 9000, C, dt) if C < 5000 else _channels_a_lane(2, 9000, C, dt)
+        seen.add(V)
+        assert V == 1 or C % 128 != 1, C
+    assert seen == {1, 2}
+
+
 def test_binding_refuses_host_tensors():
     torch = pytest.importorskip("torch")
     x, w, rng = torch.zeros(2, 3, 8), torch.zeros(8), torch.zeros(2, dtype=torch.int64)

@@ -231,6 +231,30 @@ def test_rows_at_any_element_and_what_is_around_them(B, N, C, dtype):
         assert bool((around[:9] == 7).all()) and bool((around[9 + n:] == 7).all())
 
 
+@pytest.mark.parametrize("B,N,C,dtype", [(4, 5000, 129, "fp32"), (2, 5000, 257, "fp32"), (3, 6000, 385, "bf16"), (4, 5000, 131, "fp32")])
+def test_a_steep_channel_beside_the_last_of_an_odd_width(B, N, C, dtype):
+    """One fast decay in the column before the last, slow ones in the last two channels: every call gives the same bits."""
+    print(f"recurrence with a steep channel B={B} N={N} C={C} {dtype}", flush=True)
+    (x, r, g, lam), s, d_y = _inputs(B, N, C, dtype, True, None, False)
+    lam = torch.full_like(lam, -5.0)
+    lam[C - 20] = 2.0
+    end, kept = torch.empty(B, C, device="cuda"), torch.empty(B, (N + 63) // 64, C, device="cuda")
+
+    def call():
+        y = T.ttt_forward_gated_recurrence(x, r, g, lam, h_out=end, states=kept, **s)
+        return (y, end.clone(), kept.clone(), *T.ttt_backward_gated_recurrence(x, r, g, lam, d_y, states=kept, **s))
+
+    want = call()
+    for name, got, ref in zip(("y", "h_out", "states"), want, (lambda d: (d["y"], d["h_out"], [v[:, ::64] for v in d["before"]]))(
+            R.recurrence(x, r, g, lam, **s))):
+        held(name, got, tuple(ref))
+    ref = R.recurrence(x, r, g, lam, d_y, depth=_depth(B, N), **s)
+    for name, got in zip(("d_x", "d_r", "d_i", "d_lam", "d_h0"), want[3:]):
+        held(name, got, ref[name])
+    for _ in range(20):
+        assert all(torch.equal(a, b) for a, b in zip(call(), want))
+
+
 @pytest.mark.parametrize("B,N,C,dtype", [(2, 700, 130, "bf16"), (1, 5000, 64, "fp32"), (3, 257, 101, "bf16"), (2, 64, 33, "fp32"),
                                          (1, 1, 8, "bf16")])
 def test_workspaces_are_enough_and_not_left(B, N, C, dtype):
