@@ -32,8 +32,9 @@ extern "C" {
  *   y = s / sqrt(mean(s^2) + eps) * weight[h].
  * residual, sum, y: [M, H, D]. sum, given exactly when residual is, receives s; it may be the residual in place. The norm is taken
  * of s before it is rounded. A residual needs H = 1, dropout (p > 0, with rng) a residual. D in [1, 16384], H at most
- * 65535, H * D at most 2^24, M * H at most 2^31 - 1; eps finite and not negative. Rows whose sum of squares is
- * not finite in fp32 are normed all the same, as long as they are finite. No workspace.
+ * 65535, H * D at most 2^24, M * H at most 2^31 - 1; eps finite and not negative. Rows whose sum of squares is past
+ * fp32's numbers, above or (with an eps next to zero) below, are normed all the same, as long as they are finite; a row of zeros with an eps of
+ * zero is NaN. No workspace.
  */
 ttt_status ttt_forward_rmsnorm(ttt_dtype dt, int M, int H, int D, float eps, const void* x, long long x_stride,
                                const void* residual, double p, const long long* rng, const float* weight, void* sum,

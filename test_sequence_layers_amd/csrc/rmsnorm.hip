@@ -83,9 +83,10 @@ __device__ __forceinline__ void load_weights(const float* w, float* out, const S
     }
 }
 
-// rstd of a row, times *back; v is scaled by 1 / *back where its squares overflow (from 2^60 or so on: the largest squares
-// are 2^96 then, and eps is nothing beside them), so that such rows are normed like others. An infinite or NaN entry makes its row
-// NaN at least where the entry is.
+// rstd of a row, over *back: v is multiplied by *back where its squares overflow (from 2^60 or so on: the largest squares are 2^96
+// then, and eps is nothing beside them) or are next to nothing under an eps that is too (a mean below 2^-90: the smallest numbers become
+// 2^-41, the largest squares 2^126), so that such rows are normed like others. An infinite or NaN entry makes its row NaN at least
+// where the entry is.
 template <int L, int K, int V>
 __device__ __forceinline__ float inverse_rms(float* v, int D, float eps, float (*red)[16], float* back) {
   float q = 0.f;
@@ -93,18 +94,18 @@ __device__ __forceinline__ float inverse_rms(float* v, int D, float eps, float (
   for (int j = 0; j < K * V; ++j) q = fmaf(v[j], v[j], q);
   q = row_sum<L>(q, red, 0);
   *back = 1.f;
-  const bool over = !(q < __builtin_inff());
-  if (__ballot(over)) {  // (rows of more than a wave: the same for all of it)
-    const float down = over ? 0x1p-80f : 1.f;
+  const bool over = !(q < __builtin_inff()), under = q < 0x1p-90f && eps < 0x1p-90f;
+  if (__ballot(over || under)) {  // (rows of more than a wave: the same for all of it)
+    const float by = over ? 0x1p-80f : under ? 0x1p108f : 1.f;
     float t = 0.f;
 #pragma unroll
     for (int j = 0; j < K * V; ++j) {
-      v[j] *= down;
+      v[j] *= by;
       t = fmaf(v[j], v[j], t);
     }
     q = row_sum<L>(t, red, 1);
-    eps = over ? 0.f : eps;
-    *back = down;
+    eps = over ? 0.f : eps * by * by;
+    *back = by;
   }
   return rcp_hw(sqrtf(fmaf(q, rcp_hw((float)D), eps)));
 }
@@ -333,7 +334,13 @@ __global__ __launch_bounds__(bwd_threads(L, K* kPiece<T>)) void rmsnorm_bwd(cons
       s2 = fmaf(d[j], v[j], s2);
     }
     s2 = row_sum<L>(s2, red, 2) * inv_d;
-    const float outer = rstd * back;
+    float outer = rstd * back;
+    if (__ballot(!(outer < __builtin_inff()))) {  // (of a row below 2^-128 it is past fp32, not what comes of it)
+      const float by = outer < __builtin_inff() ? 1.f : 0x1p40f;
+#pragma unroll
+      for (int j = 0; j < K * V; ++j) d[j] *= by;
+      s2 *= by, outer = by == 1.f ? outer : rstd * (back * 0x1p-40f);
+    }
 #pragma unroll
     for (int j = 0; j < K * V; ++j) d[j] = outer * (d[j] - v[j] * s2) + (ADD ? e[j] : 0.f);
     const long long o = (m * H + h) * D;
