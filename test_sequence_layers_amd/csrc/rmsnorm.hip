@@ -271,10 +271,10 @@ __global__ __launch_bounds__(threads_of<L>) void rmsnorm_fwd(const T* __restrict
         scale = fmaf(fmaf(-scale, kE4m3Most, scaled), 1.f / kE4m3Most, scale);
       } else {  // zeros, next to nothing, infinities, NaN
         scaled = scaled < kLeastMax ? kLeastMax : scaled;
-        const float plain = rstd * (kE4m3Most / scaled);
+        const float plain = kE4m3Most / scaled;  // (up to 448 * 2^100; times rstd it could pass fp32)
         for (int i = 0; i < V; ++i) {
           const int j = k * V + i;
-          v[j] = odd ? v[j] * plain : fmaf(v[j], inv, fmaf(v[j], inv_low, low[j] * inv));
+          v[j] = odd ? v[j] * rstd * plain : fmaf(v[j], inv, fmaf(v[j], inv_low, low[j] * inv));
         }
         scale = scaled / kE4m3Most;
       }

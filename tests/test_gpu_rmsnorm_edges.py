@@ -13,6 +13,7 @@ from seq_reference import held  # noqa: E402
 import test_sequence_layers_amd as T  # noqa: E402
 
 DEPTH = 24 + 6 + 16  # additions of a row's sum: in a lane, over lanes, over waves
+LEAST = 2.0 ** -100 / 448
 
 
 def _within(got, ref, group, D):
@@ -23,6 +24,50 @@ def _within(got, ref, group, D):
 
 
 # --------------------------------------------------------------------------- zeros and next to zero
+@pytest.mark.parametrize("eps", [2.0 ** -40, 2.0 ** -100, 2.0 ** -126])
+@pytest.mark.parametrize("D,group,dtype", [(64, 0, "bf16"), (96, 32, "fp32"), (256, 128, "bf16"), (1001, 0, "fp32"), (4096, 64, "bf16")])
+def test_rows_and_groups_of_zeros_in_8_bits(D, group, dtype, eps):
+    """Zeros, at the least scale, whatever eps is: padding's rows, and groups that their weights or their row leave without a value."""
+    i = Inputs(D, dtype)
+    x, w = i.normal(9, D), i.param(D, mean=1.0, scale=0.2)
+    x[[0, 3, 8]] = 0
+    size = group or D
+    if group:
+        x[1:3, size:2 * size] = 0
+        w[:size] = 0
+    y, scales = T.ttt_forward_rmsnorm_e4m3(x, w, eps, group=group)
+    empty = torch.zeros_like(scales, dtype=torch.bool)
+    empty[[0, 3, 8]] = True
+    if group:
+        empty[1:3, 1] = True
+        empty[:, 0] = True
+    wide = empty.repeat_interleave(size, -1)
+    assert not y.float()[wide].any() and bool((y.float()[~wide] != 0).any())
+    assert float((scales.double()[empty] / LEAST - 1).abs().max()) < 2.0 ** -23
+    _within((y, scales), R.rmsnorm_e4m3(x, w, eps, DEPTH, size), group, D)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_a_group_of_zeros_in_a_row_next_to_zero(dtype):
+    """No eps, rows of 1e-7 and of 1e-15, and a group of zeros in them."""
+    i = Inputs(5, dtype)
+    x, w = i.normal(8, 256), i.param(256, mean=1.0, scale=0.2)
+    x *= torch.tensor([1e-7, 1e-15], device="cuda").repeat(4)[:, None].to(x.dtype)
+    x[:, 32:64] = 0
+    y, scales = T.ttt_forward_rmsnorm_e4m3(x, w, 0.0, group=32)
+    assert not y.float()[:, 32:64].any() and float((scales.double()[:, 1] / LEAST - 1).abs().max()) < 2.0 ** -23
+    _within((y, scales), R.rmsnorm_e4m3(x, w, 0.0, DEPTH, 32), 32, 256)
+
+
+def test_outputs_below_the_least_scale():
+    """Groups whose largest output is below 2^-100 take that as their largest: 1e-38 under eps 2^-40 comes to 1e-32."""
+    i = Inputs(6, "fp32")
+    x, w = (i.normal(8, 256).double() * 1e-38).float(), i.param(256, mean=1.0, scale=0.2)
+    got = T.ttt_forward_rmsnorm_e4m3(x, w, 2.0 ** -40, group=64)
+    assert float((got[1].double() / LEAST - 1).abs().max()) < 2.0 ** -23 and bool(got[0].float().any())
+    _within(got, R.rmsnorm_e4m3(x, w, 2.0 ** -40, DEPTH, 64), 64, 256)
+
+
 @pytest.mark.parametrize("size", [-45, -60, -74, -80, -100, -126, -132])
 @pytest.mark.parametrize("D,dtype", [(64, "bf16"), (768, "fp32"), (1001, "bf16"), (1001, "fp32"), (4096, "bf16"), (16384, "fp32")])
 def test_rows_next_to_zero_are_normed_like_others(D, dtype, size):
