@@ -220,8 +220,12 @@ __global__ __launch_bounds__(threads_of<L>) void rmsnorm_fwd(const T* __restrict
     AnyRow<T, L, K, PART>::store((T*)y + row * D, v, s);
   } else {
     // rstd is not in y / scale: of v w, its maximum M over the group and 448 / M, the first and the last as two numbers
-    // each, so that the rounding to 8 bits has but one other before it. Maxima of the absolute values' bits: as numbers they are in the
-    // same order, and a NaN is above all.
+    // each, so that the rounding to 8 bits has but one other before it. v comes by the power of two 8 to 16 times below rstd, so that the
+    // products are of the output's size and pass fp32 at neither end where that does not; `fine` is what is left of rstd (2^-66 stands below an
+    // rstd of zero, of a row with an infinity). Maxima of the
+    // absolute values' bits: as numbers they are in the same order, and a NaN is above all.
+    const uint32_t part = max(__float_as_uint(rstd) & 0x7f800000u, 0x20000000u) - 0x01800000u;
+    const float coarse = __uint_as_float(part), fine = rstd * __uint_as_float(0x7f000000u - part);
     float low[K * V];
     uint32_t most[K], all = 0;
 #pragma unroll
@@ -229,6 +233,7 @@ __global__ __launch_bounds__(threads_of<L>) void rmsnorm_fwd(const T* __restrict
       most[k] = 0;
       for (int i = 0; i < V; ++i) {
         const int j = k * V + i;
+        v[j] *= coarse;
         const float t = v[j] * wv[j];
         low[j] = fmaf(v[j], wv[j], -t);
         v[j] = s.holds(k, i) ? t : 0.f;
@@ -250,7 +255,7 @@ __global__ __launch_bounds__(threads_of<L>) void rmsnorm_fwd(const T* __restrict
 #pragma unroll
     for (int k = 0; k < K; ++k) {
       const float top = __uint_as_float(group == D ? all : lanes_max(most[k], share));
-      float scaled = top * rstd;  // the largest of the norm's output
+      float scaled = top * fine;  // the largest of the norm's output
       float scale;
       const bool odd = !(scaled >= kLeastMax && scaled < __builtin_inff());
       const float r = rcp_hw(top), inv = kE4m3Most * r, inv_low = fmaf(-inv, top, kE4m3Most) * r;
@@ -271,10 +276,10 @@ __global__ __launch_bounds__(threads_of<L>) void rmsnorm_fwd(const T* __restrict
         scale = fmaf(fmaf(-scale, kE4m3Most, scaled), 1.f / kE4m3Most, scale);
       } else {  // zeros, next to nothing, infinities, NaN
         scaled = scaled < kLeastMax ? kLeastMax : scaled;
-        const float plain = kE4m3Most / scaled;  // (up to 448 * 2^100; times rstd it could pass fp32)
+        const float plain = kE4m3Most / scaled;
         for (int i = 0; i < V; ++i) {
           const int j = k * V + i;
-          v[j] = odd ? v[j] * rstd * plain : fmaf(v[j], inv, fmaf(v[j], inv_low, low[j] * inv));
+          v[j] = odd ? v[j] * fine * plain : fmaf(v[j], inv, fmaf(v[j], inv_low, low[j] * inv));
         }
         scale = scaled / kE4m3Most;
       }

@@ -6,7 +6,7 @@ torch = pytest.importorskip("torch")
 pytestmark = pytest.mark.gpu
 
 import lm_reference as R  # noqa: E402
-from lm_helpers import within  # noqa: E402
+from lm_helpers import EPS, within  # noqa: E402
 from seq_helpers import Inputs  # noqa: E402
 from seq_reference import held  # noqa: E402
 
@@ -92,3 +92,13 @@ def test_a_gradient_of_nothing_stays_nothing():
     d_sum = i.normal(4, 96)
     d_s, _, d_w = T.ttt_backward_rmsnorm(x, i.param(96), torch.zeros_like(x), 0.0, d_sum=d_sum)
     assert torch.equal(d_s, d_sum) and not d_w.any()
+
+
+@pytest.mark.parametrize("group", [0, 64])
+def test_weights_and_rows_at_the_ends_of_fp32_in_8_bits(group):
+    """The product of a row and its weights is past fp32 or next to nothing before the norm, and ordinary behind it."""
+    i = Inputs(9, "fp32")
+    x, w = i.normal(6, 512), i.param(512, mean=1.0, scale=0.2)
+    for row, weight, eps in ((1e3, 1e36, EPS), (1e-42, 1.0, 2.0 ** -100), (1e18, 1e30, EPS), (1e-20, 1e-25, 2.0 ** -149), (1e-3, 1e-28, EPS)):
+        a, b = (x.double() * row).float(), (w.double() * weight).float()
+        _within(T.ttt_forward_rmsnorm_e4m3(a, b, eps, group=group), R.rmsnorm_e4m3(a, b, eps, DEPTH, group or 512), group, 512)
