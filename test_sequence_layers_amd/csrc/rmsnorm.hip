@@ -255,34 +255,29 @@ __global__ __launch_bounds__(threads_of<L>) void rmsnorm_fwd(const T* __restrict
 #pragma unroll
     for (int k = 0; k < K; ++k) {
       const float top = __uint_as_float(group == D ? all : lanes_max(most[k], share));
-      float scaled = top * fine;  // the largest of the norm's output
-      float scale;
-      const bool odd = !(scaled >= kLeastMax && scaled < __builtin_inff());
+      const float scaled = top * fine;  // the largest of the norm's output
+      float scale = scaled * (1.f / kE4m3Most);  // (divided: the remainder is exact)
+      scale = fmaf(fmaf(-scale, kE4m3Most, scaled), 1.f / kE4m3Most, scale);
       const float r = rcp_hw(top), inv = kE4m3Most * r, inv_low = fmaf(-inv, top, kE4m3Most) * r;
-      if (__ballot(odd) == 0) {
-        bool tie = false;
-        float h[V];
-        for (int i = 0; i < V; ++i) {
-          h[i] = fmaf(v[k * V + i], inv, fmaf(v[k * V + i], inv_low, low[k * V + i] * inv));
-          tie = tie || is_tie(h[i]);
-        }
-        if (__ballot(tie) != 0)
-          for (int i = 0; i < V; ++i) {
-            const float rest = fmaf(v[k * V + i], inv, -h[i]) + fmaf(v[k * V + i], inv_low, low[k * V + i] * inv);
-            if (is_tie(h[i])) h[i] = towards(h[i], rest);
-          }
-        for (int i = 0; i < V; ++i) v[k * V + i] = h[i];
-        scale = scaled * (1.f / kE4m3Most);  // (divided: the remainder is exact)
-        scale = fmaf(fmaf(-scale, kE4m3Most, scaled), 1.f / kE4m3Most, scale);
-      } else {  // zeros, next to nothing, infinities, NaN
-        scaled = scaled < kLeastMax ? kLeastMax : scaled;
-        const float plain = kE4m3Most / scaled;
+      // Zeros, next to nothing, infinities, NaN. (Lanes past the row are none of them: what they have is not stored.)
+      const bool odd = s.any(k) && !(scaled >= kLeastMax && scaled < __builtin_inff());
+      bool tie = odd;
+      float h[V];
+      for (int i = 0; i < V; ++i) {
+        h[i] = fmaf(v[k * V + i], inv, fmaf(v[k * V + i], inv_low, low[k * V + i] * inv));
+        tie = tie || is_tie(h[i]);
+      }
+      if (__ballot(tie) != 0) {  // (each lane by itself: a row's bits do not go by its neighbours)
+        const float most = scaled < kLeastMax ? kLeastMax : scaled, plain = kE4m3Most / most;
         for (int i = 0; i < V; ++i) {
           const int j = k * V + i;
-          v[j] = odd ? v[j] * fine * plain : fmaf(v[j], inv, fmaf(v[j], inv_low, low[j] * inv));
+          const float rest = fmaf(v[j], inv, -h[i]) + fmaf(v[j], inv_low, low[j] * inv);
+          if (is_tie(h[i])) h[i] = towards(h[i], rest);
+          if (odd) h[i] = v[j] * fine * plain;
         }
-        scale = scaled / kE4m3Most;
+        if (odd) scale = most / kE4m3Most;
       }
+      for (int i = 0; i < V; ++i) v[k * V + i] = h[i];
       const int at = (k * L + s.lane) * V;
       if (at < D && (group == D ? at == 0 : (s.lane & (share - 1)) == 0)) scales[(row * D + at) / group] = scale;
     }

@@ -10,10 +10,15 @@ from lm_helpers import EPS, within  # noqa: E402
 from seq_helpers import Inputs  # noqa: E402
 from seq_reference import held  # noqa: E402
 
+from oracle import lm_oracle as O  # noqa: E402
 import test_sequence_layers_amd as T  # noqa: E402
 
 DEPTH = 24 + 6 + 16  # additions of a row's sum: in a lane, over lanes, over waves
 LEAST = 2.0 ** -100 / 448
+
+
+def _bits(t):
+    return t.view(torch.uint8) if t.element_size() == 1 else t.view(torch.int16 if t.element_size() == 2 else torch.int32)
 
 
 def _within(got, ref, group, D):
@@ -102,3 +107,49 @@ def test_weights_and_rows_at_the_ends_of_fp32_in_8_bits(group):
     for row, weight, eps in ((1e3, 1e36, EPS), (1e-42, 1.0, 2.0 ** -100), (1e18, 1e30, EPS), (1e-20, 1e-25, 2.0 ** -149), (1e-3, 1e-28, EPS)):
         a, b = (x.double() * row).float(), (w.double() * weight).float()
         _within(T.ttt_forward_rmsnorm_e4m3(a, b, eps, group=group), R.rmsnorm_e4m3(a, b, eps, DEPTH, group or 512), group, 512)
+
+
+# --------------------------------------------------------------------- next to halfway points of e4m3
+def _beside(ties, rows, D, group, seed=0, top=None):
+    """Rows [rows, D] of fp32 whose groups each hold their largest, `top` of the row, and numbers next to (at most 2^-24 of themselves
+    from) halfway points of that group's scale, and their quotients by it in float64 (weights of one leave them so)."""
+    gen = torch.Generator().manual_seed(seed)
+    if top is None:
+        top = (torch.rand(rows, 1, generator=gen) + 1) * 2.0 ** torch.arange(rows)[:, None].remainder(40).sub(20).float()
+    n = rows * D // group
+    v = ties[torch.randint(0, len(ties), (n, group), generator=gen)] * (torch.randint(0, 2, (n, group), generator=gen) * 2 - 1)
+    v[torch.arange(n), torch.randint(0, group, (n,), generator=gen)] = 448.0
+    x = (v.view(rows, D) * top.double() / 448).float()
+    return x, x.double() * 448 / top.double()
+
+
+NORMAL = torch.tensor([(8.5 + m) * 2.0 ** (e - 3) for e in range(-6, 9) for m in range(8)], dtype=torch.float64)
+NORMAL = NORMAL[NORMAL < 448]
+
+
+def _to_e4m3(q):
+    return torch.from_numpy(O.e4m3(q.numpy()))
+
+
+@pytest.mark.parametrize("D,group", [(96, 32), (160, 32), (384, 128), (384, 64), (768, 128), (1312, 32), (2592, 32), (64, 64), (16000, 128)])
+def test_halfway_points_beside_lanes_without_a_value(D, group):
+    """Widths that leave lanes of a row's last access empty: every value is the nearest of its quotient in 64 bits."""
+    x, q = _beside(NORMAL, 64, D, group, D)
+    y, _ = T.ttt_forward_rmsnorm_e4m3(x.cuda(), torch.ones(D, device="cuda"), EPS, group=group)
+    assert torch.equal(y.double().cpu(), _to_e4m3(q))
+
+
+@pytest.mark.parametrize("D,group", [(32, 32), (64, 32), (128, 128), (128, 64), (256, 64), (20, 20)])
+@pytest.mark.parametrize("ties", [NORMAL], ids=["normal"])
+def test_a_row_in_8_bits_is_its_own_whatever_its_neighbours(D, group, ties):
+    """Rows that share a wave with zeros, infinities and NaN: the bits of the rows by themselves, and the nearest."""
+    x, q = _beside(ties, 48, D, group, D)
+    w = torch.ones(D, device="cuda")
+    alone = T.ttt_forward_rmsnorm_e4m3(x.cuda(), w, EPS, group=0 if group == D else group)
+    assert torch.equal(alone[0].double().cpu(), _to_e4m3(q))
+    for bad in (0.0, float("nan"), float("inf"), 1e-44):
+        both = torch.full((96, D), bad)
+        both[1::2] = x
+        got = T.ttt_forward_rmsnorm_e4m3(both.cuda(), w, EPS, group=0 if group == D else group)
+        for a, b in zip(got, alone):
+            assert torch.equal(_bits(a[1::2]), _bits(b)), bad
