@@ -152,10 +152,17 @@ __device__ __forceinline__ uint32_t to_e4m3(const float* v) {
   const int r = __builtin_amdgcn_cvt_pk_fp8_f32(v[0], v[1], 0, false);
   return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(v[2], v[3], r, true);
 }
-// Halfway between two (normal) numbers of e4m3; the neighbour of such a number on the side of `rest`, what it lacks to the value that it was
-// rounded from (less than 2^-40 of it is none: products are known to 2^-46). Rounding to fp32 comes to a halfway point, but not past it, so
-// that the value's own nearest is kept.
-__device__ __forceinline__ bool is_tie(float v) { return (__float_as_uint(v) & 0xfffffu) == 0x80000u; }
+// Halfway between two numbers of e4m3, from 2^-6 on, and of any size: 20 bits of fp32's fraction are past theirs, and below 2^-6, where
+// their steps stay 2^-9, one more for each halving. (The second is for waves that have one of the first or a number below 2^-6: 16384 x 1536 in groups of
+// 128 33.8 us, 33.3 with the first alone.)
+__device__ __forceinline__ bool is_normal_tie(float v) { return (__float_as_uint(v) & 0xfffffu) == 0x80000u; }
+__device__ __forceinline__ bool is_tie(float v) {
+  const uint32_t u = __float_as_uint(v) & 0x7fffffffu;
+  const int past = 20 + max(0, 121 - (int)(u >> 23));  // (of 2^-6 the exponent is 121)
+  return past <= 24 && (((u & 0x7fffffu) | 0x800000u) & ((1u << past) - 1)) == 1u << (past - 1);
+}
+// The neighbour of such a number on the side of `rest`, what it lacks to the value that it was rounded from (less than 2^-40 of it is
+// none: products are known to 2^-46). Rounding to fp32 comes to a halfway point, but not past it, so that the value's own nearest is kept.
 __device__ __forceinline__ float towards(float v, float rest) {
   const int u = __float_as_int(v), up = (__float_as_int(rest) ^ u) >= 0 ? 1 : -1;
   return __int_as_float(fabsf(rest) < 0x1p-40f * fabsf(v) ? u : u + up);
@@ -262,12 +269,14 @@ __global__ __launch_bounds__(threads_of<L>) void rmsnorm_fwd(const T* __restrict
       // Zeros, next to nothing, infinities, NaN. (Lanes past the row are none of them: what they have is not stored.)
       const bool odd = s.any(k) && !(scaled >= kLeastMax && scaled < __builtin_inff());
       bool tie = odd;
+      uint32_t least = ~0u;  // of the numbers other than zero, their bits twice (without the sign) less one
       float h[V];
       for (int i = 0; i < V; ++i) {
         h[i] = fmaf(v[k * V + i], inv, fmaf(v[k * V + i], inv_low, low[k * V + i] * inv));
-        tie = tie || is_tie(h[i]);
+        tie = tie || is_normal_tie(h[i]);
+        least = min(least, (__float_as_uint(h[i]) << 1) - 1);
       }
-      if (__ballot(tie) != 0) {  // (each lane by itself: a row's bits do not go by its neighbours)
+      if (__ballot(tie || least < 0x79000000u - 1) != 0) {  // (2^-6; each lane by itself: a row's bits do not go by its neighbours)
         const float most = scaled < kLeastMax ? kLeastMax : scaled, plain = kE4m3Most / most;
         for (int i = 0; i < V; ++i) {
           const int j = k * V + i;

@@ -125,6 +125,7 @@ def _beside(ties, rows, D, group, seed=0, top=None):
 
 NORMAL = torch.tensor([(8.5 + m) * 2.0 ** (e - 3) for e in range(-6, 9) for m in range(8)], dtype=torch.float64)
 NORMAL = NORMAL[NORMAL < 448]
+SMALL = (torch.arange(8, dtype=torch.float64) + 0.5) * 2.0 ** -9
 
 
 def _to_e4m3(q):
@@ -140,7 +141,7 @@ def test_halfway_points_beside_lanes_without_a_value(D, group):
 
 
 @pytest.mark.parametrize("D,group", [(32, 32), (64, 32), (128, 128), (128, 64), (256, 64), (20, 20)])
-@pytest.mark.parametrize("ties", [NORMAL], ids=["normal"])
+@pytest.mark.parametrize("ties", [NORMAL, SMALL], ids=["normal", "small"])
 def test_a_row_in_8_bits_is_its_own_whatever_its_neighbours(D, group, ties):
     """Rows that share a wave with zeros, infinities and NaN: the bits of the rows by themselves, and the nearest."""
     x, q = _beside(ties, 48, D, group, D)
@@ -153,3 +154,15 @@ def test_a_row_in_8_bits_is_its_own_whatever_its_neighbours(D, group, ties):
         got = T.ttt_forward_rmsnorm_e4m3(both.cuda(), w, EPS, group=0 if group == D else group)
         for a, b in zip(got, alone):
             assert torch.equal(_bits(a[1::2]), _bits(b)), bad
+
+
+@pytest.mark.parametrize("D,group", [(128, 128), (384, 128), (512, 32), (1001, 1001), (8192, 64)])
+def test_halfway_points_below_the_normal_numbers(D, group):
+    """Below 2^-6 of the scale, where e4m3's steps stay 2^-9: the nearest there too, and of exact halves the even one."""
+    x, q = _beside(SMALL, 64, D, group, D)
+    whole = 0 if group == D else group
+    y, _ = T.ttt_forward_rmsnorm_e4m3(x.cuda(), torch.ones(D, device="cuda"), EPS, group=whole)
+    assert torch.equal(y.double().cpu(), _to_e4m3(q))
+    x, q = _beside(torch.cat([SMALL, NORMAL]), 64, D, group, D + 1, torch.full((64, 1), 448.0))
+    y, _ = T.ttt_forward_rmsnorm_e4m3(x.cuda(), torch.ones(D, device="cuda"), EPS, group=whole)
+    assert torch.equal(x.double(), q) and torch.equal(y.double().cpu(), _to_e4m3(q))
