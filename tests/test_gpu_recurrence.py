@@ -87,6 +87,51 @@ def test_backward(case, kept):
     assert (got[4] is None) == (s["h0"] is None)
 
 
+GENTLE = [  # cases with whole waves: one and two channels a lane, whole tiles and padding, several groups of tiles
+    (1, 64, 64, "fp32", True, None, False), (2, 300, 128, "bf16", True, [300, 129], False), (4, 5000, 384, "bf16", True, None, False),
+    (4, 2500, 256, "fp32", True, [2500, 1024, 1025, 63], True), (3, 1999, 1000, "fp32", True, [1999, 777, 1500], False),
+    (2, 2048, 768, "bf16", False, None, True), (6, 700, 771, "bf16", True, None, True), (1, 16500, 64, "fp32", False, None, False),
+]
+
+
+def _lam(which, C):
+    """Decays whose largest exponent, 8 softplus(lam), is up to 1/4 in every channel, on both sides of it, or up to it but for one
+    channel in 64."""
+    i = Inputs(C, "fp32")
+    lam = i.param(C, scale=1.5, mean=-5.5).clamp(max=-3.46)  # (8 softplus(-3.46) is 0.2475)
+    if which == "around":
+        lam = -3.45 + i.param(C, scale=0.02)
+    elif which == "few":
+        lam[C // 2 % 64::64] = 1.0
+    return lam
+
+
+@pytest.mark.parametrize("which", ["gentle", "around", "few"])
+@pytest.mark.parametrize("case", GENTLE, ids=ids)
+def test_slow_decays(case, which):
+    """Waves of slow decays alone, whose tokens are one straight piece of code without exponentials, beside others: forward, and back
+    with kept states and without."""
+    B, N, C, dtype = case[:4]
+    print(f"recurrence {which} {case}", flush=True)
+    mats, s, d_y = _inputs(*case)
+    mats = (*mats[:3], _lam(which, C))
+    steep = 8 * torch.log1p(torch.exp(mats[3].double())) > 0.25
+    assert bool(steep.any()) == (which != "gentle") and not bool(steep.all())
+    end, kept = torch.full((B, C), 7.0, device="cuda"), torch.full((B, (N + 63) // 64, C), 7.0, device="cuda")
+    y = T.ttt_forward_gated_recurrence(*mats, h_out=end, states=kept, **s)
+    ref = R.recurrence(*mats, **s)
+    held("y", y, ref["y"])
+    held("h_out", end, ref["h_out"])
+    held("states", kept, tuple(v[:, ::64] for v in ref["before"]))
+    ref = R.recurrence(*mats, d_y, depth=_depth(B, N), **s)
+    got = T.ttt_backward_gated_recurrence(*mats, d_y, states=kept, **s)
+    for name, g in zip(("d_x", "d_r", "d_i", "d_lam", "d_h0"), got):
+        if g is not None:
+            held(name, g, ref[name])
+    for a, b in zip(got, T.ttt_backward_gated_recurrence(*mats, d_y, **s)):
+        assert a is b is None or torch.equal(a, b)
+
+
 @pytest.mark.parametrize("B,C,dtype,cut", [(1, 1, "fp32", False), (64, 1536, "bf16", True), (3, 77, "bf16", True), (5, 130, "fp32", False),
                                            (200, 33, "fp32", True)])
 def test_step(B, C, dtype, cut):

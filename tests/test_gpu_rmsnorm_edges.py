@@ -6,8 +6,8 @@ torch = pytest.importorskip("torch")
 pytestmark = pytest.mark.gpu
 
 import lm_reference as R  # noqa: E402
-from lm_helpers import EPS, within  # noqa: E402
-from seq_helpers import Inputs  # noqa: E402
+from lm_helpers import EPS, rng_of, within  # noqa: E402
+from seq_helpers import Inputs, sliced  # noqa: E402
 from seq_reference import held  # noqa: E402
 
 from oracle import lm_oracle as O  # noqa: E402
@@ -166,3 +166,18 @@ def test_halfway_points_below_the_normal_numbers(D, group):
     x, q = _beside(torch.cat([SMALL, NORMAL]), 64, D, group, D + 1, torch.full((64, 1), 448.0))
     y, _ = T.ttt_forward_rmsnorm_e4m3(x.cuda(), torch.ones(D, device="cuda"), EPS, group=whole)
     assert torch.equal(x.double(), q) and torch.equal(y.double().cpu(), _to_e4m3(q))
+
+
+# ------------------------------------------------------------------------------------- alignment
+@pytest.mark.parametrize("D,dtype", [(512, "bf16"), (1001, "bf16"), (768, "fp32"), (65, "fp32"), (4096, "bf16")])
+def test_rows_at_any_alignment_give_the_same_bits(D, dtype):
+    i = Inputs(13, dtype)
+    x, w, res, d_y, d_sum = i.normal(50, D), i.param(D), i.normal(50, D), i.normal(50, D), i.normal(50, D)
+    rng = rng_of(1 << 63, 9)
+    want = (*T.ttt_forward_rmsnorm(x, w, EPS, residual=res, p=0.25, rng=rng), *T.ttt_forward_rmsnorm_e4m3(x, w, EPS),
+            *T.ttt_backward_rmsnorm(x, w, d_y, EPS, d_sum=d_sum, p=0.25, rng=rng))
+    for extra in (1, 2, 3, 4, 8):
+        a = sliced(x, 1, extra)
+        got = (*T.ttt_forward_rmsnorm(a, w, EPS, residual=res, p=0.25, rng=rng), *T.ttt_forward_rmsnorm_e4m3(a, w, EPS),
+               *T.ttt_backward_rmsnorm(a, w, d_y, EPS, d_sum=d_sum, p=0.25, rng=rng))
+        assert len(got) == len(want) and all(torch.equal(_bits(a), _bits(b)) for a, b in zip(got, want)), extra
