@@ -43,8 +43,10 @@ ttt_status ttt_forward_rmsnorm(ttt_dtype dt, int M, int H, int D, float eps, con
 /*
  * The same with an output in 8 bits: y: [M, H, D] of e4m3 (4 bits of exponent, 3 of fraction, largest 448, no
  * infinities), scales: fp32 [M, H, D / group]; y * scale is the norm's output,
- *   scale = max |.| of `group` channels / 448 (of 2^-100 where that is larger), y = the nearest to . / scale, ties to even.
- * group: D (one scale for a row), or 32, 64 or 128 where that divides D. A group with a NaN is NaN, one with an infinity NaN there and zeros elsewhere.
+ *   scale = max |.| of `group` channels / 448 (of 2^-100 where that is larger), y = the nearest to . / scale, ties to even. (The
+ * quotient is known to the rounding of s and of the largest to fp32, 2^-24 of it, whatever rows are beside this one.)
+ * group: D (one scale for a row), or 32, 64 or 128 where that divides D. A group whose output has a NaN is NaN, scale and all; one whose output
+ * has an infinity is NaN there and zeros elsewhere. (Of a row with an infinity in s the norm's output is NaN there and zero elsewhere.)
  */
 ttt_status ttt_forward_rmsnorm_e4m3(ttt_dtype dt, int M, int H, int D, int group, float eps, const void* x,
                                     long long x_stride, const void* residual, const float* weight, void* sum, void* y,
@@ -85,7 +87,8 @@ long long ttt_dropout_counters(int M, int C);
  * 128, ... (of padding: the sequence's last), which the backward pass can take. scale finite and positive. B at most 65535, N at
  * most 2^22, C at most 2^20, B * (N + 128) * (C + 64) at most 2^38. A NaN, or an infinite x or h0, stays in its channel of its sequence:
  * what is before it is as without it, what is behind it infinite or NaN. Of a state the decays of many tokens may leave nothing (their product is
- * fp32's): what is below 2^-126 of it is lost.
+ * fp32's): what is below 2^-126 of it is lost. Workgroups of a call wait for each other's results; such a wait ends after some seconds
+ * whatever happens (a device held up for as long), with TTT_OK, and leaves NaN from its tokens on (backward: up to them).
  */
 ttt_status ttt_forward_gated_recurrence(ttt_dtype dt, int B, int N, int C, float scale, const void* x,
                                         long long x_stride, const void* r, long long r_stride, const void* i,

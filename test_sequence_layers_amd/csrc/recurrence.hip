@@ -10,14 +10,16 @@
 // (A2 A1, A2 e1 + e2). So a sequence is cut into tiles of W waves x TW tokens x 64 V channels that run at once, and every input is read
 // and every output written once: a tile loads its tokens and forms their a and m sigmoid(i) x in registers, joins its waves' pairs in LDS,
 // tells the other tiles its own, folds those of the tiles before it onto the last state that is known, and walks its tokens again from
-// registers. The way back does the same from the sequences' ends on for q, with the states that the forward pass kept at every 64th
-// token for h. Sums over tokens (lam's) are written for each tile and added in a fixed order; folds are in the tokens' order whatever
+// registers (a single-pass scan with decoupled look-back, as Merrill and Garland published it in 2016; it is a method here, the code is
+// written for this recurrence). The way back does the same from the sequences' ends on for q, with the states that the forward pass kept at every
+// 64th token for h. Sums over tokens (lam's) are written for each tile and added in a fixed order; folds are in the tokens' order whatever
 // comes first, so that the same call gives the same bits.
 //
 // Bound by HBM, then by the vector ALU: 32 instructions an element forward, 72 backward, five of which (two
-// exponentials, two reciprocals, a root) take four times as long. 4 x 8192 x 768 in bf16: forward 52 us (201 MB, 3.9 TB/s; the
-// bytes alone 39), 4647 with a thread a channel and no tiles; backward 100 us (352 MB, 3.5 TB/s; the bytes 68, the ALU busy for 49).
-// Forward the tiles' loads, products and stores take 44.5 of it, their telling and asking 5, clearing the board 3.
+// exponentials, two reciprocals, a root) take four times as long. 4 x 8192 x 768 in bf16, slow decays (of 0.78 a token and slower, Gates): forward
+// 52 us (201 MB, 3.9 TB/s; the bytes alone 39), 4647 with a thread a channel and no tiles; backward 100 us (352 MB, 3.5 TB/s; the bytes 68,
+// the ALU busy for 49). With a fast decay in every wave, or fast ones alone, 56 and 102. Forward the tiles' loads, products and stores take 44.5
+// of it, their telling and asking 5, clearing the board 3.
 #include <type_traits>
 
 #include "internal.hpp"
@@ -43,7 +45,7 @@ __device__ __forceinline__ float one_minus(float u, float e) { return u > -0.5f 
 __device__ __forceinline__ float root(float v) { return __builtin_amdgcn_sqrtf(v); }
 
 // log(1 + exp(v)): exp(-|v|) from its base-2 exponent in two parts (as one it would lose 2 |v| 2^-24 of itself), log1p(e) = s P(s^2)
-// with s = e / (2 + e), P within 4e-9 over e in (0, 1].
+// with s = e / (2 + e), P within 1.6e-8, which is 8e-9 of it, over e in (0, 1].
 __device__ __forceinline__ float softplus(float v) {
   const float w = fmaxf(-fabsf(v), -200.f), hi = w * kLog2e;
   const float lo = fmaf(w, kLog2e, -hi) + w * 1.925962991e-8f;  // (log2(e) less kLog2e)
@@ -58,7 +60,7 @@ __device__ __forceinline__ float softplus(float v) {
 }
 
 // k = scale softplus(lam) is the decay's largest exponent. Where it is at most kSmall for a whole wave, as ordinary decays are (0.78 a
-// token and slower), E = a - 1 is la times a polynomial (within 3e-9), a = 1 + E and 1 - a^2 = -E (2 + E), without an
+// token and slower), E = a - 1 is la times a polynomial (within 5e-9), a = 1 + E and 1 - a^2 = -E (2 + E), without an
 // exponential or a choice; `wide` says that it is not.
 constexpr float kSmall = 0.25f;
 
@@ -136,7 +138,7 @@ struct Pair {
 // A tile of a column (64 V channels of a sequence) tells the later ones its (decay, end) pairs, and every kGroup-th its
 // end state: 64-bit words that are all ones until they are there, written and read whole by device-scope atomics, so that a word
 // says by itself that it has come. A NaN is told as the one NaN that is not all ones. (Groups of 8 and of 32 tiles are
-// no faster.) A wait that exceeds kMostPolls, some seconds, gives NaN rather than none: there is none without end.
+// no faster.) A wait that exceeds kMostPolls, some seconds, gives NaN (a word that has not come reads as one): there is none without end.
 constexpr int kGroup = 16;
 constexpr unsigned long long kNotYet = ~0ull;
 constexpr int kMostPolls = 1 << 22;

@@ -109,6 +109,23 @@ def test_weights_and_rows_at_the_ends_of_fp32_in_8_bits(group):
         _within(T.ttt_forward_rmsnorm_e4m3(a, b, eps, group=group), R.rmsnorm_e4m3(a, b, eps, DEPTH, group or 512), group, 512)
 
 
+def test_infinities_and_nan_in_groups():
+    """A group whose output has a NaN is NaN, one whose output has an infinity is NaN there and zeros elsewhere; an infinite entry of a row is a
+    NaN of the output and leaves the row's other groups zeros, a NaN leaves nothing."""
+    i = Inputs(10, "fp32")
+    x, w = i.normal(5, 256), i.param(256, mean=1.0, scale=0.2)
+    w[200] = float("inf")
+    x[1, 70], x[2, 5] = -float("inf"), float("nan")
+    want = R.rmsnorm_e4m3(x, w.clamp(max=9), EPS, DEPTH, 64)
+    y, scales = T.ttt_forward_rmsnorm_e4m3(x, w, EPS, group=64)
+    y = y.double().view(5, 4, 64)
+    for m in (0, 3, 4):
+        assert torch.isnan(y[m, 3, 8]) and not y[m, 3, :8].any() and not y[m, 3, 9:].any() and scales[m, 3] == float("inf")
+        within("y * scales", (y[m, :3] * scales[m, :3, None].double()).flatten(), tuple(t[m, :192] for t in want["deq"]))
+    assert torch.isnan(y[1, 1]).all() and torch.isnan(scales[1, 1]) and not y[1, [0, 2]].any()
+    assert torch.isnan(y[2]).all() and torch.isnan(scales[2]).all()
+
+
 # --------------------------------------------------------------------- next to halfway points of e4m3
 def _beside(ties, rows, D, group, seed=0, top=None):
     """Rows [rows, D] of fp32 whose groups each hold their largest, `top` of the row, and numbers next to (at most 2^-24 of themselves
