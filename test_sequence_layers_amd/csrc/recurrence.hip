@@ -18,8 +18,8 @@
 // Bound by HBM, then by the vector ALU: 32 instructions an element forward, 72 backward, five of which (two
 // exponentials, two reciprocals, a root) take four times as long. 4 x 8192 x 768 in bf16, slow decays (of 0.78 a token and slower, Gates): forward
 // 52 us (201 MB, 3.9 TB/s; the bytes alone 39), 4647 with a thread a channel and no tiles; backward 100 us (352 MB, 3.5 TB/s; the bytes 68,
-// the ALU busy for 49). With a fast decay in every wave, or fast ones alone, 56 and 102. Forward the tiles' loads, products and stores take 44.5
-// of it, their telling and asking 5, clearing the board 3.
+// the ALU busy for 49). With a fast decay in every wave, or fast ones alone, 3 us more each. As many tokens in sequences of one tile, which tell and
+// ask for nothing, take 39 us forward (256 x 128 x 768) and 78 backward (512 x 64 x 768); clearing the board is 3 of the rest.
 #include <type_traits>
 
 #include "internal.hpp"
