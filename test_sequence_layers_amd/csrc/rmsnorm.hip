@@ -84,8 +84,8 @@ __device__ __forceinline__ void load_weights(const float* w, float* out, const S
 }
 
 // rstd of a row, over *back: v is multiplied by *back where its squares overflow (from 2^60 or so on: the largest squares are 2^96
-// then, and eps is nothing beside them) or are next to nothing under an eps that is too (a mean below 2^-90: the smallest numbers become
-// 2^-41, the largest squares 2^126), so that such rows are normed like others. An infinite or NaN entry makes its row NaN at least
+// then, and eps is nothing beside them) or are next to nothing under an eps that is too (their sum and eps below 2^-90: the smallest numbers
+// become 2^-41, the largest squares 2^126), so that such rows are normed like others. An infinite or NaN entry makes its row NaN at least
 // where the entry is.
 template <int L, int K, int V>
 __device__ __forceinline__ float inverse_rms(float* v, int D, float eps, float (*red)[16], float* back) {
